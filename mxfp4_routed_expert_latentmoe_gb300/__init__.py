@@ -19,6 +19,8 @@ _BUILD = os.path.join(_HERE, "_build")
 _SO = os.path.join(_BUILD, "libk3moe.so")
 _CSRC = os.path.join(_HERE, "csrc")
 _HEADER = os.path.join(_ROOT, "include", "k3moe.h")
+_ATTN = os.path.join(_CSRC, "attn")  # the attention operators (attn.py)
+_ATTN_HEADER = os.path.join(_ROOT, "include", "k3attn.h")
 _lock = threading.Lock()
 _lib = None
 
@@ -39,18 +41,20 @@ class K3MoEError(RuntimeError):
 
 
 def _sources():
-    return [os.path.join(_CSRC, f) for f in sorted(os.listdir(_CSRC)) if f.endswith((".cu", ".cuh"))] + [_HEADER]
+    return [os.path.join(d, f) for d in (_CSRC, _ATTN) for f in sorted(os.listdir(d))
+            if f.endswith((".cu", ".cuh"))] + [_HEADER, _ATTN_HEADER]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/ into _build/libk3moe.so for sm_103a (in-tree)."""
+    """Compile csrc/ and csrc/attn/ into _build/libk3moe.so for sm_103a (in-tree)."""
     os.makedirs(_BUILD, exist_ok=True)
     newest = max(os.path.getmtime(f) for f in _sources())
     if not force and os.path.exists(_SO) and os.path.getmtime(_SO) >= newest:
         return _SO
     nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     tmp = _SO + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, os.path.join(_CSRC, "k3moe_api.cu")]
+    cmd = [nvcc, *NVCC_FLAGS, "-t", "2", "-o", tmp, os.path.join(_CSRC, "k3moe_api.cu"),
+           os.path.join(_ATTN, "k3attn_api.cu")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)

@@ -1,0 +1,262 @@
+"""The attention operators that stand before the routed-expert block when it serves tokens:
+norms of queries and keys per head with the position rotation, the paged key-value cache
+(bf16, or E4M3 with a scale per row), and the attention of one new token over its pages.
+
+Thin binding over the C ABI declared in ``include/k3attn.h``, which has the formulas.  Every
+function checks its tensors (ValueError), passes pointers and strides, and launches on the
+current CUDA stream or on ``stream``; device-detected conditions (DEV_BAD_*) are read with
+``device_status(ws)``.
+
+    d = attn.dims(n_heads=64, n_kv_heads=8, head_dim=128, rot_dim=128)
+    cache = attn.KVCache.empty(d, n_pages=4096, page_size=64, fmt="e4m3")
+    ws = attn.workspace(d)
+    attn.kv_append(d, q, k, v, positions, slots, inv_freq, q_w, k_w, cache, q_out, ws)
+    attn.decode(d, q_out, cache, page_table, lens, out, ws)
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _stream, device_status, lib  # noqa: F401  (device_status: the status word of ws)
+
+BF16, E4M3 = 0, 1  # K3ATTN_BF16, K3ATTN_E4M3
+MIN_WORKSPACE = 256  # K3ATTN_MIN_WORKSPACE
+DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_BAD_LENGTH = 0x1, 0x2, 0x4
+_fns = None
+
+
+class Dims(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("rot_interleaved", ctypes.c_int32), ("rms_eps", ctypes.c_float),
+                ("softmax_scale", ctypes.c_float), ("window", ctypes.c_int32)]
+
+
+def dims(n_heads, n_kv_heads, head_dim, rot_dim=None, rot_interleaved=False, rms_eps=1e-6, softmax_scale=None,
+         window=0) -> Dims:
+    """The k3attn_dims struct; rot_dim defaults to head_dim, softmax_scale to 1 / sqrt(head_dim)."""
+    return Dims(n_heads, n_kv_heads, head_dim, head_dim if rot_dim is None else rot_dim, int(rot_interleaved), rms_eps,
+                head_dim ** -0.5 if softmax_scale is None else softmax_scale, window)
+
+
+class CacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64)]
+
+
+def _funcs():
+    """The library's attention functions with their signatures set."""
+    global _fns
+    if _fns is None:
+        L = lib()
+        p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        D, C = ctypes.POINTER(Dims), ctypes.POINTER(CacheC)
+        sigs = {
+            "k3attn_workspace_bytes": ([D], sz),
+            "k3attn_workspace_init": ([p, sz, p], ctypes.c_int),
+            "k3attn_qk_norm_rope": ([D, i32, p, i64, p, i64, p, p, p, p, p, p, p], ctypes.c_int),
+            "k3attn_kv_write": ([D, i32, p, i64, p, i64, p, C, p, sz, p], ctypes.c_int),
+            "k3attn_kv_append": ([D, i32, p, i64, p, i64, p, i64, p, p, p, p, p, C, p, p, p, sz, p], ctypes.c_int),
+            "k3attn_kv_read": ([D, i32, p, C, p, p, p, sz, p], ctypes.c_int),
+            "k3attn_decode": ([D, i32, p, i64, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
+        }
+        for name, (args, res) in sigs.items():
+            f = getattr(L, name)
+            f.argtypes = args
+            f.restype = res
+        _fns = L
+    return _fns
+
+
+def declared_functions() -> list:
+    """Function names declared in include/k3attn.h."""
+    import re
+
+    from . import _ATTN_HEADER
+    return sorted(set(re.findall(r"\b(k3attn_[a-z0-9_]+)\s*\(", open(_ATTN_HEADER).read())))
+
+
+# ------------------------------------------------------------------------------ checks
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name, dtype, shape):
+    _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == shape,
+          f"{name}: a CUDA tensor {list(shape)} of {dtype} is needed, got {list(t.shape)} of {t.dtype} on {t.device}")
+
+
+def _dense(t, name, dtype, shape):
+    _tensor(t, name, dtype, shape)
+    _need(t.is_contiguous(), f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, T, heads, D):
+    """Pointer and token stride of a [T, heads, D] bf16 tensor whose tokens' rows are dense."""
+    import torch
+    _tensor(t, name, torch.bfloat16, (T, heads, D))
+    sT, sH, sD = t.stride()
+    _need((sD == 1 or D == 1) and (sH == D or heads == 1), f"{name}: the heads of a token must be dense")
+    return t.data_ptr(), sT if T > 1 else max(sT, heads * D)
+
+
+def _ws(ws):
+    import torch
+    _need(ws.is_cuda and ws.is_contiguous() and ws.dtype == torch.uint8, "ws: a uint8 CUDA tensor is needed")
+    return ws.data_ptr(), ws.numel()
+
+
+# ------------------------------------------------------------------------------ what a program keeps
+def workspace_bytes(d: Dims) -> int:
+    return int(_funcs().k3attn_workspace_bytes(ctypes.byref(d)))
+
+
+def workspace(d: Dims, device="cuda"):
+    """A workspace for calls with these dims (or smaller ones), readied for its first use."""
+    import torch
+    n = workspace_bytes(d)
+    _need(n > 0, "unsupported dims")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    workspace_init(ws)
+    return ws
+
+
+def workspace_init(ws, stream=None):
+    """k3attn_workspace_init: readies a workspace (also clears its status word)."""
+    p, n = _ws(ws)
+    _check(_funcs().k3attn_workspace_init(p, n, _stream(stream)), "k3attn_workspace_init")
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
+    """inv_freq [rot_dim / 2] f64: theta^(-2i / rot_dim)."""
+    import torch
+    return theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+
+
+class KVCache:
+    """A paged cache over the caller's tensors: k, v [n_pages, Hkv, page_size, D], bf16 or
+    float8_e4m3fn, with the same strides (any order of pages, heads and tokens; a row's D
+    values dense); for E4M3 k_scale, v_scale [n_pages, Hkv, page_size] f32."""
+
+    def __init__(self, d: Dims, k, v, k_scale=None, v_scale=None):
+        import torch
+        _need(k.dim() == 4 and k.dtype in (torch.bfloat16, torch.float8_e4m3fn),
+              "k: [n_pages, Hkv, page_size, D] of bfloat16 or float8_e4m3fn is needed")
+        n, page = k.shape[0], k.shape[2]
+        for t, name in ((k, "k"), (v, "v")):
+            _tensor(t, name, k.dtype, (n, d.n_kv_heads, page, d.head_dim))
+            _need(t.stride(3) == 1, f"{name}: a row's values must be dense")
+        _need(k.stride() == v.stride(), "k and v must have the same strides")
+        fmt = E4M3 if k.dtype == torch.float8_e4m3fn else BF16
+        ss = (0, 0, 0)
+        if fmt == E4M3:
+            _need(k_scale is not None and v_scale is not None, "an E4M3 cache needs k_scale and v_scale")
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _tensor(t, name, torch.float32, (n, d.n_kv_heads, page))
+            _need(k_scale.stride() == v_scale.stride(), "k_scale and v_scale must have the same strides")
+            ss = k_scale.stride()
+        else:
+            _need(k_scale is None and v_scale is None, "a bf16 cache has no scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.head_shape = n, page, (d.n_kv_heads, d.head_dim)
+        self.c = CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt == E4M3 else None,
+                        v_scale.data_ptr() if fmt == E4M3 else None, fmt, n, page, 0, *k.stride()[:3], *ss)
+
+    @classmethod
+    def empty(cls, d: Dims, n_pages: int, page_size: int, fmt: str = "bf16", device="cuda"):
+        """A dense cache of zeros; fmt "bf16" or "e4m3"."""
+        import torch
+        _need(fmt in ("bf16", "e4m3"), "fmt is bf16 or e4m3")
+        shape = (n_pages, d.n_kv_heads, page_size, d.head_dim)
+        if fmt == "bf16":
+            return cls(d, *(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        return cls(d, *codes, *(torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _cache(d: Dims, cache: KVCache):
+    _need(cache.head_shape == (d.n_kv_heads, d.head_dim), "the cache has another head shape")
+    return ctypes.byref(cache.c)
+
+
+# ------------------------------------------------------------------------------ the operators
+def _norm_args(d, T, positions, inv_freq, q_w, k_w):
+    import torch
+    D = d.head_dim
+    return (_dense(positions, "positions", torch.int32, (T,)),
+            _dense(inv_freq, "inv_freq", torch.float64, (d.rot_dim // 2,)) if d.rot_dim else None,
+            _dense(q_w, "q_w", torch.float32, (D,)), _dense(k_w, "k_w", torch.float32, (D,)))
+
+
+def qk_norm_rope(d: Dims, q, k, positions, inv_freq, q_w, k_w, q_out, k_out, stream=None):
+    """k3attn_qk_norm_rope: q [T, Hq, D], k [T, Hkv, D] bf16 (slices of one projection's output
+    will do) -> q_out, k_out, dense, normed per head and rotated.  inv_freq may be None when
+    d.rot_dim is 0."""
+    import torch
+    T, D = q.shape[0], d.head_dim
+    qp, qs = _rows(q, "q", T, d.n_heads, D)
+    kp, ks = _rows(k, "k", T, d.n_kv_heads, D)
+    pos, freq, qw, kw = _norm_args(d, T, positions, inv_freq, q_w, k_w)
+    _check(_funcs().k3attn_qk_norm_rope(ctypes.byref(d), T, qp, qs, kp, ks, pos, freq, qw, kw,
+                                        _dense(q_out, "q_out", torch.bfloat16, (T, d.n_heads, D)),
+                                        _dense(k_out, "k_out", torch.bfloat16, (T, d.n_kv_heads, D)),
+                                        _stream(stream)), "k3attn_qk_norm_rope")
+
+
+def kv_write(d: Dims, k, v, slots, cache: KVCache, ws, stream=None):
+    """k3attn_kv_write: k, v [T, Hkv, D] bf16 into the cache at slots [T] int32 (-1: not written)."""
+    import torch
+    T, D = k.shape[0], d.head_dim
+    kp, ks = _rows(k, "k", T, d.n_kv_heads, D)
+    vp, vs = _rows(v, "v", T, d.n_kv_heads, D)
+    _check(_funcs().k3attn_kv_write(ctypes.byref(d), T, kp, ks, vp, vs, _dense(slots, "slots", torch.int32, (T,)),
+                                    _cache(d, cache), *_ws(ws), _stream(stream)), "k3attn_kv_write")
+
+
+def kv_append(d: Dims, q, k, v, positions, slots, inv_freq, q_w, k_w, cache: KVCache, q_out, ws, k_out=None,
+              stream=None):
+    """k3attn_kv_append: qk_norm_rope of q into q_out and of k, and the write of k and v into the
+    cache, in one pass; k_out (optional) also receives the keys."""
+    import torch
+    T, D = q.shape[0], d.head_dim
+    qp, qs = _rows(q, "q", T, d.n_heads, D)
+    kp, ks = _rows(k, "k", T, d.n_kv_heads, D)
+    vp, vs = _rows(v, "v", T, d.n_kv_heads, D)
+    pos, freq, qw, kw = _norm_args(d, T, positions, inv_freq, q_w, k_w)
+    _check(_funcs().k3attn_kv_append(ctypes.byref(d), T, qp, qs, kp, ks, vp, vs, pos,
+                                     _dense(slots, "slots", torch.int32, (T,)), freq, qw, kw, _cache(d, cache),
+                                     _dense(q_out, "q_out", torch.bfloat16, (T, d.n_heads, D)),
+                                     None if k_out is None else
+                                     _dense(k_out, "k_out", torch.bfloat16, (T, d.n_kv_heads, D)),
+                                     *_ws(ws), _stream(stream)), "k3attn_kv_append")
+
+
+def kv_read(d: Dims, slots, cache: KVCache, k_out, v_out, ws, stream=None):
+    """k3attn_kv_read: the rows at slots [T] int32 as bf16, k_out and v_out [T, Hkv, D]."""
+    import torch
+    T = slots.shape[0]
+    shape = (T, d.n_kv_heads, d.head_dim)
+    _check(_funcs().k3attn_kv_read(ctypes.byref(d), T, _dense(slots, "slots", torch.int32, (T,)), _cache(d, cache),
+                                   _dense(k_out, "k_out", torch.bfloat16, shape),
+                                   _dense(v_out, "v_out", torch.bfloat16, shape), *_ws(ws), _stream(stream)),
+           "k3attn_kv_read")
+
+
+def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None):
+    """k3attn_decode: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
+    of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32."""
+    import torch
+    B, D = q.shape[0], d.head_dim
+    qp, qs = _rows(q, "q", B, d.n_heads, D)
+    width = page_table.shape[1] if page_table.dim() == 2 else -1
+    _check(_funcs().k3attn_decode(ctypes.byref(d), B, qp, qs, _cache(d, cache),
+                                  _dense(page_table, "page_table", torch.int32, (B, width)), width,
+                                  _dense(lens, "lens", torch.int32, (B,)),
+                                  _dense(out, "out", torch.bfloat16, (B, d.n_heads, D)),
+                                  None if lse is None else _dense(lse, "lse", torch.float32, (B, d.n_heads)),
+                                  *_ws(ws), _stream(stream)), "k3attn_decode")

@@ -1,0 +1,302 @@
+// k3attn_api.cu -- C ABI of the attention operators (see include/k3attn.h): host-side
+// validation and launches.  No allocation, no synchronisation.
+#include <atomic>
+#include <cmath>
+#include <utility>
+
+#include "k3_decode.cuh"
+#include "k3_qkv.cuh"
+
+namespace {
+
+using namespace k3;
+
+constexpr int kMaxDevices = 64;
+
+#define K3A_TRY(x)                                       \
+  do {                                                   \
+    if ((x) != cudaSuccess) {                            \
+      (void)cudaGetLastError();                          \
+      return K3MOE_ERR_CUDA;                             \
+    }                                                    \
+  } while (0)
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+k3moe_status check_dims(const k3attn_dims* d) {
+  if (!d) return K3MOE_ERR_ARG;
+  if (d->n_heads <= 0 || d->n_heads > 1024 || d->n_kv_heads <= 0 || d->n_heads % d->n_kv_heads) return K3MOE_ERR_SHAPE;
+  if (d->head_dim < 16 || d->head_dim > 256 || d->head_dim % 16) return K3MOE_ERR_SHAPE;
+  if (d->rot_dim < 0 || d->rot_dim > d->head_dim || d->rot_dim % 16) return K3MOE_ERR_SHAPE;
+  if (d->rot_interleaved != 0 && d->rot_interleaved != 1) return K3MOE_ERR_ARG;
+  if (!(d->rms_eps >= 0.0f) || d->rms_eps > 1.0f) return K3MOE_ERR_ARG;
+  if (!(d->softmax_scale > 0.0f) || std::isinf(d->softmax_scale)) return K3MOE_ERR_ARG;
+  if (d->window < 0) return K3MOE_ERR_ARG;
+  return K3MOE_OK;
+}
+
+k3moe_status check_cache(const k3attn_cache* c, const k3attn_dims& d) {
+  if (!c || !c->k || !c->v) return K3MOE_ERR_ARG;
+  if (c->format != K3ATTN_BF16 && c->format != K3ATTN_E4M3) return K3MOE_ERR_ARG;
+  const bool e4m3 = c->format == K3ATTN_E4M3;
+  if (e4m3 && (!c->k_scale || !c->v_scale)) return K3MOE_ERR_ARG;
+  if (c->n_pages <= 0 || c->page_size <= 0 || c->reserved != 0) return K3MOE_ERR_ARG;
+  if ((int64_t)c->n_pages * c->page_size > INT32_MAX) return K3MOE_ERR_SHAPE;  // slots are int32
+  if (c->page_stride < d.head_dim || c->head_stride < d.head_dim || c->token_stride < d.head_dim)
+    return K3MOE_ERR_SHAPE;
+  const int64_t unit = e4m3 ? 16 : 8;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->head_stride % unit ||
+      c->token_stride % unit)
+    return K3MOE_ERR_ALIGN;
+  if (e4m3) {
+    if (c->scale_page_stride < 1 || c->scale_head_stride < 1 || c->scale_token_stride < 1) return K3MOE_ERR_SHAPE;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return K3MOE_ERR_ALIGN;
+  }
+  return K3MOE_OK;
+}
+
+CacheView view_of(const k3attn_cache& c) {
+  const int64_t b = c.format == K3ATTN_E4M3 ? 1 : 2;
+  CacheView v{};
+  v.k = static_cast<uint8_t*>(c.k);
+  v.v = static_cast<uint8_t*>(c.v);
+  v.ks = c.k_scale;
+  v.vs = c.v_scale;
+  v.page = c.page_stride * b;
+  v.head = c.head_stride * b;
+  v.tok = c.token_stride * b;
+  v.spage = c.scale_page_stride;
+  v.shead = c.scale_head_stride;
+  v.stok = c.scale_token_stride;
+  v.n_pages = c.n_pages;
+  v.page_size = c.page_size;
+  return v;
+}
+
+// rows of `width` bf16 values, `stride` apart
+k3moe_status check_rows(int64_t stride, int64_t width) {
+  if (stride < width) return K3MOE_ERR_SHAPE;
+  return stride % 8 ? K3MOE_ERR_ALIGN : K3MOE_OK;
+}
+
+struct DevInfo {
+  int sms = 0;
+  bool ok = false;
+};
+DevInfo g_dev[kMaxDevices];
+std::atomic<bool> g_dev_init[kMaxDevices];
+
+k3moe_status check_device(int* dev_out, int* sms_out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    (void)cudaGetLastError();
+    return K3MOE_ERR_DEVICE;
+  }
+  if (!g_dev_init[dev].load(std::memory_order_acquire)) {
+    int major = 0, minor = 0, sms = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    g_dev[dev].sms = sms;
+    g_dev[dev].ok = (major == 10 && minor == 3);
+    g_dev_init[dev].store(true, std::memory_order_release);
+  }
+  if (!g_dev[dev].ok) return K3MOE_ERR_DEVICE;
+  *dev_out = dev;
+  *sms_out = g_dev[dev].sms;
+  return K3MOE_OK;
+}
+
+// Launch with programmatic stream serialization: the kernel may start while its predecessor
+// finishes; it waits (griddepcontrol.wait) before it touches memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, int smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+QkvParams qkv_params(const k3attn_dims& d, int32_t T) {
+  QkvParams p{};
+  p.T = T;
+  p.Hq = d.n_heads;
+  p.Hkv = d.n_kv_heads;
+  p.D = d.head_dim;
+  p.R = d.rot_dim;
+  p.inter = d.rot_interleaved;
+  p.eps = d.rms_eps;
+  return p;
+}
+
+template <bool NORM, int FMT>
+cudaError_t launch_qkv(const QkvParams& p, cudaStream_t s) {
+  return launch(k3_qkv_kernel<NORM, FMT>, dim3(p.T), dim3(QKV_WARPS * 32), 0, s, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t k3attn_workspace_bytes(const k3attn_dims* dims) {
+  if (check_dims(dims) != K3MOE_OK) return 0;
+  return K3ATTN_MIN_WORKSPACE;
+}
+
+k3moe_status k3attn_workspace_init(void* ws, size_t ws_bytes, void* stream) {
+  if (!ws) return K3MOE_ERR_ARG;
+  if (!aligned(ws, 16)) return K3MOE_ERR_ALIGN;
+  if (ws_bytes < K3ATTN_MIN_WORKSPACE) return K3MOE_ERR_WORKSPACE;
+  int dev, sms;
+  const k3moe_status st = check_device(&dev, &sms);
+  if (st != K3MOE_OK) return st;
+  K3A_TRY(cudaMemsetAsync(ws, 0, K3ATTN_MIN_WORKSPACE, static_cast<cudaStream_t>(stream)));
+  return K3MOE_OK;
+}
+
+k3moe_status k3attn_qk_norm_rope(const k3attn_dims* dims, int32_t T, const uint16_t* q, int64_t q_stride,
+                                 const uint16_t* k, int64_t k_stride, const int32_t* positions,
+                                 const double* inv_freq, const float* q_w, const float* k_w, uint16_t* q_out,
+                                 uint16_t* k_out, void* stream) {
+  k3moe_status st = check_dims(dims);
+  if (st != K3MOE_OK) return st;
+  const k3attn_dims& d = *dims;
+  if (T < 0) return K3MOE_ERR_ARG;
+  if (T == 0) return K3MOE_OK;
+  if (!q || !k || !positions || (d.rot_dim > 0 && !inv_freq) || !q_w || !k_w || !q_out || !k_out) return K3MOE_ERR_ARG;
+  if ((st = check_rows(q_stride, (int64_t)d.n_heads * d.head_dim)) != K3MOE_OK) return st;
+  if ((st = check_rows(k_stride, (int64_t)d.n_kv_heads * d.head_dim)) != K3MOE_OK) return st;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(positions, 4) || !aligned(inv_freq, 8) || !aligned(q_w, 16) ||
+      !aligned(k_w, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
+    return K3MOE_ERR_ALIGN;
+  int dev, sms;
+  if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
+  QkvParams p = qkv_params(d, T);
+  p.q = q; p.q_stride = q_stride; p.k = k; p.k_stride = k_stride;
+  p.pos = positions; p.inv_freq = inv_freq; p.q_w = q_w; p.k_w = k_w; p.q_out = q_out; p.k_out = k_out;
+  K3A_TRY((launch_qkv<true, CF_NONE>(p, static_cast<cudaStream_t>(stream))));
+  return K3MOE_OK;
+}
+
+k3moe_status k3attn_kv_write(const k3attn_dims* dims, int32_t T, const uint16_t* k, int64_t k_stride,
+                             const uint16_t* v, int64_t v_stride, const int32_t* slots, const k3attn_cache* cache,
+                             void* ws, size_t ws_bytes, void* stream) {
+  k3moe_status st = check_dims(dims);
+  if (st != K3MOE_OK) return st;
+  const k3attn_dims& d = *dims;
+  if ((st = check_cache(cache, d)) != K3MOE_OK) return st;
+  if (T < 0) return K3MOE_ERR_ARG;
+  if (T == 0) return K3MOE_OK;
+  if (!k || !v || !slots || !ws) return K3MOE_ERR_ARG;
+  if ((st = check_rows(k_stride, (int64_t)d.n_kv_heads * d.head_dim)) != K3MOE_OK) return st;
+  if ((st = check_rows(v_stride, (int64_t)d.n_kv_heads * d.head_dim)) != K3MOE_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(ws, 16)) return K3MOE_ERR_ALIGN;
+  if (ws_bytes < K3ATTN_MIN_WORKSPACE) return K3MOE_ERR_WORKSPACE;
+  int dev, sms;
+  if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
+  QkvParams p = qkv_params(d, T);
+  p.k = k; p.k_stride = k_stride; p.v = v; p.v_stride = v_stride; p.slots = slots;
+  p.c = view_of(*cache);
+  p.status = static_cast<uint32_t*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_qkv<false, CF_E4M3>(p, s) : launch_qkv<false, CF_BF16>(p, s)));
+  return K3MOE_OK;
+}
+
+k3moe_status k3attn_kv_append(const k3attn_dims* dims, int32_t T, const uint16_t* q, int64_t q_stride,
+                              const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                              const int32_t* positions, const int32_t* slots, const double* inv_freq,
+                              const float* q_w, const float* k_w, const k3attn_cache* cache, uint16_t* q_out,
+                              uint16_t* k_out, void* ws, size_t ws_bytes, void* stream) {
+  k3moe_status st = check_dims(dims);
+  if (st != K3MOE_OK) return st;
+  const k3attn_dims& d = *dims;
+  if ((st = check_cache(cache, d)) != K3MOE_OK) return st;
+  if (T < 0) return K3MOE_ERR_ARG;
+  if (T == 0) return K3MOE_OK;
+  if (!q || !k || !v || !positions || !slots || (d.rot_dim > 0 && !inv_freq) || !q_w || !k_w || !q_out || !ws)
+    return K3MOE_ERR_ARG;
+  if ((st = check_rows(q_stride, (int64_t)d.n_heads * d.head_dim)) != K3MOE_OK) return st;
+  if ((st = check_rows(k_stride, (int64_t)d.n_kv_heads * d.head_dim)) != K3MOE_OK) return st;
+  if ((st = check_rows(v_stride, (int64_t)d.n_kv_heads * d.head_dim)) != K3MOE_OK) return st;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(positions, 4) || !aligned(slots, 4) ||
+      !aligned(inv_freq, 8) || !aligned(q_w, 16) || !aligned(k_w, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(ws, 16))
+    return K3MOE_ERR_ALIGN;
+  if (ws_bytes < K3ATTN_MIN_WORKSPACE) return K3MOE_ERR_WORKSPACE;
+  int dev, sms;
+  if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
+  QkvParams p = qkv_params(d, T);
+  p.q = q; p.q_stride = q_stride; p.k = k; p.k_stride = k_stride; p.v = v; p.v_stride = v_stride;
+  p.pos = positions; p.slots = slots; p.inv_freq = inv_freq; p.q_w = q_w; p.k_w = k_w;
+  p.q_out = q_out; p.k_out = k_out;
+  p.c = view_of(*cache);
+  p.status = static_cast<uint32_t*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_qkv<true, CF_E4M3>(p, s) : launch_qkv<true, CF_BF16>(p, s)));
+  return K3MOE_OK;
+}
+
+k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* slots, const k3attn_cache* cache,
+                            uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes, void* stream) {
+  k3moe_status st = check_dims(dims);
+  if (st != K3MOE_OK) return st;
+  const k3attn_dims& d = *dims;
+  if ((st = check_cache(cache, d)) != K3MOE_OK) return st;
+  if (T < 0) return K3MOE_ERR_ARG;
+  if (T == 0) return K3MOE_OK;
+  if (!slots || !k_out || !v_out || !ws) return K3MOE_ERR_ARG;
+  if (!aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(ws, 16)) return K3MOE_ERR_ALIGN;
+  if (ws_bytes < K3ATTN_MIN_WORKSPACE) return K3MOE_ERR_WORKSPACE;
+  int dev, sms;
+  if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
+  QkvParams p = qkv_params(d, T);
+  p.slots = slots; p.k_out = k_out; p.v_out = v_out;
+  p.c = view_of(*cache);
+  p.status = static_cast<uint32_t*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  K3A_TRY(launch(cache->format == K3ATTN_E4M3 ? k3_kv_read_kernel<CF_E4M3> : k3_kv_read_kernel<CF_BF16>, dim3(T),
+                 dim3(QKV_WARPS * 32), 0, s, p));
+  return K3MOE_OK;
+}
+
+k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q, int64_t q_stride,
+                           const k3attn_cache* cache, const int32_t* page_table, int32_t table_width,
+                           const int32_t* lens, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                           void* stream) {
+  k3moe_status st = check_dims(dims);
+  if (st != K3MOE_OK) return st;
+  const k3attn_dims& d = *dims;
+  if ((st = check_cache(cache, d)) != K3MOE_OK) return st;
+  if (B < 0 || table_width < 0) return K3MOE_ERR_ARG;
+  if (B == 0) return K3MOE_OK;
+  if (!q || (table_width > 0 && !page_table) || !lens || !out || !ws) return K3MOE_ERR_ARG;
+  if (B > 65535 || (int64_t)table_width * cache->page_size > INT32_MAX) return K3MOE_ERR_SHAPE;
+  if ((st = check_rows(q_stride, (int64_t)d.n_heads * d.head_dim)) != K3MOE_OK) return st;
+  if (!aligned(q, 16) || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(ws, 16))
+    return K3MOE_ERR_ALIGN;
+  if (ws_bytes < k3attn_workspace_bytes(dims)) return K3MOE_ERR_WORKSPACE;
+  int dev, sms;
+  if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
+  DecodeParams p{};
+  p.q = q; p.q_stride = q_stride;
+  p.B = B; p.Hq = d.n_heads; p.Hkv = d.n_kv_heads; p.D = d.head_dim; p.window = d.window;
+  p.scale = d.softmax_scale;
+  p.c = view_of(*cache);
+  p.table = page_table; p.table_width = table_width; p.lens = lens;
+  p.out = out; p.lse = lse;
+  p.status = static_cast<uint32_t*>(ws);
+  K3A_TRY(launch(cache->format == K3ATTN_E4M3 ? k3_decode_kernel<CF_E4M3> : k3_decode_kernel<CF_BF16>,
+                 dim3(d.n_heads, B), dim3(DEC_WARPS * 32), 0, static_cast<cudaStream_t>(stream), p));
+  return K3MOE_OK;
+}
+
+}  // extern "C"
