@@ -141,13 +141,55 @@ cudaError_t launch_qkv(const QkvParams& p, cudaStream_t s) {
   return launch(k3_qkv_kernel<NORM, FMT>, dim3(p.T), dim3(QKV_WARPS * 32), 0, s, p);
 }
 
+// per (kernel, device): raise the kernel's dynamic shared memory limit once
+template <auto Kern>
+bool set_smem(int dev, int bytes) {
+  static std::atomic<bool> granted[kMaxDevices];
+  if (granted[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  granted[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+// The decode workspace: the status word, the blocks' counters (cleared once by
+// k3attn_workspace_init), the blocks' records.
+constexpr size_t kCounters = K3ATTN_MIN_WORKSPACE, kRecords = kCounters + DEC_MAX_BLOCKS * 4;
+static_assert(kRecords % 16 == 0, "the records are written 16 bytes at a time");
+
+// padded head dim and head group (8 NT query heads of a key head) of the decode instance
+int dec_dp(const k3attn_dims& d) { return (d.head_dim + 63) / 64 * 64; }
+int dec_nt(const k3attn_dims& d) { return d.n_heads / d.n_kv_heads <= 8 ? 1 : 2; }
+
+template <int FMT, int DP, int NT>
+cudaError_t launch_decode_t(DecodeParams p, int dev, int sms, cudaStream_t s) {
+  using C = DecCfg<FMT, DP, NT>;
+  if (!set_smem<k3_decode_kernel<FMT, DP, NT>>(dev, C::SMEM)) return cudaErrorInvalidValue;
+  p.groups = (p.G + C::HEADS - 1) / C::HEADS;
+  const int grid = sms < DEC_MAX_BLOCKS ? sms : DEC_MAX_BLOCKS;
+  return launch(k3_decode_kernel<FMT, DP, NT>, dim3(grid), dim3(C::WARPS * 32), C::SMEM, s, p);
+}
+template <int FMT>
+cudaError_t launch_decode(const DecodeParams& p, int dp, int nt, int dev, int sms, cudaStream_t s) {
+  switch (dp * 2 + nt - 1) {
+    case 128: return launch_decode_t<FMT, 64, 1>(p, dev, sms, s);
+    case 129: return launch_decode_t<FMT, 64, 2>(p, dev, sms, s);
+    case 256: return launch_decode_t<FMT, 128, 1>(p, dev, sms, s);
+    case 257: return launch_decode_t<FMT, 128, 2>(p, dev, sms, s);
+    case 384: return launch_decode_t<FMT, 192, 1>(p, dev, sms, s);
+    case 385: return launch_decode_t<FMT, 192, 2>(p, dev, sms, s);
+    case 512: return launch_decode_t<FMT, 256, 1>(p, dev, sms, s);
+    case 513: return launch_decode_t<FMT, 256, 2>(p, dev, sms, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t k3attn_workspace_bytes(const k3attn_dims* dims) {
   if (check_dims(dims) != K3MOE_OK) return 0;
-  return K3ATTN_MIN_WORKSPACE;
+  return kRecords + (size_t)2 * DEC_MAX_BLOCKS * 8 * dec_nt(*dims) * (dec_dp(*dims) + 2) * 4;
 }
 
 k3moe_status k3attn_workspace_init(void* ws, size_t ws_bytes, void* stream) {
@@ -157,7 +199,7 @@ k3moe_status k3attn_workspace_init(void* ws, size_t ws_bytes, void* stream) {
   int dev, sms;
   const k3moe_status st = check_device(&dev, &sms);
   if (st != K3MOE_OK) return st;
-  K3A_TRY(cudaMemsetAsync(ws, 0, K3ATTN_MIN_WORKSPACE, static_cast<cudaStream_t>(stream)));
+  K3A_TRY(cudaMemsetAsync(ws, 0, ws_bytes < kRecords ? ws_bytes : kRecords, static_cast<cudaStream_t>(stream)));
   return K3MOE_OK;
 }
 
@@ -288,14 +330,24 @@ k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q
   if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
   DecodeParams p{};
   p.q = q; p.q_stride = q_stride;
-  p.B = B; p.Hq = d.n_heads; p.Hkv = d.n_kv_heads; p.D = d.head_dim; p.window = d.window;
-  p.scale = d.softmax_scale;
+  p.B = B; p.Hq = d.n_heads; p.Hkv = d.n_kv_heads; p.G = d.n_heads / d.n_kv_heads; p.D = d.head_dim;
+  p.window = d.window;
+  p.scale = d.softmax_scale * 1.4426950408889634f;
   p.c = view_of(*cache);
+  // t / page_size as a product's high half: with 2^s >= page_size, mul = floor(2^32 (2^s - page_size) /
+  // page_size) + 1, it is (umulhi(t, mul) + t) >> s for every t < 2^31
+  while ((1u << p.page_shift) < (uint32_t)cache->page_size) ++p.page_shift;
+  p.page_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << p.page_shift) - (uint64_t)cache->page_size)) /
+                              (uint64_t)cache->page_size + 1);
   p.table = page_table; p.table_width = table_width; p.lens = lens;
   p.out = out; p.lse = lse;
-  p.status = static_cast<uint32_t*>(ws);
-  K3A_TRY(launch(cache->format == K3ATTN_E4M3 ? k3_decode_kernel<CF_E4M3> : k3_decode_kernel<CF_BF16>,
-                 dim3(d.n_heads, B), dim3(DEC_WARPS * 32), 0, static_cast<cudaStream_t>(stream), p));
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.status = reinterpret_cast<uint32_t*>(w);
+  p.arrived = reinterpret_cast<uint32_t*>(w + kCounters);
+  p.parts = reinterpret_cast<float*>(w + kRecords);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_decode<CF_E4M3>(p, dec_dp(d), dec_nt(d), dev, sms, s)
+                                        : launch_decode<CF_BF16>(p, dec_dp(d), dec_nt(d), dev, sms, s)));
   return K3MOE_OK;
 }
 
