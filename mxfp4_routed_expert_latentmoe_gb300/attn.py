@@ -17,7 +17,9 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _stream, device_status, lib  # noqa: F401  (device_status: the status word of ws)
+import torch
+
+from . import K3MoEError, device_status, lib  # noqa: F401  (device_status: the status word of ws)
 
 BF16, E4M3 = 0, 1  # K3ATTN_BF16, K3ATTN_E4M3
 MIN_WORKSPACE = 256  # K3ATTN_MIN_WORKSPACE
@@ -29,6 +31,10 @@ class Dims(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("rot_dim", ctypes.c_int32), ("rot_interleaved", ctypes.c_int32), ("rms_eps", ctypes.c_float),
                 ("softmax_scale", ctypes.c_float), ("window", ctypes.c_int32)]
+
+    def __init__(self, *args):
+        super().__init__(*args)
+        self.ref = ctypes.byref(self)
 
 
 def dims(n_heads, n_kv_heads, head_dim, rot_dim=None, rot_interleaved=False, rms_eps=1e-6, softmax_scale=None,
@@ -80,35 +86,49 @@ def declared_functions() -> list:
 
 
 # ------------------------------------------------------------------------------ checks
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+# (a decode step's call takes a few microseconds on the GPU: the checks are comparisons alone,
+# and a message is put together only where one fails)
+_bf16, _f32, _i32, _f64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.float64, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _tensor(t, name, dtype, shape):
-    _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == shape,
-          f"{name}: a CUDA tensor {list(shape)} of {dtype} is needed, got {list(t.shape)} of {t.dtype} on {t.device}")
+def _refuse(t, name, dtype, shape, how=""):
+    got = f"{list(t.shape)} (strides {list(t.stride())}) of {t.dtype} on {t.device}" if torch.is_tensor(t) else repr(t)
+    raise ValueError(f"{name}: a CUDA tensor {list(shape)} of {dtype}{how} is needed, got {got}")
 
 
 def _dense(t, name, dtype, shape):
-    _tensor(t, name, dtype, shape)
-    _need(t.is_contiguous(), f"{name}: must be contiguous")
+    """Pointer of a contiguous tensor."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, ", contiguous")
     return t.data_ptr()
 
 
 def _rows(t, name, T, heads, D):
     """Pointer and token stride of a [T, heads, D] bf16 tensor whose tokens' rows are dense."""
-    import torch
-    _tensor(t, name, torch.bfloat16, (T, heads, D))
+    if not (t.dtype is _bf16 and t.shape == (T, heads, D) and t.is_cuda):
+        _refuse(t, name, _bf16, (T, heads, D))
     sT, sH, sD = t.stride()
-    _need((sD == 1 or D == 1) and (sH == D or heads == 1), f"{name}: the heads of a token must be dense")
-    return t.data_ptr(), sT if T > 1 else max(sT, heads * D)
+    if sD != 1 or (sH != D and heads != 1):
+        _refuse(t, name, _bf16, (T, heads, D), ", the heads of a token dense,")
+    return t.data_ptr(), sT if T > 1 else heads * D
 
 
 def _ws(ws):
-    import torch
-    _need(ws.is_cuda and ws.is_contiguous() and ws.dtype == torch.uint8, "ws: a uint8 CUDA tensor is needed")
+    if not (ws.dtype is _u8 and ws.is_cuda and ws.is_contiguous()):
+        _refuse(ws, "ws", _u8, ("bytes",))
     return ws.data_ptr(), ws.numel()
+
+
+def _launch(fn, t, stream, *args):
+    """Calls fn(*args, stream): on `stream`, or the current stream of t's device."""
+    if stream is None:
+        s = _raw_stream(t.device.index)
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    code = fn(*args, s)
+    if code:
+        raise K3MoEError(code, fn.__name__)
 
 
 # ------------------------------------------------------------------------------ what a program keeps
@@ -118,9 +138,9 @@ def workspace_bytes(d: Dims) -> int:
 
 def workspace(d: Dims, device="cuda"):
     """A workspace for calls with these dims (or smaller ones), readied for its first use."""
-    import torch
     n = workspace_bytes(d)
-    _need(n > 0, "unsupported dims")
+    if n == 0:
+        raise ValueError("unsupported dims")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     workspace_init(ws)
     return ws
@@ -128,13 +148,11 @@ def workspace(d: Dims, device="cuda"):
 
 def workspace_init(ws, stream=None):
     """k3attn_workspace_init: readies a workspace (also clears its status word)."""
-    p, n = _ws(ws)
-    _check(_funcs().k3attn_workspace_init(p, n, _stream(stream)), "k3attn_workspace_init")
+    _launch(_funcs().k3attn_workspace_init, ws, stream, *_ws(ws))
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
     """inv_freq [rot_dim / 2] f64: theta^(-2i / rot_dim)."""
-    import torch
     return theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
 
 
@@ -144,34 +162,32 @@ class KVCache:
     values dense); for E4M3 k_scale, v_scale [n_pages, Hkv, page_size] f32."""
 
     def __init__(self, d: Dims, k, v, k_scale=None, v_scale=None):
-        import torch
-        _need(k.dim() == 4 and k.dtype in (torch.bfloat16, torch.float8_e4m3fn),
-              "k: [n_pages, Hkv, page_size, D] of bfloat16 or float8_e4m3fn is needed")
-        n, page = k.shape[0], k.shape[2]
+        shape = (k.shape[0], d.n_kv_heads, k.shape[2], d.head_dim) if k.dim() == 4 else ("n_pages", "Hkv", "page", "D")
+        fmt = E4M3 if k.dtype is torch.float8_e4m3fn else BF16
         for t, name in ((k, "k"), (v, "v")):
-            _tensor(t, name, k.dtype, (n, d.n_kv_heads, page, d.head_dim))
-            _need(t.stride(3) == 1, f"{name}: a row's values must be dense")
-        _need(k.stride() == v.stride(), "k and v must have the same strides")
-        fmt = E4M3 if k.dtype == torch.float8_e4m3fn else BF16
-        ss = (0, 0, 0)
+            if not (t.dtype is (torch.float8_e4m3fn if fmt == E4M3 else _bf16) and t.shape == shape and t.is_cuda
+                    and t.stride(3) == 1 and t.stride() == k.stride()):
+                _refuse(t, name, "bfloat16 or float8_e4m3fn", shape, ", a row's values dense, strides as k's,")
+        n, page, ss = shape[0], shape[2], (0, 0, 0)
         if fmt == E4M3:
-            _need(k_scale is not None and v_scale is not None, "an E4M3 cache needs k_scale and v_scale")
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                _tensor(t, name, torch.float32, (n, d.n_kv_heads, page))
-            _need(k_scale.stride() == v_scale.stride(), "k_scale and v_scale must have the same strides")
+                if t is None or not (t.dtype is _f32 and t.shape == shape[:3] and t.is_cuda
+                                     and t.stride() == k_scale.stride()):
+                    _refuse(t, name, _f32, shape[:3], ", strides as k_scale's,")
             ss = k_scale.stride()
-        else:
-            _need(k_scale is None and v_scale is None, "a bf16 cache has no scales")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.page_size, self.head_shape = n, page, (d.n_kv_heads, d.head_dim)
         self.c = CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt == E4M3 else None,
                         v_scale.data_ptr() if fmt == E4M3 else None, fmt, n, page, 0, *k.stride()[:3], *ss)
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, d: Dims, n_pages: int, page_size: int, fmt: str = "bf16", device="cuda"):
         """A dense cache of zeros; fmt "bf16" or "e4m3"."""
-        import torch
-        _need(fmt in ("bf16", "e4m3"), "fmt is bf16 or e4m3")
+        if fmt not in ("bf16", "e4m3"):
+            raise ValueError("fmt is bf16 or e4m3")
         shape = (n_pages, d.n_kv_heads, page_size, d.head_dim)
         if fmt == "bf16":
             return cls(d, *(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
@@ -179,84 +195,60 @@ class KVCache:
         return cls(d, *codes, *(torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
 
 
-def _cache(d: Dims, cache: KVCache):
-    _need(cache.head_shape == (d.n_kv_heads, d.head_dim), "the cache has another head shape")
-    return ctypes.byref(cache.c)
+def _cache(d, cache):
+    if cache.head_shape != (d.n_kv_heads, d.head_dim):
+        raise ValueError(f"the cache's (Hkv, D) are {cache.head_shape}, the dims' {(d.n_kv_heads, d.head_dim)}")
+    return cache.ref
 
 
 # ------------------------------------------------------------------------------ the operators
-def _norm_args(d, T, positions, inv_freq, q_w, k_w):
-    import torch
-    D = d.head_dim
-    return (_dense(positions, "positions", torch.int32, (T,)),
-            _dense(inv_freq, "inv_freq", torch.float64, (d.rot_dim // 2,)) if d.rot_dim else None,
-            _dense(q_w, "q_w", torch.float32, (D,)), _dense(k_w, "k_w", torch.float32, (D,)))
+def _freq(d, inv_freq):
+    return _dense(inv_freq, "inv_freq", _f64, (d.rot_dim // 2,)) if d.rot_dim else None
 
 
 def qk_norm_rope(d: Dims, q, k, positions, inv_freq, q_w, k_w, q_out, k_out, stream=None):
     """k3attn_qk_norm_rope: q [T, Hq, D], k [T, Hkv, D] bf16 (slices of one projection's output
     will do) -> q_out, k_out, dense, normed per head and rotated.  inv_freq may be None when
     d.rot_dim is 0."""
-    import torch
-    T, D = q.shape[0], d.head_dim
-    qp, qs = _rows(q, "q", T, d.n_heads, D)
-    kp, ks = _rows(k, "k", T, d.n_kv_heads, D)
-    pos, freq, qw, kw = _norm_args(d, T, positions, inv_freq, q_w, k_w)
-    _check(_funcs().k3attn_qk_norm_rope(ctypes.byref(d), T, qp, qs, kp, ks, pos, freq, qw, kw,
-                                        _dense(q_out, "q_out", torch.bfloat16, (T, d.n_heads, D)),
-                                        _dense(k_out, "k_out", torch.bfloat16, (T, d.n_kv_heads, D)),
-                                        _stream(stream)), "k3attn_qk_norm_rope")
+    T, Hq, Hkv, D = q.shape[0], d.n_heads, d.n_kv_heads, d.head_dim
+    _launch(_funcs().k3attn_qk_norm_rope, q, stream, d.ref, T, *_rows(q, "q", T, Hq, D), *_rows(k, "k", T, Hkv, D),
+            _dense(positions, "positions", _i32, (T,)), _freq(d, inv_freq), _dense(q_w, "q_w", _f32, (D,)),
+            _dense(k_w, "k_w", _f32, (D,)), _dense(q_out, "q_out", _bf16, (T, Hq, D)),
+            _dense(k_out, "k_out", _bf16, (T, Hkv, D)))
 
 
 def kv_write(d: Dims, k, v, slots, cache: KVCache, ws, stream=None):
     """k3attn_kv_write: k, v [T, Hkv, D] bf16 into the cache at slots [T] int32 (-1: not written)."""
-    import torch
-    T, D = k.shape[0], d.head_dim
-    kp, ks = _rows(k, "k", T, d.n_kv_heads, D)
-    vp, vs = _rows(v, "v", T, d.n_kv_heads, D)
-    _check(_funcs().k3attn_kv_write(ctypes.byref(d), T, kp, ks, vp, vs, _dense(slots, "slots", torch.int32, (T,)),
-                                    _cache(d, cache), *_ws(ws), _stream(stream)), "k3attn_kv_write")
+    T, Hkv, D = k.shape[0], d.n_kv_heads, d.head_dim
+    _launch(_funcs().k3attn_kv_write, k, stream, d.ref, T, *_rows(k, "k", T, Hkv, D), *_rows(v, "v", T, Hkv, D),
+            _dense(slots, "slots", _i32, (T,)), _cache(d, cache), *_ws(ws))
 
 
 def kv_append(d: Dims, q, k, v, positions, slots, inv_freq, q_w, k_w, cache: KVCache, q_out, ws, k_out=None,
               stream=None):
     """k3attn_kv_append: qk_norm_rope of q into q_out and of k, and the write of k and v into the
     cache, in one pass; k_out (optional) also receives the keys."""
-    import torch
-    T, D = q.shape[0], d.head_dim
-    qp, qs = _rows(q, "q", T, d.n_heads, D)
-    kp, ks = _rows(k, "k", T, d.n_kv_heads, D)
-    vp, vs = _rows(v, "v", T, d.n_kv_heads, D)
-    pos, freq, qw, kw = _norm_args(d, T, positions, inv_freq, q_w, k_w)
-    _check(_funcs().k3attn_kv_append(ctypes.byref(d), T, qp, qs, kp, ks, vp, vs, pos,
-                                     _dense(slots, "slots", torch.int32, (T,)), freq, qw, kw, _cache(d, cache),
-                                     _dense(q_out, "q_out", torch.bfloat16, (T, d.n_heads, D)),
-                                     None if k_out is None else
-                                     _dense(k_out, "k_out", torch.bfloat16, (T, d.n_kv_heads, D)),
-                                     *_ws(ws), _stream(stream)), "k3attn_kv_append")
+    T, Hq, Hkv, D = q.shape[0], d.n_heads, d.n_kv_heads, d.head_dim
+    _launch(_funcs().k3attn_kv_append, q, stream, d.ref, T, *_rows(q, "q", T, Hq, D), *_rows(k, "k", T, Hkv, D),
+            *_rows(v, "v", T, Hkv, D), _dense(positions, "positions", _i32, (T,)),
+            _dense(slots, "slots", _i32, (T,)), _freq(d, inv_freq), _dense(q_w, "q_w", _f32, (D,)),
+            _dense(k_w, "k_w", _f32, (D,)), _cache(d, cache), _dense(q_out, "q_out", _bf16, (T, Hq, D)),
+            None if k_out is None else _dense(k_out, "k_out", _bf16, (T, Hkv, D)), *_ws(ws))
 
 
 def kv_read(d: Dims, slots, cache: KVCache, k_out, v_out, ws, stream=None):
     """k3attn_kv_read: the rows at slots [T] int32 as bf16, k_out and v_out [T, Hkv, D]."""
-    import torch
-    T = slots.shape[0]
-    shape = (T, d.n_kv_heads, d.head_dim)
-    _check(_funcs().k3attn_kv_read(ctypes.byref(d), T, _dense(slots, "slots", torch.int32, (T,)), _cache(d, cache),
-                                   _dense(k_out, "k_out", torch.bfloat16, shape),
-                                   _dense(v_out, "v_out", torch.bfloat16, shape), *_ws(ws), _stream(stream)),
-           "k3attn_kv_read")
+    T, Hkv, D = slots.shape[0], d.n_kv_heads, d.head_dim
+    _launch(_funcs().k3attn_kv_read, slots, stream, d.ref, T, _dense(slots, "slots", _i32, (T,)), _cache(d, cache),
+            _dense(k_out, "k_out", _bf16, (T, Hkv, D)), _dense(v_out, "v_out", _bf16, (T, Hkv, D)), *_ws(ws))
 
 
 def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None):
     """k3attn_decode: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
     of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32."""
-    import torch
-    B, D = q.shape[0], d.head_dim
-    qp, qs = _rows(q, "q", B, d.n_heads, D)
-    width = page_table.shape[1] if page_table.dim() == 2 else -1
-    _check(_funcs().k3attn_decode(ctypes.byref(d), B, qp, qs, _cache(d, cache),
-                                  _dense(page_table, "page_table", torch.int32, (B, width)), width,
-                                  _dense(lens, "lens", torch.int32, (B,)),
-                                  _dense(out, "out", torch.bfloat16, (B, d.n_heads, D)),
-                                  None if lse is None else _dense(lse, "lse", torch.float32, (B, d.n_heads)),
-                                  *_ws(ws), _stream(stream)), "k3attn_decode")
+    B, Hq, D = q.shape[0], d.n_heads, d.head_dim
+    width = page_table.shape[-1]
+    _launch(_funcs().k3attn_decode, q, stream, d.ref, B, *_rows(q, "q", B, Hq, D), _cache(d, cache),
+            _dense(page_table, "page_table", _i32, (B, width)), width, _dense(lens, "lens", _i32, (B,)),
+            _dense(out, "out", _bf16, (B, Hq, D)), None if lse is None else _dense(lse, "lse", _f32, (B, Hq)),
+            *_ws(ws))

@@ -136,9 +136,34 @@ QkvParams qkv_params(const k3attn_dims& d, int32_t T) {
   return p;
 }
 
-template <bool NORM, int FMT>
-cudaError_t launch_qkv(const QkvParams& p, cudaStream_t s) {
-  return launch(k3_qkv_kernel<NORM, FMT>, dim3(p.T), dim3(QKV_WARPS * 32), 0, s, p);
+// lanes of a row: eight elements each
+template <int FMT, bool WRITE>
+cudaError_t launch_rows(const QkvParams& p, cudaStream_t s) {
+  const int lpr = p.D <= 64 ? 8 : (p.D <= 128 ? 16 : 32);
+  const int64_t per = (int64_t)(QKV_THREADS / lpr) * QKV_ROWS;
+  const int64_t grid = ((int64_t)p.T * 2 * p.Hkv + per - 1) / per;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return launch(lpr == 8 ? k3_rows_kernel<8, FMT, WRITE>
+                         : (lpr == 16 ? k3_rows_kernel<16, FMT, WRITE> : k3_rows_kernel<32, FMT, WRITE>),
+                dim3((unsigned)grid), dim3(QKV_THREADS), 0, s, p);
+}
+
+// The norms' blocks: as many tokens' rows as the threads take at QKV_ROWS each, or a balanced
+// part of one token's; a launch that this leaves with fewer blocks than SMs takes one row a
+// thread (a call on few tokens waits for latency: its rows are spread out).
+template <int FMT>
+cudaError_t launch_norm(QkvParams p, int sms, cudaStream_t s) {
+  const int lpr = p.D <= 64 ? 8 : (p.D <= 128 ? 16 : 32), subs = QKV_THREADS / lpr;
+  const int rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2);
+  for (int most = subs * QKV_ROWS;; most = subs) {
+    const int parts = (rows + most - 1) / most;
+    p.rows = (rows + parts - 1) / parts;
+    p.tokens = most / p.rows < QKV_TOKENS ? most / p.rows : QKV_TOKENS;
+    const dim3 grid((p.T + p.tokens - 1) / p.tokens, (rows + p.rows - 1) / p.rows);
+    if (most > subs && (int64_t)grid.x * grid.y < sms) continue;
+    return launch(lpr == 8 ? k3_norm_kernel<8, FMT> : (lpr == 16 ? k3_norm_kernel<16, FMT> : k3_norm_kernel<32, FMT>),
+                  grid, dim3(QKV_THREADS), 0, s, p);
+  }
 }
 
 // per (kernel, device): raise the kernel's dynamic shared memory limit once
@@ -223,7 +248,7 @@ k3moe_status k3attn_qk_norm_rope(const k3attn_dims* dims, int32_t T, const uint1
   QkvParams p = qkv_params(d, T);
   p.q = q; p.q_stride = q_stride; p.k = k; p.k_stride = k_stride;
   p.pos = positions; p.inv_freq = inv_freq; p.q_w = q_w; p.k_w = k_w; p.q_out = q_out; p.k_out = k_out;
-  K3A_TRY((launch_qkv<true, CF_NONE>(p, static_cast<cudaStream_t>(stream))));
+  K3A_TRY(launch_norm<CF_NONE>(p, sms, static_cast<cudaStream_t>(stream)));
   return K3MOE_OK;
 }
 
@@ -248,7 +273,7 @@ k3moe_status k3attn_kv_write(const k3attn_dims* dims, int32_t T, const uint16_t*
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_qkv<false, CF_E4M3>(p, s) : launch_qkv<false, CF_BF16>(p, s)));
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, true>(p, s) : launch_rows<CF_BF16, true>(p, s)));
   return K3MOE_OK;
 }
 
@@ -282,7 +307,7 @@ k3moe_status k3attn_kv_append(const k3attn_dims* dims, int32_t T, const uint16_t
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_qkv<true, CF_E4M3>(p, s) : launch_qkv<true, CF_BF16>(p, s)));
+  K3A_TRY(cache->format == K3ATTN_E4M3 ? launch_norm<CF_E4M3>(p, sms, s) : launch_norm<CF_BF16>(p, sms, s));
   return K3MOE_OK;
 }
 
@@ -304,8 +329,7 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY(launch(cache->format == K3ATTN_E4M3 ? k3_kv_read_kernel<CF_E4M3> : k3_kv_read_kernel<CF_BF16>, dim3(T),
-                 dim3(QKV_WARPS * 32), 0, s, p));
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, false>(p, s) : launch_rows<CF_BF16, false>(p, s)));
   return K3MOE_OK;
 }
 
