@@ -31,7 +31,6 @@ struct DecodeParams {
   int32_t groups;  // head groups of a key head: ceil(G / (8 NT))
   float scale;     // softmax_scale * log2(e): logits in powers of two
   CacheView c;
-  uint32_t page_mul, page_shift;  // t / page_size = (umulhi(t, mul) + t) >> shift for t < 2^31
   const int32_t *table, *lens;
   int32_t table_width;
   uint16_t* out;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       const int32_t t = row_token();
       entry = 0;
       if (t < ahead.n) {
-        const uint32_t pg = (__umulhi((uint32_t)t, p.page_mul) + (uint32_t)t) >> p.page_shift;
+        const uint32_t pg = p.c.by_page(t);
         entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
       }
     };
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       if (lane == 0) *reinterpret_cast<uint32_t*>(__cvta_shared_to_generic(st + C::STAGE - 16)) = mask;
       if (mask == 0) return;
       const int32_t kvh = ahead.hr / p.groups;
-      const uint32_t pg = (__umulhi((uint32_t)t, p.page_mul) + (uint32_t)t) >> p.page_shift;
+      const uint32_t pg = p.c.by_page(t);
       const int64_t in_page = t - (int32_t)(pg * (uint32_t)p.c.page_size);
       const int64_t off = ok ? entry * p.c.page + kvh * p.c.head + in_page * p.c.tok : 0;
       if constexpr (FMT == CF_E4M3) {

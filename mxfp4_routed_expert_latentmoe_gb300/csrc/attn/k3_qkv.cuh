@@ -15,6 +15,19 @@ namespace k3 {
 
 enum { CF_NONE = -1, CF_BF16 = K3ATTN_BF16, CF_E4M3 = K3ATTN_E4M3 };
 
+// n / d for n < 2^31 as the high half of a product: with 2^shift >= d and mul = floor(2^32
+// (2^shift - d) / d) + 1 it is (umulhi(n, mul) + n) >> shift
+struct Divisor {
+  uint32_t mul, shift;
+  static Divisor of(uint32_t d) {
+    Divisor x{0, 0};
+    while ((1u << x.shift) < d) ++x.shift;
+    x.mul = (uint32_t)(((((uint64_t)1 << x.shift) - d) << 32) / d + 1);
+    return x;
+  }
+  K3_DEVI uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 // the cache as the kernels address it: strides of the rows in bytes, of the scales in elements
 struct CacheView {
   uint8_t *k, *v;
@@ -22,6 +35,7 @@ struct CacheView {
   int64_t page, head, tok;
   int64_t spage, shead, stok;
   int32_t n_pages, page_size;
+  Divisor by_page;
 };
 
 struct QkvParams {
@@ -35,8 +49,8 @@ struct QkvParams {
   uint16_t *q_out, *k_out, *v_out;
   CacheView c;
   uint32_t* status;
-  int32_t tokens;  // tokens of a block (norms), rows of a token in a block
-  int32_t rows;
+  int32_t tokens, rows;  // a block's tokens (norms), and rows of each
+  Divisor by_rows;       // by `rows`; rows_kernel: by 2 Hkv
 };
 
 constexpr int QKV_THREADS = 256;
@@ -77,12 +91,6 @@ K3_DEVI uint2 e4m3x8(const float (&x)[8]) {
     h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
-K3_DEVI void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
 // The place of a slot in the cache.
 struct Place {
   int64_t page;
@@ -92,7 +100,7 @@ struct Place {
 K3_DEVI Place place_of(const QkvParams& p, int32_t slot, bool report) {
   Place x{0, 0, false};
   if (slot >= 0) {
-    const int32_t pg = slot / p.c.page_size;
+    const int32_t pg = (int32_t)p.c.by_page(slot);
     x.ok = pg < p.c.n_pages;
     x.page = x.ok ? pg : 0;
     x.at = x.ok ? slot - pg * p.c.page_size : 0;
@@ -101,15 +109,18 @@ K3_DEVI Place place_of(const QkvParams& p, int32_t slot, bool report) {
   return x;
 }
 
-// One row of the cache from its LPR lanes (lane li holds elements 8 li .. 8 li + 7, `on` where
-// they lie below D): `raw` is the row in bf16 (a row that came as bf16 keeps its bits), y in
-// fp32.  All lanes of a warp call it; `keep`: whether the row is written.
+// One row of the cache from its LPR lanes (lane li holds the four elements from ea and the four
+// from eb, `on` where they lie below D): `raw` is the row in bf16 (a row that came as bf16
+// keeps its bits), y in fp32.  All lanes of a warp call it; `keep`: whether the row is written.
 template <int FMT, int LPR>
 K3_DEVI void store_row(const QkvParams& p, bool is_v, int h, const Place& pl, bool keep, uint4 raw,
-                       const float (&y)[8], int li, bool on) {
+                       const float (&y)[8], int li, int ea, int eb, bool on) {
   uint8_t* row = (is_v ? p.c.v : p.c.k) + pl.page * p.c.page + h * p.c.head + pl.at * p.c.tok;
   if constexpr (FMT == CF_BF16) {
-    if (on && keep) *reinterpret_cast<uint4*>(row + 16 * li) = raw;
+    if (on && keep) {
+      *reinterpret_cast<uint2*>(row + 2 * ea) = make_uint2(raw.x, raw.y);
+      *reinterpret_cast<uint2*>(row + 2 * eb) = make_uint2(raw.z, raw.w);
+    }
   } else {
     // the largest magnitude by its bits, where infinities and NaN order above every number
     uint32_t m = 0;
@@ -123,141 +134,158 @@ K3_DEVI void store_row(const QkvParams& p, bool is_v, int h, const Place& pl, bo
     float z[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = y[i] * inv;
-    if (on && keep) *reinterpret_cast<uint2*>(row + 8 * li) = e4m3x8(z);
+    if (on && keep) {
+      const uint2 codes = e4m3x8(z);
+      *reinterpret_cast<uint32_t*>(row + ea) = codes.x;
+      *reinterpret_cast<uint32_t*>(row + eb) = codes.y;
+    }
     if (li == 0 && keep) (is_v ? p.c.vs : p.c.ks)[pl.page * p.c.spage + h * p.c.shead + pl.at * p.c.stok] = s;
   }
 }
 
 // Norms and rotation (FMT none), with the cache's rows in the same pass (FMT bf16, E4M3): a
-// block has p.rows rows of p.tokens tokens, LPR lanes a row.  A thread's place in its rows is
-// always the same, so it keeps the weights and, for a token's rows, the angles in registers;
-// the angles (fp64 products and one sine and cosine per token and pair) are shared by the block.
-template <int LPR, int FMT>
-__global__ void __launch_bounds__(QKV_THREADS) k3_norm_kernel(const QkvParams p) {
-  // (four more: the last pairs' load8 reaches past them)
-  __shared__ __align__(16) float s_cos[QKV_TOKENS][132], s_sin[QKV_TOKENS][132];
+// block has p.rows rows of each of p.tokens tokens, LPR lanes a row and up to ROWS rows a
+// thread.  A lane holds two pieces of four elements of a row: the two halves of four rotated
+// pairs (pairs (i, i + R/2)), or eight neighbours, so that pairs never cross lanes.  Its pieces
+// are the same in all its rows: weights and angles stay in registers, reloaded where the kind
+// of row or the token changes.  The angles (fp64 products and one sine and cosine per token and
+// pair) are shared by the block.
+template <int LPR, int FMT, int ROWS>
+__global__ void __launch_bounds__(QKV_THREADS, 4) k3_norm_kernel(const QkvParams p) {
+  __shared__ __align__(16) float s_cos[QKV_TOKENS][128], s_sin[QKV_TOKENS][128];
   constexpr int SUBS = QKV_THREADS / LPR;
-  const int li = threadIdx.x % LPR, sub = threadIdx.x / LPR, e = 8 * li;
+  const int li = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int t0 = blockIdx.x * p.tokens, r0 = blockIdx.y * p.rows;
   const int nt = min(p.tokens, p.T - t0), nr = min(p.rows, p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2) - r0);
-  const bool on = e < p.D;
+  const bool on = 8 * li < p.D, rotated = 8 * li < p.R;
+  const int half = p.R / 2;
+  // this lane's pieces and their first angle
+  int ea = 8 * li, eb = ea + 4, angle = ea / 2;
+  if (!p.inter && rotated) {
+    ea = angle = 4 * li;
+    eb = ea + half;
+  }
   grid_dep_wait();
   grid_dep_launch();
-  uint4 raw[QKV_ROWS];
-  int tok[QKV_ROWS], row[QKV_ROWS];
+  uint2 ra[ROWS], rb[ROWS];
+  int tok[ROWS], row[ROWS];
 #pragma unroll
-  for (int i = 0; i < QKV_ROWS; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     const int it = sub + i * SUBS;
-    tok[i] = it / nr;
-    row[i] = r0 + it - tok[i] * nr;
-    const int64_t t = t0 + tok[i];
-    const int r = row[i];
-    raw[i] = make_uint4(0, 0, 0, 0);
+    tok[i] = p.tokens == 1 ? (it < nr ? 0 : 1) : (int)p.by_rows(it);
+    row[i] = r0 + it - tok[i] * p.rows;
+    ra[i] = rb[i] = make_uint2(0, 0);
     if (tok[i] < nt && on) {
+      const int64_t t = t0 + tok[i];
+      const int r = row[i];
       const uint16_t* src = r < p.Hq ? p.q + t * p.q_stride + r * p.D
                             : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (r - p.Hq) * p.D
                                                : p.v + t * p.v_stride + (r - p.Hq - p.Hkv) * p.D;
-      raw[i] = *reinterpret_cast<const uint4*>(src + e);
+      ra[i] = *reinterpret_cast<const uint2*>(src + ea);
+      rb[i] = *reinterpret_cast<const uint2*>(src + eb);
     }
   }
-  float wq[8] = {}, wk[8] = {};
-  if (on) {
-    load8(p.q_w + e, wq);
-    load8(p.k_w + e, wk);
-  }
-  const int half = p.R / 2;
   for (int i = threadIdx.x; i < nt * half; i += QKV_THREADS) {
     const int t = i / half, j = i - t * half;
     rotation(p.pos[t0 + t], p.inv_freq[j], s_cos[t][j], s_sin[t][j]);
   }
   __syncthreads();
-  // the lanes of the other half of the rotated dims, this lane's angles
-  const bool first = e < half, rotated = e < p.R;
-  const int partner = (threadIdx.x & 31) + (rotated ? (first ? half / 8 : -(half / 8)) : 0);
-  const int a0 = p.inter ? e / 2 : (first ? e : e - half);
-  float c[8] = {}, s[8] = {};
-  int have = -1;
+  const float over_d = 1.0f / (float)p.D;
+  float4 wa = {}, wb = {}, c = {}, s = {};
+  int have_tok = -1, have_w = -1;
 #pragma unroll
-  for (int i = 0; i < QKV_ROWS; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     if (i * SUBS >= nt * nr) break;  // the whole block
     const bool there = tok[i] < nt;
     const int r = row[i];
-    const int64_t t = t0 + tok[i];
     const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
     const int h = is_q ? r : (is_v ? r - p.Hq - p.Hkv : r - p.Hq);
     float x[8];
-    unpack8(raw[i], x);
+    unpack8(make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y), x);
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    const float rs = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-    if (!is_v)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] *= rs * (is_q ? wq[k] : wk[k]);
-    if (half) {
-      if (there && tok[i] != have && rotated) {
-        have = tok[i];
-        load8(&s_cos[have][a0], c);  // (interleaved pairs use the first four)
-        load8(&s_sin[have][a0], s);
+    uint4 raw = make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y);
+    if (!is_v) {
+      const float rs = rsqrtf(ss * over_d + p.eps);
+      if (on && have_w != (int)is_q) {
+        have_w = is_q;
+        const float* w = is_q ? p.q_w : p.k_w;
+        wa = __ldg(reinterpret_cast<const float4*>(w + ea));
+        wb = __ldg(reinterpret_cast<const float4*>(w + eb));
       }
-      if (p.inter) {
-        if (rotated && !is_v)
+      x[0] *= rs * wa.x; x[1] *= rs * wa.y; x[2] *= rs * wa.z; x[3] *= rs * wa.w;
+      x[4] *= rs * wb.x; x[5] *= rs * wb.y; x[6] *= rs * wb.z; x[7] *= rs * wb.w;
+      if (rotated) {
+        if (there && tok[i] != have_tok) {
+          have_tok = tok[i];
+          c = *reinterpret_cast<const float4*>(&s_cos[have_tok][angle]);
+          s = *reinterpret_cast<const float4*>(&s_sin[have_tok][angle]);
+        }
+        const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        if (p.inter) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float a = x[2 * k], b = x[2 * k + 1];
-            x[2 * k] = a * c[k] - b * s[k];
-            x[2 * k + 1] = b * c[k] + a * s[k];
+            x[2 * k] = a * cc[k] - b * sn[k];
+            x[2 * k + 1] = b * cc[k] + a * sn[k];
           }
-      } else {
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float o = __shfl_sync(0xFFFFFFFFu, x[k], partner);
-          if (rotated && !is_v) x[k] = first ? x[k] * c[k] - o * s[k] : x[k] * c[k] + o * s[k];
+          for (int k = 0; k < 4; ++k) {
+            const float a = x[k], b = x[4 + k];
+            x[k] = a * cc[k] - b * sn[k];
+            x[4 + k] = b * cc[k] + a * sn[k];
+          }
         }
       }
+      raw = pack8(x);
     }
-    if (!is_v) raw[i] = pack8(x);
-    if (there && on) {
-      if (is_q) *reinterpret_cast<uint4*>(p.q_out + (t * p.Hq + h) * p.D + e) = raw[i];
-      if (!is_q && !is_v && p.k_out) *reinterpret_cast<uint4*>(p.k_out + (t * p.Hkv + h) * p.D + e) = raw[i];
+    const int64_t t = t0 + tok[i];
+    if (there && on && !is_v) {
+      uint16_t* dst = is_q ? p.q_out + (t * p.Hq + h) * p.D : (p.k_out ? p.k_out + (t * p.Hkv + h) * p.D : nullptr);
+      if (dst) {
+        *reinterpret_cast<uint2*>(dst + ea) = make_uint2(raw.x, raw.y);
+        *reinterpret_cast<uint2*>(dst + eb) = make_uint2(raw.z, raw.w);
+      }
     }
     if constexpr (FMT != CF_NONE) {
       const bool cached = there && !is_q;
       if (__any_sync(0xFFFFFFFFu, cached)) {
         const Place pl = place_of(p, cached ? p.slots[t] : -1, li == 0);
-        store_row<FMT, LPR>(p, is_v, h, pl, cached && pl.ok, raw[i], x, li, on);
+        store_row<FMT, LPR>(p, is_v, h, pl, cached && pl.ok, raw, x, li, ea, eb, on);
       }
     }
   }
 }
 
 // Rows of the cache written from dense k, v (WRITE) or read back: row r of 2 Hkv a token, keys
-// first; a block takes QKV_ROWS times its row groups in a line.
-template <int LPR, int FMT, bool WRITE>
+// first; a block takes ROWS times its row groups in a line.
+template <int LPR, int FMT, bool WRITE, int ROWS>
 __global__ void __launch_bounds__(QKV_THREADS) k3_rows_kernel(const QkvParams p) {
   constexpr int SUBS = QKV_THREADS / LPR;
   const int li = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const bool on = 8 * li < p.D;
   const int nr = 2 * p.Hkv;
-  const int64_t first = (int64_t)blockIdx.x * (SUBS * QKV_ROWS);
+  const int64_t first = (int64_t)blockIdx.x * (SUBS * ROWS);
   const int32_t t0 = (int32_t)(first / nr), rest = (int32_t)(first - (int64_t)t0 * nr);
   grid_dep_wait();
   grid_dep_launch();
-  int32_t slot[QKV_ROWS], tok[QKV_ROWS], row[QKV_ROWS];
+  int32_t slot[ROWS], tok[ROWS], row[ROWS];
 #pragma unroll
-  for (int i = 0; i < QKV_ROWS; ++i) {
-    const int32_t it = rest + sub + i * SUBS, dt = it / nr;
+  for (int i = 0; i < ROWS; ++i) {
+    const int32_t it = rest + sub + i * SUBS, dt = (int32_t)p.by_rows(it);
     row[i] = it - dt * nr;
     tok[i] = dt < p.T - t0 ? t0 + dt : -1;
     slot[i] = tok[i] >= 0 ? p.slots[tok[i]] : -1;
   }
-  uint4 raw[QKV_ROWS];
-  float sc[QKV_ROWS];
-  Place pl[QKV_ROWS];
+  uint4 raw[ROWS];
+  float sc[ROWS];
+  Place pl[ROWS];
 #pragma unroll
-  for (int i = 0; i < QKV_ROWS; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     pl[i] = place_of(p, slot[i], li == 0);
     const bool is_v = row[i] >= p.Hkv;
     const int h = is_v ? row[i] - p.Hkv : row[i];
@@ -280,13 +308,13 @@ __global__ void __launch_bounds__(QKV_THREADS) k3_rows_kernel(const QkvParams p)
     }
   }
 #pragma unroll
-  for (int i = 0; i < QKV_ROWS; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     const bool is_v = row[i] >= p.Hkv;
     const int h = is_v ? row[i] - p.Hkv : row[i];
     float x[8];
     if constexpr (WRITE) {
       unpack8(raw[i], x);
-      store_row<FMT, LPR>(p, is_v, h, pl[i], pl[i].ok, raw[i], x, li, on);
+      store_row<FMT, LPR>(p, is_v, h, pl[i], pl[i].ok, raw[i], x, li, 8 * li, 8 * li + 4, on);
     } else {
       if constexpr (FMT == CF_E4M3) {
         const uint32_t w[2] = {raw[i].x, raw[i].y};

@@ -70,6 +70,7 @@ CacheView view_of(const k3attn_cache& c) {
   v.stok = c.scale_token_stride;
   v.n_pages = c.n_pages;
   v.page_size = c.page_size;
+  v.by_page = Divisor::of((uint32_t)c.page_size);
   return v;
 }
 
@@ -137,33 +138,46 @@ QkvParams qkv_params(const k3attn_dims& d, int32_t T) {
 }
 
 // lanes of a row: eight elements each
-template <int FMT, bool WRITE>
-cudaError_t launch_rows(const QkvParams& p, cudaStream_t s) {
-  const int lpr = p.D <= 64 ? 8 : (p.D <= 128 ? 16 : 32);
-  const int64_t per = (int64_t)(QKV_THREADS / lpr) * QKV_ROWS;
-  const int64_t grid = ((int64_t)p.T * 2 * p.Hkv + per - 1) / per;
+int lanes_of(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
+
+// ROWS rows a thread, where that leaves every SM a block (a smaller call waits for latency:
+// its rows are spread out, one a thread)
+template <int FMT, bool WRITE, int ROWS>
+cudaError_t launch_rows_t(const QkvParams& p, int lpr, int64_t grid, cudaStream_t s) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch(lpr == 8 ? k3_rows_kernel<8, FMT, WRITE>
-                         : (lpr == 16 ? k3_rows_kernel<16, FMT, WRITE> : k3_rows_kernel<32, FMT, WRITE>),
+  return launch(lpr == 8 ? k3_rows_kernel<8, FMT, WRITE, ROWS>
+                         : (lpr == 16 ? k3_rows_kernel<16, FMT, WRITE, ROWS> : k3_rows_kernel<32, FMT, WRITE, ROWS>),
                 dim3((unsigned)grid), dim3(QKV_THREADS), 0, s, p);
 }
+template <int FMT, bool WRITE>
+cudaError_t launch_rows(QkvParams p, int sms, cudaStream_t s) {
+  const int lpr = lanes_of(p.D);
+  const int64_t rows = (int64_t)p.T * 2 * p.Hkv, per = QKV_THREADS / lpr;
+  p.by_rows = Divisor::of(2 * p.Hkv);
+  const int64_t grid = (rows + per * QKV_ROWS - 1) / (per * QKV_ROWS);
+  if (grid >= sms) return launch_rows_t<FMT, WRITE, QKV_ROWS>(p, lpr, grid, s);
+  return launch_rows_t<FMT, WRITE, 1>(p, lpr, (rows + per - 1) / per, s);
+}
 
-// The norms' blocks: as many tokens' rows as the threads take at QKV_ROWS each, or a balanced
-// part of one token's; a launch that this leaves with fewer blocks than SMs takes one row a
-// thread (a call on few tokens waits for latency: its rows are spread out).
+// The norms' blocks: as many tokens' rows as the threads take at ROWS each, or a balanced part
+// of one token's
+template <int FMT, int ROWS>
+cudaError_t launch_norm_t(QkvParams p, int sms, cudaStream_t s) {
+  const int lpr = lanes_of(p.D), most = QKV_THREADS / lpr * ROWS;
+  const int rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2), parts = (rows + most - 1) / most;
+  p.rows = (rows + parts - 1) / parts;
+  p.tokens = most / p.rows < QKV_TOKENS ? most / p.rows : QKV_TOKENS;
+  p.by_rows = Divisor::of(p.rows);
+  const dim3 grid((p.T + p.tokens - 1) / p.tokens, (rows + p.rows - 1) / p.rows);
+  if constexpr (ROWS > 1)
+    if ((int64_t)grid.x * grid.y < sms) return launch_norm_t<FMT, 1>(p, sms, s);
+  return launch(lpr == 8 ? k3_norm_kernel<8, FMT, ROWS>
+                         : (lpr == 16 ? k3_norm_kernel<16, FMT, ROWS> : k3_norm_kernel<32, FMT, ROWS>),
+                grid, dim3(QKV_THREADS), 0, s, p);
+}
 template <int FMT>
-cudaError_t launch_norm(QkvParams p, int sms, cudaStream_t s) {
-  const int lpr = p.D <= 64 ? 8 : (p.D <= 128 ? 16 : 32), subs = QKV_THREADS / lpr;
-  const int rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2);
-  for (int most = subs * QKV_ROWS;; most = subs) {
-    const int parts = (rows + most - 1) / most;
-    p.rows = (rows + parts - 1) / parts;
-    p.tokens = most / p.rows < QKV_TOKENS ? most / p.rows : QKV_TOKENS;
-    const dim3 grid((p.T + p.tokens - 1) / p.tokens, (rows + p.rows - 1) / p.rows);
-    if (most > subs && (int64_t)grid.x * grid.y < sms) continue;
-    return launch(lpr == 8 ? k3_norm_kernel<8, FMT> : (lpr == 16 ? k3_norm_kernel<16, FMT> : k3_norm_kernel<32, FMT>),
-                  grid, dim3(QKV_THREADS), 0, s, p);
-  }
+cudaError_t launch_norm(const QkvParams& p, int sms, cudaStream_t s) {
+  return launch_norm_t<FMT, QKV_ROWS>(p, sms, s);
 }
 
 // per (kernel, device): raise the kernel's dynamic shared memory limit once
@@ -273,7 +287,7 @@ k3moe_status k3attn_kv_write(const k3attn_dims* dims, int32_t T, const uint16_t*
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, true>(p, s) : launch_rows<CF_BF16, true>(p, s)));
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, true>(p, sms, s) : launch_rows<CF_BF16, true>(p, sms, s)));
   return K3MOE_OK;
 }
 
@@ -329,7 +343,7 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, false>(p, s) : launch_rows<CF_BF16, false>(p, s)));
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, false>(p, sms, s) : launch_rows<CF_BF16, false>(p, sms, s)));
   return K3MOE_OK;
 }
 
@@ -358,11 +372,6 @@ k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q
   p.window = d.window;
   p.scale = d.softmax_scale * 1.4426950408889634f;
   p.c = view_of(*cache);
-  // t / page_size as a product's high half: with 2^s >= page_size, mul = floor(2^32 (2^s - page_size) /
-  // page_size) + 1, it is (umulhi(t, mul) + t) >> s for every t < 2^31
-  while ((1u << p.page_shift) < (uint32_t)cache->page_size) ++p.page_shift;
-  p.page_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << p.page_shift) - (uint64_t)cache->page_size)) /
-                              (uint64_t)cache->page_size + 1);
   p.table = page_table; p.table_width = table_width; p.lens = lens;
   p.out = out; p.lse = lse;
   uint8_t* w = static_cast<uint8_t*>(ws);
