@@ -15,6 +15,23 @@ namespace k3 {
 
 enum { CF_NONE = -1, CF_BF16 = K3ATTN_BF16, CF_E4M3 = K3ATTN_E4M3 };
 
+// two fp32 at once
+K3_DEVI float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+K3_DEVI float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+
 // n / d for n < 2^31 as the high half of a product: with 2^shift >= d and mul = floor(2^32
 // (2^shift - d) / d) + 1 it is (umulhi(n, mul) + n) >> shift
 struct Divisor {
@@ -50,12 +67,12 @@ struct QkvParams {
   CacheView c;
   uint32_t* status;
   int32_t tokens, rows;  // a block's tokens (norms), and rows of each
-  Divisor by_rows;       // by `rows`; rows_kernel: by 2 Hkv
+  Divisor by_rows;       // by `rows`; the rows kernel's: by Hkv
 };
 
-constexpr int QKV_THREADS = 256;
-constexpr int QKV_ROWS = 4;    // rows of a thread
-constexpr int QKV_TOKENS = 8;  // most tokens of a block of the norms
+constexpr int QKV_THREADS = 512;  // most threads of a block
+constexpr int QKV_ROWS = 4;       // rows of a thread in flight
+constexpr int QKV_TOKENS = 8;     // most tokens of a block of the norms
 constexpr float E4M3_MAX = 448.0f;
 constexpr float KV_MIN_SCALE = 0x1p-100f;  // its reciprocal and 448 times it are normal numbers
 
@@ -66,31 +83,40 @@ K3_DEVI void rotation(int32_t pos, double f, float& c, float& s) {
   sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
 }
 
-K3_DEVI void unpack8(uint4 v, float (&x)[8]) {
+// eight bf16 as four pairs of fp32, and back
+K3_DEVI void unpack8(uint4 v, float2 (&x)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-K3_DEVI uint4 pack8(const float (&x)[8]) {
+K3_DEVI uint4 pack8(const float2 (&x)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 b = __float22bfloat162_rn(x[i]);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // eight values to E4M3 (round to nearest even, saturated)
-K3_DEVI uint2 e4m3x8(const float (&x)[8]) {
+K3_DEVI uint2 e4m3x8(const float2 (&x)[4]) {
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) h[i] = __nv_cvt_float2_to_fp8x2(x[i], __NV_SATFINITE, __NV_E4M3);
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
+// eight E4M3 codes times s, rounded to bf16
+K3_DEVI uint4 e4m3x8_bf16(uint2 c, float s) {
+  float2 x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2_raw hr =
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((k < 2 ? c.x : c.y) >> (16 * (k & 1))), __NV_E4M3);
+    x[k] = mul2(__half22float2(__half2(hr)), make_float2(s, s));
+  }
+  return pack8(x);
+}
+
 // The place of a slot in the cache.
 struct Place {
   int64_t page;
@@ -109,13 +135,20 @@ K3_DEVI Place place_of(const QkvParams& p, int32_t slot, bool report) {
   return x;
 }
 
-// One row of the cache from its LPR lanes (lane li holds the four elements from ea and the four
+// byte offset of a head's row at a place, and the place of its scale
+K3_DEVI int64_t row_at(const QkvParams& p, const Place& pl, int h) {
+  return pl.page * p.c.page + (h * p.c.head + pl.at * p.c.tok);
+}
+K3_DEVI int64_t scale_at(const QkvParams& p, const Place& pl, int h) {
+  return pl.page * p.c.spage + (h * p.c.shead + pl.at * p.c.stok);
+}
+
+// One row of the cache from its LPR lanes (a lane holds the four elements from ea and the four
 // from eb, `on` where they lie below D): `raw` is the row in bf16 (a row that came as bf16
 // keeps its bits), y in fp32.  All lanes of a warp call it; `keep`: whether the row is written.
 template <int FMT, int LPR>
-K3_DEVI void store_row(const QkvParams& p, bool is_v, int h, const Place& pl, bool keep, uint4 raw,
-                       const float (&y)[8], int li, int ea, int eb, bool on) {
-  uint8_t* row = (is_v ? p.c.v : p.c.k) + pl.page * p.c.page + h * p.c.head + pl.at * p.c.tok;
+K3_DEVI void store_row(uint8_t* row, float* scale, bool keep, uint4 raw, const float2 (&y)[4], int li, int ea, int eb,
+                       bool on) {
   if constexpr (FMT == CF_BF16) {
     if (on && keep) {
       *reinterpret_cast<uint2*>(row + 2 * ea) = make_uint2(raw.x, raw.y);
@@ -126,20 +159,21 @@ K3_DEVI void store_row(const QkvParams& p, bool is_v, int h, const Place& pl, bo
     uint32_t m = 0;
     if (on)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 4; ++i)
+        m = max(m, max(__float_as_uint(y[i].x) & 0x7FFFFFFFu, __float_as_uint(y[i].y) & 0x7FFFFFFFu));
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const float s = m < 0x7F800000u ? fmaxf(__uint_as_float(m) / E4M3_MAX, KV_MIN_SCALE) : __uint_as_float(0x7FC00000u);
     const float inv = 1.0f / s;
-    float z[8];
+    float2 z[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = y[i] * inv;
+    for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], make_float2(inv, inv));
     if (on && keep) {
       const uint2 codes = e4m3x8(z);
       *reinterpret_cast<uint32_t*>(row + ea) = codes.x;
       *reinterpret_cast<uint32_t*>(row + eb) = codes.y;
     }
-    if (li == 0 && keep) (is_v ? p.c.vs : p.c.ks)[pl.page * p.c.spage + h * p.c.shead + pl.at * p.c.stok] = s;
+    if (li == 0 && keep) *scale = s;
   }
 }
 
@@ -147,13 +181,14 @@ K3_DEVI void store_row(const QkvParams& p, bool is_v, int h, const Place& pl, bo
 // block has p.rows rows of each of p.tokens tokens, LPR lanes a row and up to ROWS rows a
 // thread.  A lane holds two pieces of four elements of a row: the two halves of four rotated
 // pairs (pairs (i, i + R/2)), or eight neighbours, so that pairs never cross lanes.  Its pieces
-// are the same in all its rows: weights and angles stay in registers, reloaded where the kind
-// of row or the token changes.  The angles (fp64 products and one sine and cosine per token and
-// pair) are shared by the block.
+// are the same in all its rows: the products of weights and angles stay in registers, formed
+// anew where the kind of row or the token changes, and a row takes 12 packed operations for its
+// norm and rotation.  The angles (fp64 products and one sine and cosine per token and pair) are
+// shared by the block.
 template <int LPR, int FMT, int ROWS>
-__global__ void __launch_bounds__(QKV_THREADS, 4) k3_norm_kernel(const QkvParams p) {
+__global__ void __launch_bounds__(QKV_THREADS, 2) k3_norm_kernel(const QkvParams p) {
   __shared__ __align__(16) float s_cos[QKV_TOKENS][128], s_sin[QKV_TOKENS][128];
-  constexpr int SUBS = QKV_THREADS / LPR;
+  const int subs = blockDim.x / LPR;
   const int li = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int t0 = blockIdx.x * p.tokens, r0 = blockIdx.y * p.rows;
   const int nt = min(p.tokens, p.T - t0), nr = min(p.rows, p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2) - r0);
@@ -171,7 +206,7 @@ __global__ void __launch_bounds__(QKV_THREADS, 4) k3_norm_kernel(const QkvParams
   int tok[ROWS], row[ROWS];
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int it = sub + i * SUBS;
+    const int it = sub + i * subs;
     tok[i] = p.tokens == 1 ? (it < nr ? 0 : 1) : (int)p.by_rows(it);
     row[i] = r0 + it - tok[i] * p.rows;
     ra[i] = rb[i] = make_uint2(0, 0);
@@ -185,61 +220,76 @@ __global__ void __launch_bounds__(QKV_THREADS, 4) k3_norm_kernel(const QkvParams
       rb[i] = *reinterpret_cast<const uint2*>(src + eb);
     }
   }
-  for (int i = threadIdx.x; i < nt * half; i += QKV_THREADS) {
+  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
     const int t = i / half, j = i - t * half;
     rotation(p.pos[t0 + t], p.inv_freq[j], s_cos[t][j], s_sin[t][j]);
   }
   __syncthreads();
   const float over_d = 1.0f / (float)p.D;
-  float4 wa = {}, wb = {}, c = {}, s = {};
+  // y = x * co + z * si, z the other element of x's pair; without rotation co is the weight alone
+  float2 co[4] = {}, si[4] = {};
   int have_tok = -1, have_w = -1;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    if (i * SUBS >= nt * nr) break;  // the whole block
     const bool there = tok[i] < nt;
+    if (!__any_sync(0xFFFFFFFFu, there)) break;
     const int r = row[i];
     const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
     const int h = is_q ? r : (is_v ? r - p.Hq - p.Hkv : r - p.Hq);
-    float x[8];
-    unpack8(make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y), x);
-    float ss = 0.f;
+    uint4 raw = make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y);
+    float2 x[4];
+    unpack8(raw, x);
+    float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
+    for (int k = 1; k < 4; ++k) s2 = fma2(x[k], x[k], s2);
+    float ss = s2.x + s2.y;
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    uint4 raw = make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y);
     if (!is_v) {
-      const float rs = rsqrtf(ss * over_d + p.eps);
-      if (on && have_w != (int)is_q) {
+      if (on && there && (have_w != (int)is_q || have_tok != tok[i])) {
         have_w = is_q;
+        have_tok = tok[i];
         const float* w = is_q ? p.q_w : p.k_w;
-        wa = __ldg(reinterpret_cast<const float4*>(w + ea));
-        wb = __ldg(reinterpret_cast<const float4*>(w + eb));
+        const float4 wa = __ldg(reinterpret_cast<const float4*>(w + ea));
+        const float4 wb = __ldg(reinterpret_cast<const float4*>(w + eb));
+        co[0] = make_float2(wa.x, wa.y);
+        co[1] = make_float2(wa.z, wa.w);
+        co[2] = make_float2(wb.x, wb.y);
+        co[3] = make_float2(wb.z, wb.w);
+        if (rotated) {
+          const float4 c = *reinterpret_cast<const float4*>(&s_cos[have_tok][angle]);
+          const float4 s = *reinterpret_cast<const float4*>(&s_sin[have_tok][angle]);
+          if (p.inter) {  // pairs are (x, y) of each of the four
+            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              si[k] = make_float2(-co[k].y * sn[k], co[k].x * sn[k]);
+              co[k] = mul2(co[k], make_float2(cc[k], cc[k]));
+            }
+          } else {  // 0 with 2, 1 with 3
+            si[0] = make_float2(-co[2].x * s.x, -co[2].y * s.y);
+            si[1] = make_float2(-co[3].x * s.z, -co[3].y * s.w);
+            si[2] = mul2(co[0], make_float2(s.x, s.y));
+            si[3] = mul2(co[1], make_float2(s.z, s.w));
+            const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
+            co[0] = mul2(co[0], c0);
+            co[1] = mul2(co[1], c1);
+            co[2] = mul2(co[2], c0);
+            co[3] = mul2(co[3], c1);
+          }
+        }
       }
-      x[0] *= rs * wa.x; x[1] *= rs * wa.y; x[2] *= rs * wa.z; x[3] *= rs * wa.w;
-      x[4] *= rs * wb.x; x[5] *= rs * wb.y; x[6] *= rs * wb.z; x[7] *= rs * wb.w;
-      if (rotated) {
-        if (there && tok[i] != have_tok) {
-          have_tok = tok[i];
-          c = *reinterpret_cast<const float4*>(&s_cos[have_tok][angle]);
-          s = *reinterpret_cast<const float4*>(&s_sin[have_tok][angle]);
-        }
-        const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-        if (p.inter) {
+      const float rs = rsqrtf(ss * over_d + p.eps);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = x[2 * k], b = x[2 * k + 1];
-            x[2 * k] = a * cc[k] - b * sn[k];
-            x[2 * k + 1] = b * cc[k] + a * sn[k];
-          }
-        } else {
+      for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], make_float2(rs, rs));
+      float2 z[4] = {x[2], x[3], x[0], x[1]};
+      if (p.inter)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = x[k], b = x[4 + k];
-            x[k] = a * cc[k] - b * sn[k];
-            x[4 + k] = b * cc[k] + a * sn[k];
-          }
-        }
+        for (int k = 0; k < 4; ++k) z[k] = make_float2(x[k].y, x[k].x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] = mul2(x[k], co[k]);
+        if (rotated) x[k] = fma2(z[k], si[k], x[k]);
       }
       raw = pack8(x);
     }
@@ -255,81 +305,78 @@ __global__ void __launch_bounds__(QKV_THREADS, 4) k3_norm_kernel(const QkvParams
       const bool cached = there && !is_q;
       if (__any_sync(0xFFFFFFFFu, cached)) {
         const Place pl = place_of(p, cached ? p.slots[t] : -1, li == 0);
-        store_row<FMT, LPR>(p, is_v, h, pl, cached && pl.ok, raw, x, li, ea, eb, on);
+        store_row<FMT, LPR>((is_v ? p.c.v : p.c.k) + row_at(p, pl, h), (is_v ? p.c.vs : p.c.ks) + scale_at(p, pl, h),
+                            cached && pl.ok, raw, x, li, ea, eb, on);
       }
     }
   }
 }
 
-// Rows of the cache written from dense k, v (WRITE) or read back: row r of 2 Hkv a token, keys
-// first; a block takes ROWS times its row groups in a line.
-template <int LPR, int FMT, bool WRITE, int ROWS>
-__global__ void __launch_bounds__(QKV_THREADS) k3_rows_kernel(const QkvParams p) {
-  constexpr int SUBS = QKV_THREADS / LPR;
+// Rows of the cache written from dense k, v (WRITE) or read back: an item is a head of a token,
+// its key and its value, LPR lanes an item and ITEMS items a thread.
+template <int LPR, int FMT, bool WRITE, int ITEMS>
+__global__ void __launch_bounds__(256) k3_rows_kernel(const QkvParams p) {
+  constexpr int SUBS = 256 / LPR;
   const int li = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const bool on = 8 * li < p.D;
-  const int nr = 2 * p.Hkv;
-  const int64_t first = (int64_t)blockIdx.x * (SUBS * ROWS);
-  const int32_t t0 = (int32_t)(first / nr), rest = (int32_t)(first - (int64_t)t0 * nr);
+  const int64_t first = (int64_t)blockIdx.x * (SUBS * ITEMS);
+  const int32_t t0 = (int32_t)(first / p.Hkv), rest = (int32_t)(first - (int64_t)t0 * p.Hkv);
   grid_dep_wait();
   grid_dep_launch();
-  int32_t slot[ROWS], tok[ROWS], row[ROWS];
+  int32_t tok[ITEMS], head[ITEMS], slot[ITEMS];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const int32_t it = rest + sub + i * SUBS, dt = (int32_t)p.by_rows(it);
-    row[i] = it - dt * nr;
+    head[i] = it - dt * p.Hkv;
     tok[i] = dt < p.T - t0 ? t0 + dt : -1;
     slot[i] = tok[i] >= 0 ? p.slots[tok[i]] : -1;
   }
-  uint4 raw[ROWS];
-  float sc[ROWS];
-  Place pl[ROWS];
+  uint4 k[ITEMS], v[ITEMS];
+  float ks[ITEMS], vs[ITEMS];
+  Place pl[ITEMS];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     pl[i] = place_of(p, slot[i], li == 0);
-    const bool is_v = row[i] >= p.Hkv;
-    const int h = is_v ? row[i] - p.Hkv : row[i];
-    raw[i] = make_uint4(0, 0, 0, 0);
-    sc[i] = 0.f;
-    if (WRITE) {
-      if (on && pl[i].ok)
-        raw[i] = *reinterpret_cast<const uint4*>((is_v ? p.v + tok[i] * p.v_stride : p.k + tok[i] * p.k_stride) +
-                                                 h * p.D + 8 * li);
-    } else if (on && pl[i].ok) {
-      const uint8_t* src = (is_v ? p.c.v : p.c.k) + pl[i].page * p.c.page + h * p.c.head + pl[i].at * p.c.tok;
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    ks[i] = vs[i] = 0.f;
+    if (!on || !pl[i].ok) continue;
+    if constexpr (WRITE) {
+      const int32_t o = head[i] * p.D + 8 * li;
+      k[i] = *reinterpret_cast<const uint4*>(p.k + tok[i] * p.k_stride + o);
+      v[i] = *reinterpret_cast<const uint4*>(p.v + tok[i] * p.v_stride + o);
+    } else {
+      const int64_t o = row_at(p, pl[i], head[i]);
       if constexpr (FMT == CF_BF16) {
-        raw[i] = *reinterpret_cast<const uint4*>(src + 16 * li);
+        k[i] = *reinterpret_cast<const uint4*>(p.c.k + o + 16 * li);
+        v[i] = *reinterpret_cast<const uint4*>(p.c.v + o + 16 * li);
       } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(src + 8 * li);
-        raw[i].x = w.x;
-        raw[i].y = w.y;
-        sc[i] = (is_v ? p.c.vs : p.c.ks)[pl[i].page * p.c.spage + h * p.c.shead + pl[i].at * p.c.stok];
+        const uint2 kc = *reinterpret_cast<const uint2*>(p.c.k + o + 8 * li);
+        const uint2 vc = *reinterpret_cast<const uint2*>(p.c.v + o + 8 * li);
+        k[i].x = kc.x; k[i].y = kc.y;
+        v[i].x = vc.x; v[i].y = vc.y;
+        const int64_t so = scale_at(p, pl[i], head[i]);
+        ks[i] = p.c.ks[so];
+        vs[i] = p.c.vs[so];
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const bool is_v = row[i] >= p.Hkv;
-    const int h = is_v ? row[i] - p.Hkv : row[i];
-    float x[8];
+  for (int i = 0; i < ITEMS; ++i) {
     if constexpr (WRITE) {
-      unpack8(raw[i], x);
-      store_row<FMT, LPR>(p, is_v, h, pl[i], pl[i].ok, raw[i], x, li, 8 * li, 8 * li + 4, on);
-    } else {
+      const int64_t o = row_at(p, pl[i], head[i]), so = FMT == CF_E4M3 ? scale_at(p, pl[i], head[i]) : 0;
+      float2 x[4];
+      unpack8(k[i], x);
+      store_row<FMT, LPR>(p.c.k + o, p.c.ks + so, pl[i].ok, k[i], x, li, 8 * li, 8 * li + 4, on);
+      unpack8(v[i], x);
+      store_row<FMT, LPR>(p.c.v + o, p.c.vs + so, pl[i].ok, v[i], x, li, 8 * li, 8 * li + 4, on);
+    } else if (on && tok[i] >= 0) {
       if constexpr (FMT == CF_E4M3) {
-        const uint32_t w[2] = {raw[i].x, raw[i].y};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __half2_raw hr =
-              __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k / 2] >> (16 * (k & 1))), __NV_E4M3);
-          const float2 f = __half22float2(__half2(hr));
-          x[2 * k] = f.x * sc[i];
-          x[2 * k + 1] = f.y * sc[i];
-        }
-        raw[i] = pack8(x);
+        k[i] = e4m3x8_bf16(make_uint2(k[i].x, k[i].y), ks[i]);
+        v[i] = e4m3x8_bf16(make_uint2(v[i].x, v[i].y), vs[i]);
       }
-      if (on && tok[i] >= 0)
-        *reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((int64_t)tok[i] * p.Hkv + h) * p.D + 8 * li) = raw[i];
+      const int64_t o = ((int64_t)tok[i] * p.Hkv + head[i]) * p.D + 8 * li;
+      *reinterpret_cast<uint4*>(p.k_out + o) = k[i];
+      *reinterpret_cast<uint4*>(p.v_out + o) = v[i];
     }
   }
 }

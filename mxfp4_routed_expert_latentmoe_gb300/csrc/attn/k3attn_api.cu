@@ -140,40 +140,42 @@ QkvParams qkv_params(const k3attn_dims& d, int32_t T) {
 // lanes of a row: eight elements each
 int lanes_of(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
 
-// ROWS rows a thread, where that leaves every SM a block (a smaller call waits for latency:
-// its rows are spread out, one a thread)
-template <int FMT, bool WRITE, int ROWS>
+// ITEMS items a thread where that leaves every SM a block (a smaller call waits for latency:
+// its items are spread out, one a thread)
+template <int FMT, bool WRITE, int ITEMS>
 cudaError_t launch_rows_t(const QkvParams& p, int lpr, int64_t grid, cudaStream_t s) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch(lpr == 8 ? k3_rows_kernel<8, FMT, WRITE, ROWS>
-                         : (lpr == 16 ? k3_rows_kernel<16, FMT, WRITE, ROWS> : k3_rows_kernel<32, FMT, WRITE, ROWS>),
-                dim3((unsigned)grid), dim3(QKV_THREADS), 0, s, p);
+  return launch(lpr == 8 ? k3_rows_kernel<8, FMT, WRITE, ITEMS>
+                         : (lpr == 16 ? k3_rows_kernel<16, FMT, WRITE, ITEMS> : k3_rows_kernel<32, FMT, WRITE, ITEMS>),
+                dim3((unsigned)grid), dim3(256), 0, s, p);
 }
 template <int FMT, bool WRITE>
 cudaError_t launch_rows(QkvParams p, int sms, cudaStream_t s) {
+  constexpr int ITEMS = 2;
   const int lpr = lanes_of(p.D);
-  const int64_t rows = (int64_t)p.T * 2 * p.Hkv, per = QKV_THREADS / lpr;
-  p.by_rows = Divisor::of(2 * p.Hkv);
-  const int64_t grid = (rows + per * QKV_ROWS - 1) / (per * QKV_ROWS);
-  if (grid >= sms) return launch_rows_t<FMT, WRITE, QKV_ROWS>(p, lpr, grid, s);
-  return launch_rows_t<FMT, WRITE, 1>(p, lpr, (rows + per - 1) / per, s);
+  const int64_t items = (int64_t)p.T * p.Hkv, per = 256 / lpr;
+  p.by_rows = Divisor::of(p.Hkv);
+  const int64_t grid = (items + per * ITEMS - 1) / (per * ITEMS);
+  if (grid >= sms) return launch_rows_t<FMT, WRITE, ITEMS>(p, lpr, grid, s);
+  return launch_rows_t<FMT, WRITE, 1>(p, lpr, (items + per - 1) / per, s);
 }
 
-// The norms' blocks: as many tokens' rows as the threads take at ROWS each, or a balanced part
-// of one token's
+// The norms' blocks: the rows of as many tokens, or of a balanced part of one, as 256 threads
+// (a token that does not fit: 512) take at ROWS rows each, and just the threads for them
 template <int FMT, int ROWS>
 cudaError_t launch_norm_t(QkvParams p, int sms, cudaStream_t s) {
-  const int lpr = lanes_of(p.D), most = QKV_THREADS / lpr * ROWS;
-  const int rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2), parts = (rows + most - 1) / most;
+  const int lpr = lanes_of(p.D), rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2);
+  const int some = 256 / lpr * ROWS, most = QKV_THREADS / lpr * ROWS, parts = (rows + most - 1) / most;
   p.rows = (rows + parts - 1) / parts;
-  p.tokens = most / p.rows < QKV_TOKENS ? most / p.rows : QKV_TOKENS;
+  p.tokens = p.rows >= some ? 1 : (some / p.rows < QKV_TOKENS ? some / p.rows : QKV_TOKENS);
   p.by_rows = Divisor::of(p.rows);
   const dim3 grid((p.T + p.tokens - 1) / p.tokens, (rows + p.rows - 1) / p.rows);
   if constexpr (ROWS > 1)
     if ((int64_t)grid.x * grid.y < sms) return launch_norm_t<FMT, 1>(p, sms, s);
+  const int threads = ((p.rows * p.tokens + ROWS - 1) / ROWS * lpr + 31) / 32 * 32;
   return launch(lpr == 8 ? k3_norm_kernel<8, FMT, ROWS>
                          : (lpr == 16 ? k3_norm_kernel<16, FMT, ROWS> : k3_norm_kernel<32, FMT, ROWS>),
-                grid, dim3(QKV_THREADS), 0, s, p);
+                grid, dim3(threads), 0, s, p);
 }
 template <int FMT>
 cudaError_t launch_norm(const QkvParams& p, int sms, cudaStream_t s) {
