@@ -66,8 +66,8 @@ struct QkvParams {
   uint16_t *q_out, *k_out, *v_out;
   CacheView c;
   uint32_t* status;
-  int32_t tokens, rows;  // a block's tokens (norms), and rows of each
-  Divisor by_rows;       // by `rows`; the rows kernel's: by Hkv
+  int32_t tokens, rows, warps;  // norms: a block's tokens, rows of each and warps for each
+  Divisor by_heads;             // rows: by Hkv
 };
 
 constexpr int QKV_THREADS = 512;  // most threads of a block
@@ -143,99 +143,102 @@ K3_DEVI int64_t scale_at(const QkvParams& p, const Place& pl, int h) {
   return pl.page * p.c.spage + (h * p.c.shead + pl.at * p.c.stok);
 }
 
-// One row of the cache from its LPR lanes (a lane holds the four elements from ea and the four
-// from eb, `on` where they lie below D): `raw` is the row in bf16 (a row that came as bf16
-// keeps its bits), y in fp32.  All lanes of a warp call it; `keep`: whether the row is written.
-template <int FMT, int LPR>
-K3_DEVI void store_row(uint8_t* row, float* scale, bool keep, uint4 raw, const float2 (&y)[4], int li, int ea, int eb,
-                       bool on) {
-  if constexpr (FMT == CF_BF16) {
-    if (on && keep) {
-      *reinterpret_cast<uint2*>(row + 2 * ea) = make_uint2(raw.x, raw.y);
-      *reinterpret_cast<uint2*>(row + 2 * eb) = make_uint2(raw.z, raw.w);
-    }
-  } else {
-    // the largest magnitude by its bits, where infinities and NaN order above every number
-    uint32_t m = 0;
-    if (on)
+// The largest magnitude of a row by its bits, where infinities and NaN order above every number
+// (all lanes of a row get it): of fp32 values, of bf16 values (as an fp32's bits).
+template <int LPR>
+K3_DEVI uint32_t row_max(const float2 (&y)[4]) {
+  uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m = max(m, max(__float_as_uint(y[i].x) & 0x7FFFFFFFu, __float_as_uint(y[i].y) & 0x7FFFFFFFu));
+  for (int i = 0; i < 4; ++i)
+    m = max(m, max(__float_as_uint(y[i].x) & 0x7FFFFFFFu, __float_as_uint(y[i].y) & 0x7FFFFFFFu));
 #pragma unroll
-    for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float s = m < 0x7F800000u ? fmaxf(__uint_as_float(m) / E4M3_MAX, KV_MIN_SCALE) : __uint_as_float(0x7FC00000u);
-    const float inv = 1.0f / s;
-    float2 z[4];
+  for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  return m;
+}
+template <int LPR>
+K3_DEVI uint32_t row_max(uint4 raw) {
+  constexpr uint32_t ABS = 0x7FFF7FFFu;
+  uint32_t m = __vmaxu2(__vmaxu2(raw.x & ABS, raw.y & ABS), __vmaxu2(raw.z & ABS, raw.w & ABS));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], make_float2(inv, inv));
-    if (on && keep) {
-      const uint2 codes = e4m3x8(z);
-      *reinterpret_cast<uint32_t*>(row + ea) = codes.x;
-      *reinterpret_cast<uint32_t*>(row + eb) = codes.y;
-    }
-    if (li == 0 && keep) *scale = s;
-  }
+  for (int o = LPR / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  return max(m & 0xFFFF0000u, m << 16);
+}
+// a row's scale from its largest magnitude
+K3_DEVI float scale_of(uint32_t m) {
+  return m < 0x7F800000u ? fmaxf(__uint_as_float(m) / E4M3_MAX, KV_MIN_SCALE) : __uint_as_float(0x7FC00000u);
+}
+// a lane's eight codes of a row, given the inverse of its scale
+K3_DEVI uint2 codes_of(const float2 (&y)[4], float inv) {
+  float2 z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], make_float2(inv, inv));
+  return e4m3x8(z);
 }
 
 // Norms and rotation (FMT none), with the cache's rows in the same pass (FMT bf16, E4M3): a
-// block has p.rows rows of each of p.tokens tokens, LPR lanes a row and up to ROWS rows a
-// thread.  A lane holds two pieces of four elements of a row: the two halves of four rotated
-// pairs (pairs (i, i + R/2)), or eight neighbours, so that pairs never cross lanes.  Its pieces
-// are the same in all its rows: the products of weights and angles stay in registers, formed
-// anew where the kind of row or the token changes, and a row takes 12 packed operations for its
-// norm and rotation.  The angles (fp64 products and one sine and cosine per token and pair) are
-// shared by the block.
+// block has p.rows rows of each of p.tokens tokens, p.warps warps a token, LPR lanes a row and
+// up to ROWS rows a thread.  A lane holds two pieces of four elements of a row: the two halves
+// of four rotated pairs (pairs (i, i + R/2)), or eight neighbours, so that pairs never cross
+// lanes.  Its pieces are the same in all its rows: the products of weights and angles stay in
+// registers, formed anew where queries give way to keys, and a row takes 12 packed operations
+// for its norm and rotation.  The angles (fp64 products and one sine and cosine per token and
+// pair) are shared by the block.
 template <int LPR, int FMT, int ROWS>
 __global__ void __launch_bounds__(QKV_THREADS, 2) k3_norm_kernel(const QkvParams p) {
   __shared__ __align__(16) float s_cos[QKV_TOKENS][128], s_sin[QKV_TOKENS][128];
-  const int subs = blockDim.x / LPR;
-  const int li = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, group = warp / p.warps;
+  const int li = lane % LPR, sub = (warp - group * p.warps) * (32 / LPR) + lane / LPR, subs = p.warps * (32 / LPR);
   const int t0 = blockIdx.x * p.tokens, r0 = blockIdx.y * p.rows;
-  const int nt = min(p.tokens, p.T - t0), nr = min(p.rows, p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2) - r0);
+  const int nt = min(p.tokens, p.T - t0);
+  const bool mine = group < nt;  // this warp's token: there is one
+  const int64_t t = t0 + (mine ? group : 0);
+  const int r1 = mine ? min(r0 + p.rows, p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2)) : 0;
   const bool on = 8 * li < p.D, rotated = 8 * li < p.R;
-  const int half = p.R / 2;
+  const int half = p.R / 2, k0 = p.Hq, v0 = p.Hq + p.Hkv;
   // this lane's pieces and their first angle
   int ea = 8 * li, eb = ea + 4, angle = ea / 2;
   if (!p.inter && rotated) {
     ea = angle = 4 * li;
     eb = ea + half;
   }
+  // where row 0 would be, were all rows of its kind
+  const uint16_t* const qs = p.q + t * p.q_stride;
+  const uint16_t* const ks = p.k + t * p.k_stride - k0 * p.D;
+  const uint16_t* const vs = p.v + t * p.v_stride - v0 * p.D;
   grid_dep_wait();
   grid_dep_launch();
   uint2 ra[ROWS], rb[ROWS];
-  int tok[ROWS], row[ROWS];
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int it = sub + i * subs;
-    tok[i] = p.tokens == 1 ? (it < nr ? 0 : 1) : (int)p.by_rows(it);
-    row[i] = r0 + it - tok[i] * p.rows;
+    const int r = r0 + sub + i * subs;
     ra[i] = rb[i] = make_uint2(0, 0);
-    if (tok[i] < nt && on) {
-      const int64_t t = t0 + tok[i];
-      const int r = row[i];
-      const uint16_t* src = r < p.Hq ? p.q + t * p.q_stride + r * p.D
-                            : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (r - p.Hq) * p.D
-                                               : p.v + t * p.v_stride + (r - p.Hq - p.Hkv) * p.D;
+    if (r < r1 && on) {
+      const uint16_t* src = (r < k0 ? qs : (FMT == CF_NONE || r < v0 ? ks : vs)) + r * p.D;
       ra[i] = *reinterpret_cast<const uint2*>(src + ea);
       rb[i] = *reinterpret_cast<const uint2*>(src + eb);
     }
   }
   for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int t = i / half, j = i - t * half;
-    rotation(p.pos[t0 + t], p.inv_freq[j], s_cos[t][j], s_sin[t][j]);
+    const int g = i / half, j = i - g * half;
+    rotation(p.pos[t0 + g], p.inv_freq[j], s_cos[g][j], s_sin[g][j]);
+  }
+  Place pl{0, 0, false};
+  if constexpr (FMT != CF_NONE) {
+    if (r1 > v0 - p.Hkv) pl = place_of(p, p.slots[t], lane == 0);
   }
   __syncthreads();
   const float over_d = 1.0f / (float)p.D;
+  uint16_t* const qd = p.q_out + t * p.Hq * p.D;
+  uint16_t* const kd = p.k_out + (t * p.Hkv - k0) * p.D;
   // y = x * co + z * si, z the other element of x's pair; without rotation co is the weight alone
   float2 co[4] = {}, si[4] = {};
-  int have_tok = -1, have_w = -1;
+  int have = -1;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const bool there = tok[i] < nt;
+    const int r = r0 + sub + i * subs;
+    const bool there = r < r1;
     if (!__any_sync(0xFFFFFFFFu, there)) break;
-    const int r = row[i];
-    const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
-    const int h = is_q ? r : (is_v ? r - p.Hq - p.Hkv : r - p.Hq);
+    const bool is_q = r < k0, is_v = FMT != CF_NONE && r >= v0;
     uint4 raw = make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y);
     float2 x[4];
     unpack8(raw, x);
@@ -246,9 +249,8 @@ __global__ void __launch_bounds__(QKV_THREADS, 2) k3_norm_kernel(const QkvParams
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     if (!is_v) {
-      if (on && there && (have_w != (int)is_q || have_tok != tok[i])) {
-        have_w = is_q;
-        have_tok = tok[i];
+      if (on && there && have != (int)is_q) {
+        have = is_q;
         const float* w = is_q ? p.q_w : p.k_w;
         const float4 wa = __ldg(reinterpret_cast<const float4*>(w + ea));
         const float4 wb = __ldg(reinterpret_cast<const float4*>(w + eb));
@@ -257,8 +259,8 @@ __global__ void __launch_bounds__(QKV_THREADS, 2) k3_norm_kernel(const QkvParams
         co[2] = make_float2(wb.x, wb.y);
         co[3] = make_float2(wb.z, wb.w);
         if (rotated) {
-          const float4 c = *reinterpret_cast<const float4*>(&s_cos[have_tok][angle]);
-          const float4 s = *reinterpret_cast<const float4*>(&s_sin[have_tok][angle]);
+          const float4 c = *reinterpret_cast<const float4*>(&s_cos[group][angle]);
+          const float4 s = *reinterpret_cast<const float4*>(&s_sin[group][angle]);
           if (p.inter) {  // pairs are (x, y) of each of the four
             const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
@@ -293,20 +295,30 @@ __global__ void __launch_bounds__(QKV_THREADS, 2) k3_norm_kernel(const QkvParams
       }
       raw = pack8(x);
     }
-    const int64_t t = t0 + tok[i];
-    if (there && on && !is_v) {
-      uint16_t* dst = is_q ? p.q_out + (t * p.Hq + h) * p.D : (p.k_out ? p.k_out + (t * p.Hkv + h) * p.D : nullptr);
-      if (dst) {
-        *reinterpret_cast<uint2*>(dst + ea) = make_uint2(raw.x, raw.y);
-        *reinterpret_cast<uint2*>(dst + eb) = make_uint2(raw.z, raw.w);
-      }
+    if (there && on && !is_v && (is_q || p.k_out)) {
+      uint16_t* dst = (is_q ? qd : kd) + r * p.D;
+      *reinterpret_cast<uint2*>(dst + ea) = make_uint2(raw.x, raw.y);
+      *reinterpret_cast<uint2*>(dst + eb) = make_uint2(raw.z, raw.w);
     }
     if constexpr (FMT != CF_NONE) {
-      const bool cached = there && !is_q;
-      if (__any_sync(0xFFFFFFFFu, cached)) {
-        const Place pl = place_of(p, cached ? p.slots[t] : -1, li == 0);
-        store_row<FMT, LPR>((is_v ? p.c.v : p.c.k) + row_at(p, pl, h), (is_v ? p.c.vs : p.c.ks) + scale_at(p, pl, h),
-                            cached && pl.ok, raw, x, li, ea, eb, on);
+      if (__any_sync(0xFFFFFFFFu, there && !is_q)) {
+        const int h = r - (is_v ? v0 : k0);
+        const bool keep = there && !is_q && pl.ok;
+        uint8_t* to = (is_v ? p.c.v : p.c.k) + row_at(p, pl, h);
+        if constexpr (FMT == CF_BF16) {
+          if (keep && on) {
+            *reinterpret_cast<uint2*>(to + 2 * ea) = make_uint2(raw.x, raw.y);
+            *reinterpret_cast<uint2*>(to + 2 * eb) = make_uint2(raw.z, raw.w);
+          }
+        } else {
+          const float s = scale_of(row_max<LPR>(x));
+          const uint2 codes = codes_of(x, 1.0f / s);
+          if (keep && on) {
+            *reinterpret_cast<uint32_t*>(to + ea) = codes.x;
+            *reinterpret_cast<uint32_t*>(to + eb) = codes.y;
+          }
+          if (keep && li == 0) (is_v ? p.c.vs : p.c.ks)[scale_at(p, pl, h)] = s;
+        }
       }
     }
   }
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(256) k3_rows_kernel(const QkvParams p) {
   int32_t tok[ITEMS], head[ITEMS], slot[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int32_t it = rest + sub + i * SUBS, dt = (int32_t)p.by_rows(it);
+    const int32_t it = rest + sub + i * SUBS, dt = (int32_t)p.by_heads(it);
     head[i] = it - dt * p.Hkv;
     tok[i] = dt < p.T - t0 ? t0 + dt : -1;
     slot[i] = tok[i] >= 0 ? p.slots[tok[i]] : -1;
@@ -363,12 +375,29 @@ __global__ void __launch_bounds__(256) k3_rows_kernel(const QkvParams p) {
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     if constexpr (WRITE) {
-      const int64_t o = row_at(p, pl[i], head[i]), so = FMT == CF_E4M3 ? scale_at(p, pl[i], head[i]) : 0;
-      float2 x[4];
-      unpack8(k[i], x);
-      store_row<FMT, LPR>(p.c.k + o, p.c.ks + so, pl[i].ok, k[i], x, li, 8 * li, 8 * li + 4, on);
-      unpack8(v[i], x);
-      store_row<FMT, LPR>(p.c.v + o, p.c.vs + so, pl[i].ok, v[i], x, li, 8 * li, 8 * li + 4, on);
+      const int64_t o = row_at(p, pl[i], head[i]);
+      if constexpr (FMT == CF_BF16) {
+        if (on && pl[i].ok) {
+          *reinterpret_cast<uint4*>(p.c.k + o + 16 * li) = k[i];
+          *reinterpret_cast<uint4*>(p.c.v + o + 16 * li) = v[i];
+        }
+      } else {
+        // even lanes form the key's scale and inverse, odd ones the value's, and trade them
+        const uint32_t mk = row_max<LPR>(k[i]), mv = row_max<LPR>(v[i]);
+        const bool odd = li & 1;
+        const float s = scale_of(odd ? mv : mk), inv = 1.0f / s;
+        const float inv1 = __shfl_xor_sync(0xFFFFFFFFu, inv, 1);
+        float2 x[4];
+        unpack8(k[i], x);
+        const uint2 kc = codes_of(x, odd ? inv1 : inv);
+        unpack8(v[i], x);
+        const uint2 vc = codes_of(x, odd ? inv : inv1);
+        if (on && pl[i].ok) {
+          *reinterpret_cast<uint2*>(p.c.k + o + 8 * li) = kc;
+          *reinterpret_cast<uint2*>(p.c.v + o + 8 * li) = vc;
+          if (li < 2) (odd ? p.c.vs : p.c.ks)[scale_at(p, pl[i], head[i])] = s;
+        }
+      }
     } else if (on && tok[i] >= 0) {
       if constexpr (FMT == CF_E4M3) {
         k[i] = e4m3x8_bf16(make_uint2(k[i].x, k[i].y), ks[i]);

@@ -154,28 +154,29 @@ cudaError_t launch_rows(QkvParams p, int sms, cudaStream_t s) {
   constexpr int ITEMS = 2;
   const int lpr = lanes_of(p.D);
   const int64_t items = (int64_t)p.T * p.Hkv, per = 256 / lpr;
-  p.by_rows = Divisor::of(p.Hkv);
+  p.by_heads = Divisor::of(p.Hkv);
   const int64_t grid = (items + per * ITEMS - 1) / (per * ITEMS);
   if (grid >= sms) return launch_rows_t<FMT, WRITE, ITEMS>(p, lpr, grid, s);
   return launch_rows_t<FMT, WRITE, 1>(p, lpr, (items + per - 1) / per, s);
 }
 
-// The norms' blocks: the rows of as many tokens, or of a balanced part of one, as 256 threads
-// (a token that does not fit: 512) take at ROWS rows each, and just the threads for them
+// The norms' blocks: ROWS rows a thread and just the warps that a token's rows take so; a token
+// that takes more than a block has is cut into balanced parts, tokens of few rows share a block
+// of up to 8 warps
 template <int FMT, int ROWS>
 cudaError_t launch_norm_t(QkvParams p, int sms, cudaStream_t s) {
   const int lpr = lanes_of(p.D), rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2);
-  const int some = 256 / lpr * ROWS, most = QKV_THREADS / lpr * ROWS, parts = (rows + most - 1) / most;
+  const int a_warp = 32 / lpr * ROWS, most = QKV_THREADS / 32 * a_warp, parts = (rows + most - 1) / most;
   p.rows = (rows + parts - 1) / parts;
-  p.tokens = p.rows >= some ? 1 : (some / p.rows < QKV_TOKENS ? some / p.rows : QKV_TOKENS);
-  p.by_rows = Divisor::of(p.rows);
+  p.warps = (p.rows + a_warp - 1) / a_warp;
+  p.tokens = p.warps > 4 ? 1 : 8 / p.warps;
+  if (p.tokens > p.T) p.tokens = p.T;
   const dim3 grid((p.T + p.tokens - 1) / p.tokens, (rows + p.rows - 1) / p.rows);
   if constexpr (ROWS > 1)
     if ((int64_t)grid.x * grid.y < sms) return launch_norm_t<FMT, 1>(p, sms, s);
-  const int threads = ((p.rows * p.tokens + ROWS - 1) / ROWS * lpr + 31) / 32 * 32;
   return launch(lpr == 8 ? k3_norm_kernel<8, FMT, ROWS>
                          : (lpr == 16 ? k3_norm_kernel<16, FMT, ROWS> : k3_norm_kernel<32, FMT, ROWS>),
-                grid, dim3(threads), 0, s, p);
+                grid, dim3(32 * p.warps * p.tokens), 0, s, p);
 }
 template <int FMT>
 cudaError_t launch_norm(const QkvParams& p, int sms, cudaStream_t s) {
