@@ -66,13 +66,18 @@ struct QkvParams {
   uint16_t *q_out, *k_out, *v_out;
   CacheView c;
   uint32_t* status;
-  int32_t tokens, rows, warps;  // norms: a block's tokens, rows of each and warps for each
-  Divisor by_heads;             // rows: by Hkv
+  int32_t tokens, rows, parts;             // norms: a block's tokens, rows of each, blocks for them all
+  int32_t kv_blocks, kv_tokens, kv_warps;  // the keys' and values' blocks, their tokens, warps of each
+  Divisor by_heads;                        // rows: by Hkv
 };
 
 constexpr int QKV_THREADS = 512;  // most threads of a block
 constexpr int QKV_ROWS = 4;       // rows of a thread in flight
 constexpr int QKV_TOKENS = 8;     // most tokens of a block of the norms
+// Registers of the norm kernel: warps in flight count for more than the few spilled words
+// (16381 tokens of 72 heads of 128: 111 us at 56 registers, 121 at 64, 114 at 52; the append of
+// 8192 tokens to an E4M3 cache: 69 us at 64, 75 at 56, 78 at 72).  One row a thread: all it asks.
+constexpr int qkv_registers(int fmt, int rows) { return rows == 1 ? 128 : (fmt == CF_NONE ? 56 : 64); }
 constexpr float E4M3_MAX = 448.0f;
 constexpr float KV_MIN_SCALE = 0x1p-100f;  // its reciprocal and 448 times it are normal numbers
 
@@ -167,6 +172,15 @@ K3_DEVI uint32_t row_max(uint4 raw) {
 K3_DEVI float scale_of(uint32_t m) {
   return m < 0x7F800000u ? fmaxf(__uint_as_float(m) / E4M3_MAX, KV_MIN_SCALE) : __uint_as_float(0x7FC00000u);
 }
+// The scales of a key's and a value's row, and their inverses: even lanes form the key's, odd
+// ones the value's (s: the lane's own), and trade the inverses.
+K3_DEVI void scales_of(uint32_t mk, uint32_t mv, int li, float& s, float& ik, float& iv) {
+  const bool odd = li & 1;
+  s = scale_of(odd ? mv : mk);
+  const float own = 1.0f / s, other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+  ik = odd ? other : own;
+  iv = odd ? own : other;
+}
 // a lane's eight codes of a row, given the inverse of its scale
 K3_DEVI uint2 codes_of(const float2 (&y)[4], float inv) {
   float2 z[4];
@@ -175,151 +189,236 @@ K3_DEVI uint2 codes_of(const float2 (&y)[4], float inv) {
   return e4m3x8(z);
 }
 
-// Norms and rotation (FMT none), with the cache's rows in the same pass (FMT bf16, E4M3): a
-// block has p.rows rows of each of p.tokens tokens, p.warps warps a token, LPR lanes a row and
-// up to ROWS rows a thread.  A lane holds two pieces of four elements of a row: the two halves
-// of four rotated pairs (pairs (i, i + R/2)), or eight neighbours, so that pairs never cross
-// lanes.  Its pieces are the same in all its rows: the products of weights and angles stay in
-// registers, formed anew where queries give way to keys, and a row takes 12 packed operations
-// for its norm and rotation.  The angles (fp64 products and one sine and cosine per token and
-// pair) are shared by the block.
-template <int LPR, int FMT, int ROWS>
-__global__ void __launch_bounds__(QKV_THREADS, 2) k3_norm_kernel(const QkvParams p) {
-  __shared__ __align__(16) float s_cos[QKV_TOKENS][128], s_sin[QKV_TOKENS][128];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, group = warp / p.warps;
-  const int li = lane % LPR, sub = (warp - group * p.warps) * (32 / LPR) + lane / LPR, subs = p.warps * (32 / LPR);
-  const int t0 = blockIdx.x * p.tokens, r0 = blockIdx.y * p.rows;
-  const int nt = min(p.tokens, p.T - t0);
-  const bool mine = group < nt;  // this warp's token: there is one
-  const int64_t t = t0 + (mine ? group : 0);
-  const int r1 = mine ? min(r0 + p.rows, p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2)) : 0;
-  const bool on = 8 * li < p.D, rotated = 8 * li < p.R;
-  const int half = p.R / 2, k0 = p.Hq, v0 = p.Hq + p.Hkv;
-  // this lane's pieces and their first angle
-  int ea = 8 * li, eb = ea + 4, angle = ea / 2;
-  if (!p.inter && rotated) {
-    ea = angle = 4 * li;
-    eb = ea + half;
-  }
-  // where row 0 would be, were all rows of its kind
-  const uint16_t* const qs = p.q + t * p.q_stride;
-  const uint16_t* const ks = p.k + t * p.k_stride - k0 * p.D;
-  const uint16_t* const vs = p.v + t * p.v_stride - v0 * p.D;
-  grid_dep_wait();
-  grid_dep_launch();
-  uint2 ra[ROWS], rb[ROWS];
+// What a lane multiplies its pieces of normed rows of one kind (queries or keys) of one token by:
+// y = x * co + z * si, z the other element of x's pair; without rotation co is the weight alone.
+struct Turn {
+  float2 co[4], si[4];
+  // the pieces of four elements at ea and eb; c, s: cos and sin from this lane's first angle
+  K3_DEVI void form(const QkvParams& p, const float* w, int ea, int eb, bool rotated, const float* cp,
+                    const float* sp) {
+    const float4 wa = __ldg(reinterpret_cast<const float4*>(w + ea));
+    const float4 wb = __ldg(reinterpret_cast<const float4*>(w + eb));
+    co[0] = make_float2(wa.x, wa.y);
+    co[1] = make_float2(wa.z, wa.w);
+    co[2] = make_float2(wb.x, wb.y);
+    co[3] = make_float2(wb.z, wb.w);
+    if (!rotated) return;
+    const float4 c = *reinterpret_cast<const float4*>(cp), s = *reinterpret_cast<const float4*>(sp);
+    if (p.inter) {  // pairs are (x, y) of each of the four
+      const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int r = r0 + sub + i * subs;
-    ra[i] = rb[i] = make_uint2(0, 0);
-    if (r < r1 && on) {
-      const uint16_t* src = (r < k0 ? qs : (FMT == CF_NONE || r < v0 ? ks : vs)) + r * p.D;
-      ra[i] = *reinterpret_cast<const uint2*>(src + ea);
-      rb[i] = *reinterpret_cast<const uint2*>(src + eb);
+      for (int k = 0; k < 4; ++k) {
+        si[k] = make_float2(-co[k].y * sn[k], co[k].x * sn[k]);
+        co[k] = mul2(co[k], make_float2(cc[k], cc[k]));
+      }
+    } else {  // 0 with 2, 1 with 3
+      si[0] = make_float2(-co[2].x * s.x, -co[2].y * s.y);
+      si[1] = make_float2(-co[3].x * s.z, -co[3].y * s.w);
+      si[2] = mul2(co[0], make_float2(s.x, s.y));
+      si[3] = mul2(co[1], make_float2(s.z, s.w));
+      const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
+      co[0] = mul2(co[0], c0);
+      co[1] = mul2(co[1], c1);
+      co[2] = mul2(co[2], c0);
+      co[3] = mul2(co[3], c1);
     }
   }
-  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int g = i / half, j = i - g * half;
-    rotation(p.pos[t0 + g], p.inv_freq[j], s_cos[g][j], s_sin[g][j]);
-  }
-  Place pl{0, 0, false};
-  if constexpr (FMT != CF_NONE) {
-    if (r1 > v0 - p.Hkv) pl = place_of(p, p.slots[t], lane == 0);
-  }
-  __syncthreads();
-  const float over_d = 1.0f / (float)p.D;
-  uint16_t* const qd = p.q_out + t * p.Hq * p.D;
-  uint16_t* const kd = p.k_out + (t * p.Hkv - k0) * p.D;
-  // y = x * co + z * si, z the other element of x's pair; without rotation co is the weight alone
-  float2 co[4] = {}, si[4] = {};
-  int have = -1;
+  K3_DEVI void with(const QkvParams& p, bool rotated, float2 (&x)[4], float2 z0, float2 z1, float2 z2,
+                    float2 z3) const {
+    const float2 z[4] = {z0, z1, z2, z3};
+    float2 y[4];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int r = r0 + sub + i * subs;
-    const bool there = r < r1;
-    if (!__any_sync(0xFFFFFFFFu, there)) break;
-    const bool is_q = r < k0, is_v = FMT != CF_NONE && r >= v0;
-    uint4 raw = make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y);
-    float2 x[4];
-    unpack8(raw, x);
+    for (int k = 0; k < 4; ++k) y[k] = mul2(x[k], co[k]);
+    if (p.R == p.D || rotated)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = fma2(z[k], si[k], y[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = y[k];
+  }
+  // x: a row's pieces -> normed and rotated (all lanes of a warp call it: the sum over the row)
+  template <int LPR>
+  K3_DEVI void apply(const QkvParams& p, float over_d, bool rotated, float2 (&x)[4]) const {
     float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
     for (int k = 1; k < 4; ++k) s2 = fma2(x[k], x[k], s2);
     float ss = s2.x + s2.y;
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    if (!is_v) {
-      if (on && there && have != (int)is_q) {
-        have = is_q;
-        const float* w = is_q ? p.q_w : p.k_w;
-        const float4 wa = __ldg(reinterpret_cast<const float4*>(w + ea));
-        const float4 wb = __ldg(reinterpret_cast<const float4*>(w + eb));
-        co[0] = make_float2(wa.x, wa.y);
-        co[1] = make_float2(wa.z, wa.w);
-        co[2] = make_float2(wb.x, wb.y);
-        co[3] = make_float2(wb.z, wb.w);
-        if (rotated) {
-          const float4 c = *reinterpret_cast<const float4*>(&s_cos[group][angle]);
-          const float4 s = *reinterpret_cast<const float4*>(&s_sin[group][angle]);
-          if (p.inter) {  // pairs are (x, y) of each of the four
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+    const float rs = rsqrtf(ss * over_d + p.eps);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              si[k] = make_float2(-co[k].y * sn[k], co[k].x * sn[k]);
-              co[k] = mul2(co[k], make_float2(cc[k], cc[k]));
-            }
-          } else {  // 0 with 2, 1 with 3
-            si[0] = make_float2(-co[2].x * s.x, -co[2].y * s.y);
-            si[1] = make_float2(-co[3].x * s.z, -co[3].y * s.w);
-            si[2] = mul2(co[0], make_float2(s.x, s.y));
-            si[3] = mul2(co[1], make_float2(s.z, s.w));
-            const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
-            co[0] = mul2(co[0], c0);
-            co[1] = mul2(co[1], c1);
-            co[2] = mul2(co[2], c0);
-            co[3] = mul2(co[3], c1);
-          }
+    for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], make_float2(rs, rs));
+    if (p.inter)
+      with(p, rotated, x, make_float2(x[0].y, x[0].x), make_float2(x[1].y, x[1].x), make_float2(x[2].y, x[2].x),
+           make_float2(x[3].y, x[3].x));
+    else
+      with(p, rotated, x, x[2], x[3], x[0], x[1]);
+  }
+};
+
+// A lane's pieces of a row of queries or keys, four elements from ea and four from eb, and its
+// first angle: the two halves of four rotated pairs (pairs (i, i + R/2)), or eight neighbours,
+// so that pairs never cross lanes.
+struct Pieces {
+  int ea, eb, angle;
+  bool on, rotated;
+  K3_DEVI Pieces(const QkvParams& p, int li) {
+    on = 8 * li < p.D;
+    rotated = 8 * li < p.R;
+    ea = 8 * li;
+    eb = ea + 4;
+    angle = ea / 2;
+    if (!p.inter && rotated) {
+      ea = angle = 4 * li;
+      eb = ea + p.R / 2;
+    }
+  }
+};
+
+// Norms and rotation of dense rows (queries and, FMT none, keys), and with FMT bf16 or E4M3 the
+// keys and values of the same tokens into the cache in the same launch: the first p.kv_blocks
+// blocks take those, a head's key and value together.
+//
+// A block of the dense rows has p.rows rows of each of p.tokens tokens, LPR lanes a row and up
+// to ROWS rows a thread, whose loads it issues before it forms the token's angles (fp64 products
+// and one sine and cosine per token and pair, shared by the block).  A thread's pieces are the
+// same in all its rows, so that it keeps the products of weights and angles in registers and a
+// row takes 12 packed operations for its norm and rotation.
+template <int LPR, int FMT, int ROWS>
+__global__ void __maxnreg__(qkv_registers(FMT, ROWS)) k3_norm_kernel(const QkvParams p) {
+  __shared__ __align__(16) float s_cos[QKV_TOKENS][128], s_sin[QKV_TOKENS][128];
+  const int half = p.R / 2;
+  const float over_d = 1.0f / (float)p.D;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  if (FMT != CF_NONE && (int)blockIdx.x < p.kv_blocks) {
+    constexpr int ITEMS = ROWS > 1 ? 2 : 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, group = warp / p.kv_warps;
+    const int li = lane % LPR, sub = (warp - group * p.kv_warps) * (32 / LPR) + lane / LPR;
+    const int subs = p.kv_warps * (32 / LPR);
+    const int t0 = blockIdx.x * p.kv_tokens, nt = min(p.kv_tokens, p.T - t0);
+    const bool mine = group < nt;
+    const int64_t t = t0 + (mine ? group : 0);
+    const Pieces pc(p, li);
+    const int32_t slot = mine ? p.slots[t] : -1;
+    const uint16_t *kp = p.k + t * p.k_stride, *vp = p.v + t * p.v_stride;
+    uint2 ra[ITEMS], rb[ITEMS];
+    uint4 rv[ITEMS];
+    auto load = [&](int first) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int h = first + i * subs;
+        ra[i] = rb[i] = make_uint2(0, 0);
+        rv[i] = make_uint4(0, 0, 0, 0);
+        if (mine && h < p.Hkv && pc.on) {
+          ra[i] = *reinterpret_cast<const uint2*>(kp + h * p.D + pc.ea);
+          rb[i] = *reinterpret_cast<const uint2*>(kp + h * p.D + pc.eb);
+          rv[i] = *reinterpret_cast<const uint4*>(vp + h * p.D + 8 * li);
         }
       }
-      const float rs = rsqrtf(ss * over_d + p.eps);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], make_float2(rs, rs));
-      float2 z[4] = {x[2], x[3], x[0], x[1]};
-      if (p.inter)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[k] = make_float2(x[k].y, x[k].x);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[k] = mul2(x[k], co[k]);
-        if (rotated) x[k] = fma2(z[k], si[k], x[k]);
-      }
-      raw = pack8(x);
+    };
+    load(sub);
+    for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+      const int g = i / half, j = i - g * half;
+      rotation(p.pos[t0 + g], p.inv_freq[j], s_cos[g][j], s_sin[g][j]);
     }
-    if (there && on && !is_v && (is_q || p.k_out)) {
-      uint16_t* dst = (is_q ? qd : kd) + r * p.D;
-      *reinterpret_cast<uint2*>(dst + ea) = make_uint2(raw.x, raw.y);
-      *reinterpret_cast<uint2*>(dst + eb) = make_uint2(raw.z, raw.w);
-    }
-    if constexpr (FMT != CF_NONE) {
-      if (__any_sync(0xFFFFFFFFu, there && !is_q)) {
-        const int h = r - (is_v ? v0 : k0);
-        const bool keep = there && !is_q && pl.ok;
-        uint8_t* to = (is_v ? p.c.v : p.c.k) + row_at(p, pl, h);
+    const Place pl = place_of(p, slot, sub == 0 && li == 0);
+    const int64_t row0 = row_at(p, pl, 0), scale0 = FMT == CF_E4M3 ? scale_at(p, pl, 0) : 0;
+    __syncthreads();
+    if (!mine) return;  // the whole warp
+    Turn turn{};
+    if (pc.on)
+      turn.form(p, p.k_w, pc.ea, pc.eb, pc.rotated, &s_cos[group][pc.angle], &s_sin[group][pc.angle]);
+    for (int first = 0; first < p.Hkv; first += ITEMS * subs) {  // (of the whole warp)
+      if (first > 0) load(first + sub);
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int h = first + sub + i * subs;
+        if (first + i * subs >= p.Hkv) break;
+        const bool keep = h < p.Hkv && pc.on;
+        float2 x[4];
+        unpack8(make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y), x);
+        turn.template apply<LPR>(p, over_d, pc.rotated, x);
+        const uint4 kb = pack8(x);
+        if (keep && p.k_out) {
+          uint16_t* dst = p.k_out + (t * p.Hkv + h) * p.D;
+          *reinterpret_cast<uint2*>(dst + pc.ea) = make_uint2(kb.x, kb.y);
+          *reinterpret_cast<uint2*>(dst + pc.eb) = make_uint2(kb.z, kb.w);
+        }
+        const int64_t row = row0 + h * p.c.head;
         if constexpr (FMT == CF_BF16) {
-          if (keep && on) {
-            *reinterpret_cast<uint2*>(to + 2 * ea) = make_uint2(raw.x, raw.y);
-            *reinterpret_cast<uint2*>(to + 2 * eb) = make_uint2(raw.z, raw.w);
+          if (keep && pl.ok) {
+            *reinterpret_cast<uint2*>(p.c.k + row + 2 * pc.ea) = make_uint2(kb.x, kb.y);
+            *reinterpret_cast<uint2*>(p.c.k + row + 2 * pc.eb) = make_uint2(kb.z, kb.w);
+            *reinterpret_cast<uint4*>(p.c.v + row + 16 * li) = rv[i];
           }
         } else {
-          const float s = scale_of(row_max<LPR>(x));
-          const uint2 codes = codes_of(x, 1.0f / s);
-          if (keep && on) {
-            *reinterpret_cast<uint32_t*>(to + ea) = codes.x;
-            *reinterpret_cast<uint32_t*>(to + eb) = codes.y;
+          float s, ik, iv;
+          scales_of(row_max<LPR>(x), row_max<LPR>(rv[i]), li, s, ik, iv);
+          const uint2 kc = codes_of(x, ik);
+          unpack8(rv[i], x);
+          const uint2 vc = codes_of(x, iv);
+          if (keep && pl.ok) {
+            *reinterpret_cast<uint32_t*>(p.c.k + row + pc.ea) = kc.x;
+            *reinterpret_cast<uint32_t*>(p.c.k + row + pc.eb) = kc.y;
+            *reinterpret_cast<uint2*>(p.c.v + row + 8 * li) = vc;
+            if (li < 2) (li ? p.c.vs : p.c.ks)[scale0 + h * p.c.shead] = s;
           }
-          if (keep && li == 0) (is_v ? p.c.vs : p.c.ks)[scale_at(p, pl, h)] = s;
         }
       }
+    }
+    return;
+  }
+
+  const int block = FMT == CF_NONE ? blockIdx.x : blockIdx.x - p.kv_blocks;
+  const int tb = block / p.parts, part = block - tb * p.parts;
+  const int warps = blockDim.x / 32 / p.tokens, warp = threadIdx.x / 32, group = warp / warps;
+  const int lane = threadIdx.x % 32, li = lane % LPR;
+  const int sub = (warp - group * warps) * (32 / LPR) + lane / LPR, subs = warps * (32 / LPR);
+  const int t0 = tb * p.tokens, r0 = part * p.rows, nt = min(p.tokens, p.T - t0);
+  const bool mine = group < nt;  // this warp's token: there is one
+  const int64_t t = t0 + (mine ? group : 0);
+  const int r1 = mine ? min(r0 + p.rows, p.Hq + (FMT == CF_NONE ? p.Hkv : 0)) : 0;
+  const Pieces pc(p, li);
+  // where row 0 would be, were all rows of its kind
+  const uint16_t* const qs = p.q + t * p.q_stride;
+  const uint16_t* const ks = p.k + t * p.k_stride - p.Hq * p.D;
+  uint2 ra[ROWS], rb[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + sub + i * subs;
+    ra[i] = rb[i] = make_uint2(0, 0);
+    if (r < r1 && pc.on) {
+      const uint16_t* src = (FMT != CF_NONE || r < p.Hq ? qs : ks) + r * p.D;
+      ra[i] = *reinterpret_cast<const uint2*>(src + pc.ea);
+      rb[i] = *reinterpret_cast<const uint2*>(src + pc.eb);
+    }
+  }
+  if (mine)
+    for (int i = threadIdx.x - 32 * group * warps; i < half; i += 32 * warps)
+      rotation(p.pos[t], p.inv_freq[i], s_cos[group][i], s_sin[group][i]);
+  __syncthreads();
+  uint16_t* const qd = p.q_out + t * p.Hq * p.D;
+  uint16_t* const kd = p.k_out + (t * p.Hkv - p.Hq) * p.D;
+  Turn turn{};
+  int have = -1;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + sub + i * subs;
+    const bool there = r < r1 && pc.on, is_q = FMT != CF_NONE || r < p.Hq;
+    if (!__any_sync(0xFFFFFFFFu, there)) break;
+    if (there && have != (int)is_q) {
+      have = is_q;
+      turn.form(p, is_q ? p.q_w : p.k_w, pc.ea, pc.eb, pc.rotated, &s_cos[group][pc.angle], &s_sin[group][pc.angle]);
+    }
+    float2 x[4];
+    unpack8(make_uint4(ra[i].x, ra[i].y, rb[i].x, rb[i].y), x);
+    turn.template apply<LPR>(p, over_d, pc.rotated, x);
+    if (there) {
+      const uint4 raw = pack8(x);
+      uint16_t* dst = (is_q ? qd : kd) + r * p.D;
+      *reinterpret_cast<uint2*>(dst + pc.ea) = make_uint2(raw.x, raw.y);
+      *reinterpret_cast<uint2*>(dst + pc.eb) = make_uint2(raw.z, raw.w);
     }
   }
 }
@@ -382,20 +481,17 @@ __global__ void __launch_bounds__(256) k3_rows_kernel(const QkvParams p) {
           *reinterpret_cast<uint4*>(p.c.v + o + 16 * li) = v[i];
         }
       } else {
-        // even lanes form the key's scale and inverse, odd ones the value's, and trade them
-        const uint32_t mk = row_max<LPR>(k[i]), mv = row_max<LPR>(v[i]);
-        const bool odd = li & 1;
-        const float s = scale_of(odd ? mv : mk), inv = 1.0f / s;
-        const float inv1 = __shfl_xor_sync(0xFFFFFFFFu, inv, 1);
+        float s, ik, iv;
+        scales_of(row_max<LPR>(k[i]), row_max<LPR>(v[i]), li, s, ik, iv);
         float2 x[4];
         unpack8(k[i], x);
-        const uint2 kc = codes_of(x, odd ? inv1 : inv);
+        const uint2 kc = codes_of(x, ik);
         unpack8(v[i], x);
-        const uint2 vc = codes_of(x, odd ? inv : inv1);
+        const uint2 vc = codes_of(x, iv);
         if (on && pl[i].ok) {
           *reinterpret_cast<uint2*>(p.c.k + o + 8 * li) = kc;
           *reinterpret_cast<uint2*>(p.c.v + o + 8 * li) = vc;
-          if (li < 2) (odd ? p.c.vs : p.c.ks)[scale_at(p, pl[i], head[i])] = s;
+          if (li < 2) (li ? p.c.vs : p.c.ks)[scale_at(p, pl[i], head[i])] = s;
         }
       }
     } else if (on && tok[i] >= 0) {

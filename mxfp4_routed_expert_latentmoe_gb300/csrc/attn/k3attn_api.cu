@@ -162,21 +162,33 @@ cudaError_t launch_rows(QkvParams p, int sms, cudaStream_t s) {
 
 // The norms' blocks: ROWS rows a thread and just the warps that a token's rows take so; a token
 // that takes more than a block has is cut into balanced parts, tokens of few rows share a block
-// of up to 8 warps
+// of up to 8 warps.  Keys and values for the cache have blocks of the same size.
 template <int FMT, int ROWS>
 cudaError_t launch_norm_t(QkvParams p, int sms, cudaStream_t s) {
-  const int lpr = lanes_of(p.D), rows = p.Hq + p.Hkv * (FMT == CF_NONE ? 1 : 2);
-  const int a_warp = 32 / lpr * ROWS, most = QKV_THREADS / 32 * a_warp, parts = (rows + most - 1) / most;
-  p.rows = (rows + parts - 1) / parts;
-  p.warps = (p.rows + a_warp - 1) / a_warp;
-  p.tokens = p.warps > 4 ? 1 : 8 / p.warps;
+  const int lpr = lanes_of(p.D), rows = p.Hq + (FMT == CF_NONE ? p.Hkv : 0);
+  const int a_warp = 32 / lpr * ROWS, most = QKV_THREADS / 32 * a_warp;
+  p.parts = (rows + most - 1) / most;
+  p.rows = (rows + p.parts - 1) / p.parts;
+  p.parts = (rows + p.rows - 1) / p.rows;
+  const int token_warps = (p.rows + a_warp - 1) / a_warp;
+  p.tokens = token_warps > 4 ? 1 : 8 / token_warps;
   if (p.tokens > p.T) p.tokens = p.T;
-  const dim3 grid((p.T + p.tokens - 1) / p.tokens, (rows + p.rows - 1) / p.rows);
+  const int warps = token_warps * p.tokens;
+  p.kv_blocks = 0;
+  if constexpr (FMT != CF_NONE) {
+    const int kv_warp = 32 / lpr * (ROWS > 1 ? 2 : 1);
+    p.kv_warps = (p.Hkv + kv_warp - 1) / kv_warp;
+    if (p.kv_warps > warps) p.kv_warps = warps;
+    p.kv_tokens = warps / p.kv_warps < QKV_TOKENS ? warps / p.kv_warps : QKV_TOKENS;
+    p.kv_blocks = (p.T + p.kv_tokens - 1) / p.kv_tokens;
+  }
+  const int64_t grid = p.kv_blocks + (int64_t)((p.T + p.tokens - 1) / p.tokens) * p.parts;
   if constexpr (ROWS > 1)
-    if ((int64_t)grid.x * grid.y < sms) return launch_norm_t<FMT, 1>(p, sms, s);
+    if (grid < sms) return launch_norm_t<FMT, 1>(p, sms, s);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return launch(lpr == 8 ? k3_norm_kernel<8, FMT, ROWS>
                          : (lpr == 16 ? k3_norm_kernel<16, FMT, ROWS> : k3_norm_kernel<32, FMT, ROWS>),
-                grid, dim3(32 * p.warps * p.tokens), 0, s, p);
+                dim3((unsigned)grid), dim3(32 * warps), 0, s, p);
 }
 template <int FMT>
 cudaError_t launch_norm(const QkvParams& p, int sms, cudaStream_t s) {
