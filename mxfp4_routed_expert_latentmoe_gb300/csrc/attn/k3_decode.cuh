@@ -14,10 +14,13 @@
 // goes into its weight's exponent, with a maximum of its own, so that weights of values of any
 // size keep fp16's full precision.  bf16 rows are multiplied as they are.
 //
-// The work is cut into units (a block's tokens of one (sequence, key head, head group)), which
-// are dealt out evenly: block c takes units c * chunk .. (c + 1) * chunk - 1 of all of them,
-// whatever the lengths.  A part that is not a whole sequence leaves an unnormalised record in
-// the workspace; the block that arrives last joins a sequence's records, in block order.
+// The work is cut into units (W tiles of one (sequence, key head, head group), one for each of
+// the W warps of a team), and the units, in a line, are dealt out evenly to all teams, whatever
+// the lengths; a sequence's start counts as one more.  A team joins its warps' sums at the end
+// of a sequence's part; a part that is not a whole sequence leaves an unnormalised record in the
+// workspace, and the team that arrives last joins a sequence's records, in order.  Long
+// sequences have teams of a whole block (few records), short ones of 4, 2 or 1 warps (a warp
+// has its own sequence, and waits for nobody).
 #pragma once
 
 #include "k3_qkv.cuh"
@@ -36,12 +39,14 @@ struct DecodeParams {
   uint16_t* out;
   float* lse;
   uint32_t* status;
-  uint32_t* arrived;  // one counter a block, zero between calls
-  float* parts;       // two records a block
+  uint32_t* arrived;  // one counter a team, zero between calls
+  float* parts;       // two records a team
 };
 
-// most blocks of a launch (the workspace holds their counters and records)
+// most teams of a launch (the workspace holds their counters and records)
+constexpr int DEC_MAX_WARPS = 8;
 constexpr int DEC_MAX_BLOCKS = 192;
+constexpr int DEC_MAX_TEAMS = DEC_MAX_BLOCKS * DEC_MAX_WARPS;
 
 // Shapes of one instance: the warps of a block, the tokens of a warp's tile, the ring's depth,
 // and the dims that one pass of the block's join takes (its buffer gets what the ring leaves).
@@ -50,7 +55,7 @@ struct DecCfg {
   static constexpr int ES = FMT == CF_E4M3 ? 1 : 2;
   static constexpr int ROW = DP * ES;  // bytes of a row in shared memory
   static constexpr int MT = 2 * ROW * 32 <= 8192 ? 2 : 1;
-  static constexpr int TW = 16 * MT;
+  static constexpr int TW = 16 * MT, TLOG = 3 + MT;
   static constexpr int KV = 2 * TW * ROW;
   static constexpr int WARPS = KV <= 8192 ? 8 : 4;
   static constexpr int STAGES = 196608 / (WARPS * KV);
@@ -58,16 +63,12 @@ struct DecCfg {
   static constexpr int HEADS = 8 * NT;
   static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int ML = WARPS * HEADS * 3 * 4;
-  static constexpr int room() { return 227 * 1024 - 256 - RING - ML; }
-  static constexpr int join_bytes(int pd) { return WARPS * HEADS * (pd + 4) * 4; }
-  static constexpr int fit(int pd) { return join_bytes(pd) <= room() ? pd : fit(pd / 2); }
-  static constexpr int PD = fit(DP);
-  static constexpr int SMEM = RING + ML + join_bytes(PD) + 256;
-  static constexpr int REC = HEADS * (DP + 2);  // floats of a record
-  static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && PD % 16 == 0, "does not fit");
-  static_assert(DEC_MAX_BLOCKS * HEADS * 4 <= join_bytes(PD), "the records' weights use the join buffer");
+  static constexpr int SMEM = RING + ML + 1024;
+  // n-tiles whose sums fit the stage of a tile that is read out (the join of a team's warps)
+  static constexpr int PN = HEADS * DP * 4 <= KV ? NT : 1;
+  static constexpr int REC = HEADS * (DP + 2);  // floats of a record: sums, maxima, sums of weights
+  static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && PN * 8 * DP * 4 <= KV, "does not fit");
 };
-constexpr int DEC_MAX_REC = 16 * (256 + 2);
 
 K3_DEVI float ex2(float x) {
   float y;
@@ -134,6 +135,23 @@ K3_DEVI uint32_t chunk_at(int r, int c) {
   }
 }
 
+// a / b of non-negative numbers (that are nearly always short)
+K3_DEVI int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+// barrier of one team's threads
+K3_DEVI void team_sync(int team, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(team + 1), "r"(threads) : "memory");
+}
+// counts an arrival: what the team has written (before its barrier) is visible to the team that
+// sees the count, and the other way round
+K3_DEVI uint32_t arrive(uint32_t* counter) {
+  uint32_t before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;\n" : "=r"(before) : "l"(counter) : "memory");
+  return before;
+}
+
 // length of sequence b within what its table can hold
 K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
   const int32_t n = __ldg(p.lens + b);
@@ -142,40 +160,67 @@ K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
   return n < 0 ? 0 : (n > most ? (int32_t)most : n);
 }
 
-// A place in the order of the units: sequence b, head group hr of its Hkv * groups, unit u of nu.
-template <int UNIT>
+// A place in the order of the units: sequence b, key head kvh and group grp of its query heads,
+// unit u of nu (2^ulog tokens each); x: its number from the team's first one, a sequence's start
+// (of each group) counted in front of its units.
 struct DecAt {
-  int32_t b, hr, u, nu, first, n;
-  K3_DEVI bool open(const DecodeParams& p) {  // sequence b's tokens and units; false: a bad length
+  int32_t b, kvh, grp, u, nu, first, n, x;
+  K3_DEVI bool open(const DecodeParams& p, int ulog) {  // sequence b's tokens and units; false: a bad length
     bool bad;
     n = seq_len(p, b, bad);
     first = p.window > 0 && n > p.window ? n - p.window : 0;
-    nu = (n - first) / UNIT + ((n - first) % UNIT != 0);
+    nu = (int32_t)(((uint32_t)(n - first) + (1u << ulog) - 1) >> ulog);
     return !bad;
   }
-  K3_DEVI void next(const DecodeParams& p) {
+  K3_DEVI void next(const DecodeParams& p, int ulog) {
+    ++x;
     if (++u < nu) return;
+    ++x;
     u = 0;
-    if (++hr < p.Hkv * p.groups) return;
-    hr = 0;
+    if (++grp < p.groups) return;
+    grp = 0;
+    if (++kvh < p.Hkv) return;
+    kvh = 0;
     do {
       if (++b >= p.B) return;
-      open(p);
+      open(p, ulog);
     } while (nu == 0);
   }
 };
+// A part that is not a whole sequence, until its team asks who arrived last.
+struct DecPart {
+  int64_t i0;           // the sequence's first unit of all
+  int64_t row;          // its first row of the output
+  int32_t c0, parts;    // its first team, the number of them
+  int32_t heads, there;
+};
+
+// four values to bf16
+K3_DEVI uint2 bf16x4(float a, float b, float c, float d) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+// log-sum-exp from the maximum and the sum of powers of two
+K3_DEVI float lse_of(float base, float sum) {
+  return sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+}
 
 template <int FMT, int DP, int NT>
 __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_kernel(const DecodeParams p) {
   using C = DecCfg<FMT, DP, NT>;
   constexpr int WARPS = C::WARPS, THREADS = WARPS * 32, TW = C::TW, MT = C::MT, STAGES = C::STAGES, ROW = C::ROW;
-  constexpr int UNIT = WARPS * TW, HEADS = C::HEADS, KSTEPS = DP / 16, PD = C::PD;
+  constexpr int HEADS = C::HEADS, KSTEPS = DP / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t ring = smem_u32(smem) + warp * STAGES * C::STAGE;
-  float* s_ml = reinterpret_cast<float*>(smem + C::RING);  // [WARPS][HEADS] maxima, sums, value maxima
-  float* s_join = reinterpret_cast<float*>(smem + C::RING + C::ML);
-  int64_t* s_misc = reinterpret_cast<int64_t*>(smem + C::SMEM - 256);
+  float* const s_ml = reinterpret_cast<float*>(smem + C::RING);  // [WARPS][HEADS] maxima, sums, value maxima
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + C::RING + C::ML);               // [WARPS]
+  int64_t* const s_off = s_sum + DEC_MAX_WARPS;                                            // [teams]
+  int32_t* const s_b = reinterpret_cast<int32_t*>(s_off + DEC_MAX_WARPS);                  // [teams]
+  volatile int32_t* const s_last = s_b + DEC_MAX_WARPS;                                    // [teams]
+  int64_t* const s_count = reinterpret_cast<int64_t*>(smem + C::RING + C::ML + 256);       // [WARPS][4]
+  DecPart* const s_part = reinterpret_cast<DecPart*>(smem + C::RING + C::ML + 256);        // [teams][2]
+  static_assert(2 * DEC_MAX_WARPS * sizeof(DecPart) <= 768 && DEC_MAX_WARPS * 32 <= 256, "shared layout");
 
   // dims past D: zero in every stage, never written again
   if (p.D < DP)
@@ -185,87 +230,144 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- this block's units: all units counted, and the sequence that holds the first one found
+  // ---- the teams' size: the tiles that teams of 1, 2, 4 and 8 warps would take, with the idle
+  // warps of every sequence's last unit
   const int32_t HR = p.Hkv * p.groups;
-  const int per = (p.B + THREADS - 1) / THREADS;
-  DecAt<UNIT> at;
-  int64_t mine = 0;
-  const int b_lo = min(p.B, (int)threadIdx.x * per), b_hi = min(p.B, b_lo + per);
+  const int seqs = (p.B + THREADS - 1) / THREADS;
+  const int b_lo = min(p.B, (int)threadIdx.x * seqs), b_hi = min(p.B, b_lo + seqs);
+  DecAt at;
+  int64_t count[4] = {0, 0, 0, 0}, some = 0;
   bool any_bad = false;
   for (at.b = b_lo; at.b < b_hi; ++at.b) {
-    any_bad |= !at.open(p);
-    mine += at.nu;
+    any_bad |= !at.open(p, C::TLOG);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count[i] += (at.nu + (1 << i) - 1) >> i << i;
+    some += at.nu > 0;
   }
   if (any_bad && blockIdx.x == 0) flag_status(p.status, K3ATTN_DEV_BAD_LENGTH);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int64_t v = count[i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0) s_count[warp * 4 + i] = v;
+  }
+  __syncthreads();
+  int wlog = -1;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    int64_t v = 0, v0 = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      v += s_count[w * 4 + i];
+      v0 += s_count[w * 4];
+    }
+    // the largest that wastes at most a quarter, or leaves warps idle anyway
+    if (wlog < 0 && (1 << i) <= WARPS && (4 * v <= 5 * v0 || v * HR <= (int64_t)gridDim.x * WARPS)) wlog = i;
+  }
+  const int W = 1 << wlog, ulog = C::TLOG + wlog, teams = WARPS >> wlog, team = warp >> wlog, tw = warp & (W - 1);
+  const int tthreads = 32 << wlog, tthread = threadIdx.x & (tthreads - 1);
+
+  // ---- the teams' units: the sequences that hold their first ones
+  const int64_t mine = ((wlog == 0 ? count[0] : wlog == 1 ? count[1] : wlog == 2 ? count[2] : count[3]) >> wlog) + some;
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
     if (lane >= o) upto += v;
   }
-  if (lane == 31) s_misc[warp] = upto;
+  if (lane == 31) s_sum[warp] = upto;
   __syncthreads();
-  int64_t all = 0;
+  int64_t total = 0;
   for (int w = 0; w < WARPS; ++w) {
-    if (w == warp) upto += all;
-    all += s_misc[w];
+    if (w == warp) upto += total;
+    total += s_sum[w];
   }
-  const int64_t total = all * HR;
-  const int64_t chunk = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
-  const int64_t unit0 = blockIdx.x * chunk;
-  const int64_t left64 = min(total, unit0 + chunk) - unit0;
-  if (left64 > 0 && mine > 0 && unit0 >= (upto - mine) * HR && unit0 < upto * HR) {
-    int64_t before = (upto - mine) * HR;
-    for (at.b = b_lo;; ++at.b) {
-      at.open(p);
-      if (unit0 < before + (int64_t)at.nu * HR) break;
-      before += (int64_t)at.nu * HR;
+  total *= HR;
+  const int64_t workers = (int64_t)gridDim.x * teams, chunk = max((int64_t)1, div64(total + workers - 1, workers));
+  if (mine > 0) {
+    const int64_t lo = (upto - mine) * HR, hi = upto * HR;
+    for (int i = 0; i < teams; ++i) {
+      const int64_t x = ((int64_t)blockIdx.x * teams + i) * chunk;
+      if (x < lo || x >= hi) continue;
+      int64_t before = lo;
+      for (at.b = b_lo;; ++at.b) {
+        at.open(p, ulog);
+        const int64_t here = at.nu > 0 ? (int64_t)(at.nu + 1) * HR : 0;
+        if (x < before + here) break;
+        before += here;
+      }
+      s_b[i] = at.b;
+      s_off[i] = x - before;
     }
-    s_misc[8] = at.b;
-    s_misc[9] = unit0 - before;
   }
   __syncthreads();
 
-  if (left64 > 0) {
-    const int32_t units = (int32_t)min(left64, (int64_t)INT32_MAX);
-    at.b = (int32_t)s_misc[8];
-    at.open(p);
-    at.hr = (int32_t)(s_misc[9] / at.nu);
-    at.u = (int32_t)(s_misc[9] % at.nu);
-    DecAt<UNIT> ahead = at;  // the tile whose page entries are in `entry`
-    int32_t entry = 0, issued = 0;
+  const int64_t worker = (int64_t)blockIdx.x * teams + team, unit0 = worker * chunk;
+  const int32_t end = (int32_t)max((int64_t)0, min(min(total - unit0, chunk), (int64_t)INT32_MAX));
+  if (tthread < 2) s_part[2 * team + tthread].there = 0;
+  if (end > 0) {
+    at.b = s_b[team];
+    at.open(p, ulog);
+    const int32_t hr = (int32_t)div64(s_off[team], at.nu + 1);
+    at.kvh = hr / p.groups;
+    at.grp = hr - at.kvh * p.groups;
+    at.u = (int32_t)(s_off[team] - (int64_t)hr * (at.nu + 1)) - 1;
+    at.x = 0;
+    if (at.u < 0) at.u = 0, at.x = 1;  // a sequence's start
+    DecAt ahead = at;  // the tile whose page entries are in `entry`, with the rows' places in them
+    int32_t entry = 0, in_page = 0;
+    uint32_t got[2] = {0, 0};  // arrivals before this team's (of its first thread)
 
+    constexpr int CPR = ROW / 16;  // 16-byte chunks of a row
+    const int cpr = p.D * C::ES / 16;
     // row `lane` (of TW) of the tile at `ahead`
-    auto row_token = [&]() { return ahead.first + (ahead.u * WARPS + warp) * TW + (lane & (TW - 1)); };
+    auto row_token = [&]() { return ahead.first + (ahead.u * W + tw) * TW + (lane & (TW - 1)); };
     auto fetch = [&]() {  // the tile's page entries
       const int32_t t = row_token();
       entry = 0;
       if (t < ahead.n) {
         const uint32_t pg = p.c.by_page(t);
         entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
+        in_page = t - (int32_t)(pg * (uint32_t)p.c.page_size);
       }
     };
     auto issue = [&](int stage) {  // the copies of the tile at `ahead`
       const uint32_t st = ring + stage * C::STAGE;
-      const int32_t t = row_token();
-      const bool in = t < ahead.n;
+      if (ahead.u == 0 || ahead.x < 2) {  // a part's first tile: its queries will be wanted
+        const char* q = reinterpret_cast<const char*>(
+            p.q + ahead.b * p.q_stride + ((int64_t)ahead.kvh * p.G + ahead.grp * HEADS) * p.D);
+        const int bytes = min(HEADS, p.G - ahead.grp * HEADS) * p.D * 2;
+        for (int i = 128 * lane; i < bytes; i += 128 * 32) asm volatile("prefetch.global.L1 [%0];\n" ::"l"(q + i));
+      }
+      const bool in = row_token() < ahead.n;
       const bool ok = in && entry >= 0 && entry < p.c.n_pages;
       if (in && !ok) flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
       if (lane == 0) *reinterpret_cast<uint32_t*>(__cvta_shared_to_generic(st + C::STAGE - 16)) = mask;
       if (mask == 0) return;
-      const int32_t kvh = ahead.hr / p.groups;
-      const uint32_t pg = p.c.by_page(t);
-      const int64_t in_page = t - (int32_t)(pg * (uint32_t)p.c.page_size);
-      const int64_t off = ok ? entry * p.c.page + kvh * p.c.head + in_page * p.c.tok : 0;
+      const int64_t off = ok ? entry * p.c.page + ahead.kvh * p.c.head + in_page * p.c.tok : 0;
       if constexpr (FMT == CF_E4M3) {
-        const int64_t so = ok ? entry * p.c.spage + kvh * p.c.shead + in_page * p.c.stok : 0;
+        const int64_t so = ok ? entry * p.c.spage + ahead.kvh * p.c.shead + in_page * p.c.stok : 0;
         const uint32_t dst = st + C::KV + 4 * (lane & (TW - 1));
         if (TW == 32 || lane < 16) cp_async4_or_zero(dst, p.c.ks + so, ok ? 4 : 0);
         if (TW == 32 || lane >= 16) cp_async4_or_zero(dst + 4 * TW, p.c.vs + so, ok ? 4 : 0);
       }
-      constexpr int CPR = ROW / 16;
-      const int cpr = p.D * C::ES / 16;
+      if (mask == 0xFFFFFFFFu && p.D == DP && 32 % CPR == 0 && __shfl_sync(0xFFFFFFFFu, in_page, 0) + TW <= p.c.page_size) {
+        // all rows there, on one page: they lie a token's stride apart
+        constexpr int RPI = 32 % CPR == 0 ? 32 / CPR : 1;
+        const int64_t step = RPI * p.c.tok;
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + (lane / CPR) * p.c.tok + 16 * (lane % CPR);
+        const uint8_t *kp = p.c.k + o, *vp = p.c.v + o;
+#pragma unroll
+        for (int i = 0; i < TW * CPR / 32; ++i) {
+          const uint32_t dst = st + chunk_at<FMT, ROW>(i * RPI + lane / CPR, lane % CPR);
+          cp_async16(dst, kp);
+          cp_async16(dst + TW * ROW, vp);
+          kp += step;
+          vp += step;
+        }
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < TW * CPR / 32; ++i) {
         const int r = (i * 32 + lane) / CPR, ch = (i * 32 + lane) % CPR;
@@ -278,36 +380,33 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
         }
       }
     };
-    // copies tile `issued` (if there is one) and fetches the entries of the next
+    // copies the tile at `ahead` (if it is the team's) and fetches the entries of the next
     auto advance = [&](int stage) {
-      if (issued < units) {
+      if (ahead.x < end) {
         issue(stage);
-        ++issued;
-        if (issued < units) {
-          ahead.next(p);
-          fetch();
-        }
+        ahead.next(p, ulog);
+        if (ahead.x < end) fetch();
       }
       cp_async_commit();
     };
-    fetch();
+    if (ahead.x < end) fetch();
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) advance(s);
 
     float acc[KSTEPS][NT][4], m[NT][2], l[NT][2], vm[NT][2], qs[NT][2];
     uint32_t qf[KSTEPS][NT][2];
-    int32_t seg_u0 = 0;
+    int32_t part_u0 = 0, part_slot = 0;
     int stage = 0;
-    for (int32_t k = 0; k < units; ++k) {
+    for (bool begun = false; at.x < end; begun = true) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
       advance(stage == 0 ? STAGES - 1 : stage - 1);
-      const int32_t kvh = at.hr / p.groups, grp = at.hr - kvh * p.groups;
-      const int32_t heads = min(HEADS, p.G - grp * HEADS);  // of this group
-      const int64_t head0 = (int64_t)kvh * p.G + grp * HEADS;
+      const int32_t heads = min(HEADS, p.G - at.grp * HEADS);  // of this group
+      const int64_t head0 = (int64_t)at.kvh * p.G + at.grp * HEADS;
 
-      if (k == 0 || at.u == 0) {  // a new part: its queries, empty sums
-        seg_u0 = at.u;
+      if (!begun || at.u == 0) {  // a new part: its queries, empty sums
+        part_u0 = at.u;
+        part_slot = begun;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int h = nt * 8 + lane / 4;
@@ -513,11 +612,15 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
           }
         }
       }
+      const int used = stage * C::STAGE;  // this tile's stage: read out, copied over in the next turn
       stage = stage == STAGES - 1 ? 0 : stage + 1;
 
       // ---- the end of a part: join the warps, then write the result or leave a record
-      if (k == units - 1 || at.u == at.nu - 1) {
-        const bool whole = seg_u0 == 0 && at.u == at.nu - 1;
+      const DecAt now = at;
+      at.next(p, ulog);
+      if (at.x >= end || now.u == now.nu - 1) {
+        const bool whole = part_u0 == 0 && now.u == now.nu - 1;
+        const int64_t row0 = (int64_t)now.b * p.Hq + head0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -531,127 +634,141 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
               x[2] = FMT == CF_E4M3 ? vm[nt][h] : m[nt][h];
             }
           }
-        float* rec = p.parts + (2 * (int64_t)blockIdx.x + (seg_u0 == at.u - k ? 0 : 1)) * C::REC;
+        float* const rec = p.parts + (2 * worker + part_slot) * C::REC;
+        const int w0 = team << wlog;
+        __syncwarp();  // all lanes have read the tile
 #pragma unroll
-        for (int pass = 0; pass < DP / PD; ++pass) {
+        for (int n0 = 0; n0 < NT; n0 += C::PN) {
+          // dim d of head h at d ^ (h / 2 % 4 * 8): the heads of a fragment lie in different banks
 #pragma unroll
-          for (int c = pass * (PD / 16); c < (pass + 1) * (PD / 16); ++c)
+          for (int n = 0; n < C::PN; ++n)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int h = 0; h < 2; ++h) {
+              float* const x = reinterpret_cast<float*>(smem + warp * STAGES * C::STAGE + used) +
+                               (8 * n + 2 * (lane & 3) + h) * DP;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float* x = s_join + (warp * HEADS + nt * 8 + 2 * (lane & 3) + h) * (PD + 4) + 16 * c - pass * PD;
+              for (int c = 0; c < KSTEPS; ++c) {
                 if constexpr (FMT == CF_BF16) {
-                  x[lane / 4] = acc[c][nt][h];
-                  x[lane / 4 + 8] = acc[c][nt][2 + h];
+                  x[(16 * c + lane / 4) ^ ((lane & 3) << 3)] = acc[c][n0 + n][h];
+                  x[(16 * c + lane / 4 + 8) ^ ((lane & 3) << 3)] = acc[c][n0 + n][2 + h];
                 } else {
-                  *reinterpret_cast<float2*>(x + 2 * (lane / 4)) = make_float2(acc[c][nt][h], acc[c][nt][2 + h]);
+                  *reinterpret_cast<float2*>(x + ((16 * c + 2 * (lane / 4)) ^ ((lane & 3) << 3))) =
+                      make_float2(acc[c][n0 + n][h], acc[c][n0 + n][2 + h]);
                 }
               }
-          __syncthreads();
-          for (int i = threadIdx.x; i < heads * (PD / 4); i += THREADS) {
-            const int h = i / (PD / 4), d = 4 * (i % (PD / 4));
+            }
+          team_sync(team, tthreads);
+          const int hs = min(heads - 8 * n0, 8 * C::PN);
+          for (int i = tthread; i < hs * (DP / 4); i += tthreads) {
+            const int hp = i / (DP / 4), h = 8 * n0 + hp, d = 4 * (i % (DP / 4));
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_ml[(w * HEADS + h) * 3]);
+            for (int w = 0; w < WARPS; ++w)
+              if (w < W) top = fmaxf(top, s_ml[((w0 + w) * HEADS + h) * 3]);
             const float base = top == -INFINITY ? 0.f : top;
             float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
-              const float* x = s_ml + (w * HEADS + h) * 3;
+              if (w >= W) continue;
+              const float* x = s_ml + ((w0 + w) * HEADS + h) * 3;
               sum += x[1] * ex2(x[0] - base);
               const float f = ex2(x[2] - base);
-              const float4 v = *reinterpret_cast<const float4*>(s_join + (w * HEADS + h) * (PD + 4) + d);
+              const float4 v = *reinterpret_cast<const float4*>(
+                  reinterpret_cast<const float*>(smem + (w0 + w) * STAGES * C::STAGE + used) + hp * DP +
+                  (d ^ ((hp >> 1 & 3) << 3)));
               o[0] = fmaf(v.x, f, o[0]);
               o[1] = fmaf(v.y, f, o[1]);
               o[2] = fmaf(v.z, f, o[2]);
               o[3] = fmaf(v.w, f, o[3]);
             }
-            const int dim = pass * PD + d;
-            if (whole) {
+            if (whole) {  // (a sum of 0: nothing was attended to)
               const float r = sum == 0.f ? 0.f : 1.f / sum;
-              const int64_t row = (int64_t)at.b * p.Hq + head0 + h;
-              if (dim < p.D) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(sum == 0.f ? 0.f : o[0] * r, sum == 0.f ? 0.f : o[1] * r);
-                const __nv_bfloat162 hi = __floats2bfloat162_rn(sum == 0.f ? 0.f : o[2] * r, sum == 0.f ? 0.f : o[3] * r);
-                *reinterpret_cast<uint2*>(p.out + row * p.D + dim) = make_uint2(
-                    *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-              }
-              if (dim == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+              if (d < p.D)
+                *reinterpret_cast<uint2*>(p.out + (row0 + h) * p.D + d) =
+                    bf16x4(o[0] * r, o[1] * r, o[2] * r, o[3] * r);
+              if (d == 0 && p.lse) p.lse[row0 + h] = lse_of(base, sum);
             } else {
-              __stcg(reinterpret_cast<float4*>(rec + h * DP + dim), make_float4(o[0], o[1], o[2], o[3]));
-              if (dim == 0) {
+              __stcg(reinterpret_cast<float4*>(rec + h * DP + d), make_float4(o[0], o[1], o[2], o[3]));
+              if (d == 0) {
                 __stcg(rec + HEADS * DP + h, top);
                 __stcg(rec + HEADS * DP + HEADS + h, sum);
               }
             }
           }
-          __syncthreads();
+          team_sync(team, tthreads);
         }
-        if (!whole) {
-          // the blocks of this (sequence, head group): units i0 .. i1 - 1 of all
-          const int64_t i0 = unit0 + k - at.u, i1 = i0 + at.nu;
-          const int32_t c0 = (int32_t)(i0 / chunk), c1 = (int32_t)((i1 - 1) / chunk), parts = c1 - c0 + 1;
-          int32_t* s_last = reinterpret_cast<int32_t*>(s_misc + 10);
-          if (threadIdx.x == 0) {
-            __threadfence();
-            *s_last = atomicAdd(p.arrived + c0, 1u) == (uint32_t)(parts - 1);
+        if (p.D < DP) {  // the dims past D of the stage are zero again
+          const int pad = CPR - cpr;
+          for (int i = lane; i < 2 * TW * pad; i += 32) {
+            const int r = i / pad, ch = cpr + i % pad;
+            *reinterpret_cast<uint4*>(smem + warp * STAGES * C::STAGE + used + (r < TW ? 0 : TW * ROW) +
+                                      chunk_at<FMT, ROW>(r & (TW - 1), ch)) = make_uint4(0, 0, 0, 0);
           }
-          __syncthreads();
-          if (*s_last) {
-            __threadfence();
-            if (threadIdx.x == 0) p.arrived[c0] = 0;
-            auto record = [&](int i) {  // block c0's part is its first only where it begins there
-              return p.parts + (2 * (int64_t)(c0 + i) + (i == 0 && i0 != c0 * chunk ? 1 : 0)) * C::REC;
-            };
-            // the records' weights [parts][HEADS] into the join buffer
-            for (int h = warp; h < heads; h += WARPS) {
-              float top = -INFINITY, sum = 0.f;
-              for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(record(i) + HEADS * DP + h));
-#pragma unroll
-              for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              const float base = top == -INFINITY ? 0.f : top;
-              for (int i = lane; i < parts; i += 32) {
-                const float f = ex2(__ldcg(record(i) + HEADS * DP + h) - base);
-                s_join[i * HEADS + h] = f;
-                sum += f * __ldcg(record(i) + HEADS * DP + HEADS + h);
-              }
-#pragma unroll
-              for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-              if (lane == 0) {
-                s_ml[h] = sum;
-                if (p.lse)
-                  p.lse[(int64_t)at.b * p.Hq + head0 + h] =
-                      sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
-              }
-            }
-            __syncthreads();
-            for (int i = threadIdx.x; i < heads * (DP / 4); i += THREADS) {
-              const int h = i / (DP / 4), d = 4 * (i % (DP / 4));
-              if (d >= p.D) continue;
-              float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-              for (int j = 0; j < parts; ++j) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(record(j) + h * DP + d));
-                const float f = s_join[j * HEADS + h];
-                o[0] = fmaf(v.x, f, o[0]);
-                o[1] = fmaf(v.y, f, o[1]);
-                o[2] = fmaf(v.z, f, o[2]);
-                o[3] = fmaf(v.w, f, o[3]);
-              }
-              const float sum = s_ml[h], r = 1.f / sum;
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(sum == 0.f ? 0.f : o[0] * r, sum == 0.f ? 0.f : o[1] * r);
-              const __nv_bfloat162 hi = __floats2bfloat162_rn(sum == 0.f ? 0.f : o[2] * r, sum == 0.f ? 0.f : o[3] * r);
-              *reinterpret_cast<uint2*>(p.out + ((int64_t)at.b * p.Hq + head0 + h) * p.D + d) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            }
-            __syncthreads();
-          }
+        }
+        if (!whole && tthread == 0) {
+          // the teams of this (sequence, head group), whose first unit is i0 of all
+          const int64_t i0 = unit0 + now.x - now.u;
+          const int32_t c0 = (int32_t)div64(i0, chunk), c1 = (int32_t)div64(i0 + now.nu - 1, chunk);
+          s_part[2 * team + part_slot] = DecPart{i0, row0, c0, c1 - c0 + 1, heads, 1};
+          (part_slot ? got[1] : got[0]) = arrive(p.arrived + c0);
         }
       }
-      at.next(p);
     }
     cp_async_wait<0>();
+
+    // ---- parts: the team that arrived last joins a sequence's records
+#pragma unroll
+    for (int slot = 0; slot < 2; ++slot) {
+      __syncwarp();
+      if (tthread == 0)
+        s_last[team] = s_part[2 * team + slot].there && got[slot] == (uint32_t)(s_part[2 * team + slot].parts - 1);
+      team_sync(team, tthreads);
+      if (s_last[team]) {
+        const DecPart x = s_part[2 * team + slot];
+        if (tthread == 0) p.arrived[x.c0] = 0;
+        constexpr int BATCH = 8;
+        for (int i = tthread; i < x.heads * (DP / 4); i += tthreads) {
+          const int h = i / (DP / 4), d = 4 * (i % (DP / 4));
+          if (d >= p.D) continue;
+          float top = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int j0 = 0; j0 < x.parts; j0 += BATCH) {
+            float mj[BATCH], lj[BATCH];
+            float4 v[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+              // team c0's part is its first only where it begins there
+              const int at_second = j0 + j == 0 && x.i0 - x.c0 * chunk > 1;
+              const float* y = p.parts + (2 * (int64_t)(x.c0 + j0 + j) + at_second) * C::REC;
+              const bool on = j0 + j < x.parts;
+              mj[j] = on ? __ldcg(y + HEADS * DP + h) : -INFINITY;
+              lj[j] = on ? __ldcg(y + HEADS * DP + HEADS + h) : 0.f;
+              v[j] = on ? __ldcg(reinterpret_cast<const float4*>(y + h * DP + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float m1 = top;
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) m1 = fmaxf(m1, mj[j]);
+            const float base = m1 == -INFINITY ? 0.f : m1, fall = ex2(top - base);
+            top = m1;
+            sum *= fall;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] *= fall;
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+              const float f = ex2(mj[j] - base);
+              sum = fmaf(lj[j], f, sum);
+              o[0] = fmaf(v[j].x, f, o[0]);
+              o[1] = fmaf(v[j].y, f, o[1]);
+              o[2] = fmaf(v[j].z, f, o[2]);
+              o[3] = fmaf(v[j].w, f, o[3]);
+            }
+          }
+          const float r = sum == 0.f ? 0.f : 1.f / sum;
+          *reinterpret_cast<uint2*>(p.out + (x.row + h) * p.D + d) = bf16x4(o[0] * r, o[1] * r, o[2] * r, o[3] * r);
+          if (d == 0 && p.lse) p.lse[x.row + h] = lse_of(top, sum);
+        }
+      }
+      team_sync(team, tthreads);
+    }
   }
 
   // ---- sequences with no tokens

@@ -205,9 +205,9 @@ bool set_smem(int dev, int bytes) {
   return true;
 }
 
-// The decode workspace: the status word, the blocks' counters (cleared once by
-// k3attn_workspace_init), the blocks' records.
-constexpr size_t kCounters = K3ATTN_MIN_WORKSPACE, kRecords = kCounters + DEC_MAX_BLOCKS * 4;
+// The decode workspace: the status word, the teams' counters (cleared once by
+// k3attn_workspace_init), the teams' records.
+constexpr size_t kCounters = K3ATTN_MIN_WORKSPACE, kRecords = kCounters + DEC_MAX_TEAMS * 4;
 static_assert(kRecords % 16 == 0, "the records are written 16 bytes at a time");
 
 // padded head dim and head group (8 NT query heads of a key head) of the decode instance
@@ -243,7 +243,7 @@ extern "C" {
 
 size_t k3attn_workspace_bytes(const k3attn_dims* dims) {
   if (check_dims(dims) != K3MOE_OK) return 0;
-  return kRecords + (size_t)2 * DEC_MAX_BLOCKS * 8 * dec_nt(*dims) * (dec_dp(*dims) + 2) * 4;
+  return kRecords + (size_t)2 * DEC_MAX_TEAMS * 8 * dec_nt(*dims) * (dec_dp(*dims) + 2) * 4;
 }
 
 k3moe_status k3attn_workspace_init(void* ws, size_t ws_bytes, void* stream) {
