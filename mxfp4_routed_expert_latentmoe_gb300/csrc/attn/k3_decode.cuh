@@ -16,7 +16,8 @@
 //
 // The work is cut into units (W tiles of one (sequence, key head, head group), one for each of
 // the W warps of a team), and the units, in a line, are dealt out evenly to all teams, whatever
-// the lengths; a sequence's start counts as one more.  A team joins its warps' sums at the end
+// the lengths; a sequence's start counts as one more, and a sequence of at most DEC_WHOLE tiles
+// stays with the team that its start falls to.  A team joins its warps' sums at the end
 // of a sequence's part; a part that is not a whole sequence leaves an unnormalised record in the
 // workspace, and the team that arrives last joins a sequence's records, in order.  Long
 // sequences have teams of a whole block (few records), short ones of 4, 2 or 1 warps (a warp
@@ -70,6 +71,26 @@ struct DecCfg {
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && PN * 8 * DP * 4 <= KV, "does not fit");
 };
 
+// D += A B on pairs of sums
+K3_DEVI void mma2_bf16(float2 (&d)[2], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  float c[4] = {d[0].x, d[0].y, d[1].x, d[1].y};
+  mma_bf16(c, a, b[0], b[1], c);
+  d[0] = make_float2(c[0], c[1]);
+  d[1] = make_float2(c[2], c[3]);
+}
+K3_DEVI void mma2_f16(float2 (&d)[2], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  float c[4] = {d[0].x, d[0].y, d[1].x, d[1].y};
+  mma_f16(c, a, b[0], b[1], c);
+  d[0] = make_float2(c[0], c[1]);
+  d[1] = make_float2(c[2], c[3]);
+}
+K3_DEVI float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
 K3_DEVI float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -160,6 +181,11 @@ K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
   return n < 0 ? 0 : (n > most ? (int32_t)most : n);
 }
 
+// Tiles of a sequence that is never cut: joining its records would take longer than they do (200
+// sequences up to 100 tokens, D 128, E4M3: 16.5 us, 18.3 if they are cut; with teams of a block,
+// where these are less than a unit, cutting stays right: 8 x 1000 tokens 11.3 us, 13.2 whole)
+constexpr int DEC_WHOLE = 4;
+
 // A place in the order of the units: sequence b, key head kvh and group grp of its query heads,
 // unit u of nu (2^ulog tokens each); x: its number from the team's first one, a sequence's start
 // (of each group) counted in front of its units.
@@ -172,6 +198,8 @@ struct DecAt {
     nu = (int32_t)(((uint32_t)(n - first) + (1u << ulog) - 1) >> ulog);
     return !bad;
   }
+  // whether the unit is the team's whose range ends in front of `end`
+  K3_DEVI bool in(int32_t end, int32_t whole) const { return (nu <= whole ? x - u - 1 : x) < end; }
   K3_DEVI void next(const DecodeParams& p, int ulog) {
     ++x;
     if (++u < nu) return;
@@ -265,6 +293,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     if (wlog < 0 && (1 << i) <= WARPS && (4 * v <= 5 * v0 || v * HR <= (int64_t)gridDim.x * WARPS)) wlog = i;
   }
   const int W = 1 << wlog, ulog = C::TLOG + wlog, teams = WARPS >> wlog, team = warp >> wlog, tw = warp & (W - 1);
+  const int whole_units = DEC_WHOLE >> wlog;
   const int tthreads = 32 << wlog, tthread = threadIdx.x & (tthreads - 1);
 
   // ---- the teams' units: the sequences that hold their first ones
@@ -313,7 +342,14 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     at.grp = hr - at.kvh * p.groups;
     at.u = (int32_t)(s_off[team] - (int64_t)hr * (at.nu + 1)) - 1;
     at.x = 0;
-    if (at.u < 0) at.u = 0, at.x = 1;  // a sequence's start
+    if (at.u < 0) {  // a sequence's start
+      at.u = 0;
+      at.x = 1;
+    } else if (at.nu <= whole_units) {  // another team's
+      at.x = at.nu - 1 - at.u;
+      at.u = at.nu - 1;
+      at.next(p, ulog);
+    }
     DecAt ahead = at;  // the tile whose page entries are in `entry`, with the rows' places in them
     int32_t entry = 0, in_page = 0;
     uint32_t got[2] = {0, 0};  // arrivals before this team's (of its first thread)
@@ -382,22 +418,22 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     };
     // copies the tile at `ahead` (if it is the team's) and fetches the entries of the next
     auto advance = [&](int stage) {
-      if (ahead.x < end) {
+      if (ahead.in(end, whole_units)) {
         issue(stage);
         ahead.next(p, ulog);
-        if (ahead.x < end) fetch();
+        if (ahead.in(end, whole_units)) fetch();
       }
       cp_async_commit();
     };
-    if (ahead.x < end) fetch();
+    if (ahead.in(end, whole_units)) fetch();
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) advance(s);
 
-    float acc[KSTEPS][NT][4], m[NT][2], l[NT][2], vm[NT][2], qs[NT][2];
+    float2 acc[KSTEPS][NT][2], m[NT], l[NT], vm[NT], qs[NT];  // pairs: of two heads
     uint32_t qf[KSTEPS][NT][2];
     int32_t part_u0 = 0, part_slot = 0;
     int stage = 0;
-    for (bool begun = false; at.x < end; begun = true) {
+    for (bool begun = false; at.in(end, whole_units); begun = true) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
       advance(stage == 0 ? STAGES - 1 : stage - 1);
@@ -406,7 +442,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 
       if (!begun || at.u == 0) {  // a new part: its queries, empty sums
         part_u0 = at.u;
-        part_slot = begun;
+        part_slot = at.u == 0 && at.x > 1;  // not the team's first place of all
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int h = nt * 8 + lane / 4;
@@ -420,7 +456,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
                 const int d = 16 * c + 8 * e + 2 * (lane & 3);
                 qf[c][nt][e] = on && d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
               }
-            qs[nt][0] = qs[nt][1] = p.scale;
+            qs[nt] = make_float2(p.scale, p.scale);
           } else {
             // fp16, scaled by the power of two that brings the row's largest into [2^14, 2^15);
             // step 4 j + i of the contraction holds dims 64 j + 16 (lane % 4) + 4 i .. + 3
@@ -448,19 +484,15 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
               }
             }
             // the scale's inverse, for the two heads whose logits this lane holds
-            const float inv = p.scale * pow2f(-(pw >> 1)) * pow2f((pw >> 1) - pw);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) qs[nt][e] = __shfl_sync(0xFFFFFFFFu, inv, 4 * (2 * (lane & 3) + e));
+            // (not below the normal numbers: a masked logit's -infinity times it stays one)
+            const float inv = fmaxf(p.scale * pow2f(-(pw >> 1)) * pow2f((pw >> 1) - pw), 0x1p-126f);
+            qs[nt].x = __shfl_sync(0xFFFFFFFFu, inv, 4 * (2 * (lane & 3)));
+            qs[nt].y = __shfl_sync(0xFFFFFFFFu, inv, 4 * (2 * (lane & 3) + 1));
           }
+          m[nt] = vm[nt] = make_float2(-INFINITY, -INFINITY);
+          l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            m[nt][e] = vm[nt][e] = -INFINITY;
-            l[nt][e] = 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < KSTEPS; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
+          for (int c = 0; c < KSTEPS; ++c) acc[c][nt][0] = acc[c][nt][1] = make_float2(0.f, 0.f);
         }
       }
 
@@ -468,20 +500,20 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       const uint32_t mask = lds32(st + C::STAGE - 16);
       if (mask != 0) {
         // ---- logits: lane holds tokens lane / 4 and + 8 of each 16, heads 2 (lane % 4) and + 1
-        float s[MT][NT][4];
+        float2 s[MT][NT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+            for (int e = 0; e < 2; ++e) s[mt][nt][e] = make_float2(0.f, 0.f);
           if constexpr (FMT == CF_BF16) {
 #pragma unroll
             for (int c = 0; c < KSTEPS; ++c) {
               uint32_t a[4];
               ldsm4(a, st + chunk_at<FMT, ROW>(16 * mt + (lane & 15), 2 * c + (lane >> 4)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_bf16(s[mt][nt], a, qf[c][nt][0], qf[c][nt][1], s[mt][nt]);
+              for (int nt = 0; nt < NT; ++nt) mma2_bf16(s[mt][nt], a, qf[c][nt]);
             }
           } else {
 #pragma unroll
@@ -496,90 +528,93 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
                 e4m3x4_f16x4(w1[i], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(s[mt][nt], a, qf[4 * j + i][nt][0], qf[4 * j + i][nt][1], s[mt][nt]);
+                  mma2_f16(s[mt][nt], a, qf[4 * j + i][nt]);
               }
             }
           }
         }
-        // ---- weights
+        // ---- weights: the raw logits times the keys' scales; the factor qs of a head (softmax
+        // scale, log2(e), the scale of its fp16 queries) goes into the exponent's FMA
         float lvs[MT][2];  // log2 of the values' scales
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 16 * mt + lane / 4 + 8 * e;
-            const bool ok = (mask >> r) & 1u;
-            float ks = 1.f;
             if constexpr (FMT == CF_E4M3) {
-              ks = lds_f32(st + C::KV + 4 * r);
+              const float ks = lds_f32(st + C::KV + 4 * r);
               lvs[mt][e] = lg2(lds_f32(st + C::KV + 4 * (TW + r)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) s[mt][nt][e] = mul2(s[mt][nt][e], make_float2(ks, ks));
             }
+            if (mask != 0xFFFFFFFFu) {
+              const bool ok = (mask >> r) & 1u;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float& x = s[mt][nt][2 * e + h];
-                x = ok ? x * ks * qs[nt][h] : -INFINITY;
-              }
+              for (int nt = 0; nt < NT; ++nt)
+                if (!ok) s[mt][nt][e] = make_float2(-INFINITY, -INFINITY);
+            }
           }
         uint32_t pf[MT][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float base[2], vbase[2], fall[2];
+          // maxima: of the raw logits, and (E4M3) of the logits with the values' scales
+          float2 t = s[0][nt][0], tv = make_float2(-INFINITY, -INFINITY), sv[MT][2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float t = -INFINITY, tv = -INFINITY;
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                t = fmaxf(t, s[mt][nt][2 * e + h]);
-                if constexpr (FMT == CF_E4M3) tv = fmaxf(tv, s[mt][nt][2 * e + h] + lvs[mt][e]);
+            for (int e = 0; e < 2; ++e) {
+              t = make_float2(fmaxf(t.x, s[mt][nt][e].x), fmaxf(t.y, s[mt][nt][e].y));
+              if constexpr (FMT == CF_E4M3) {
+                sv[mt][e] = fma2(s[mt][nt][e], qs[nt], make_float2(lvs[mt][e], lvs[mt][e]));
+                tv = make_float2(fmaxf(tv.x, sv[mt][e].x), fmaxf(tv.y, sv[mt][e].y));
               }
+            }
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-              if constexpr (FMT == CF_E4M3) tv = fmaxf(tv, __shfl_xor_sync(0xFFFFFFFFu, tv, o));
-            }
-            const float m1 = fmaxf(m[nt][h], t);
-            base[h] = m1 == -INFINITY ? 0.f : m1;
-            const float f = ex2(m[nt][h] - base[h]);
-            m[nt][h] = m1;
-            l[nt][h] *= f;
-            fall[h] = f;
+          for (int o = 4; o < 32; o <<= 1) {
+            t.x = fmaxf(t.x, __shfl_xor_sync(0xFFFFFFFFu, t.x, o));
+            t.y = fmaxf(t.y, __shfl_xor_sync(0xFFFFFFFFu, t.y, o));
             if constexpr (FMT == CF_E4M3) {
-              const float v1 = fmaxf(vm[nt][h], tv);
-              vbase[h] = v1 == -INFINITY ? 0.f : v1;
-              fall[h] = ex2(vm[nt][h] - vbase[h]);
-              vm[nt][h] = v1;
+              tv.x = fmaxf(tv.x, __shfl_xor_sync(0xFFFFFFFFu, tv.x, o));
+              tv.y = fmaxf(tv.y, __shfl_xor_sync(0xFFFFFFFFu, tv.y, o));
             }
+          }
+          t = mul2(t, qs[nt]);
+          float2 fall, down, vdown;  // what old sums shrink by; the exponents' bases, negated
+          auto rebase = [](float& top, float now, float& f, float& d) {
+            const float m1 = fmaxf(top, now), base = m1 == -INFINITY ? 0.f : m1;
+            f = ex2(top - base);
+            top = m1;
+            d = -base;
+          };
+          rebase(m[nt].x, t.x, fall.x, down.x);
+          rebase(m[nt].y, t.y, fall.y, down.y);
+          l[nt] = mul2(l[nt], fall);
+          if constexpr (FMT == CF_E4M3) {
+            rebase(vm[nt].x, tv.x, fall.x, vdown.x);
+            rebase(vm[nt].y, tv.y, fall.y, vdown.y);
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float w[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float x = s[mt][nt][2 * e + h], pr = ex2(x - base[h]);
-                l[nt][h] += pr;
-                w[h] = FMT == CF_E4M3 ? ex2(x + lvs[mt][e] - vbase[h]) : pr;
-              }
-              // a masked token's scale is not read (its logit is -infinity, the sum NaN if its
-              // place held garbage): zero-filled, log2 -infinity, weight 0
+              const float2 x = fma2(s[mt][nt][e], qs[nt], down);
+              const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+              l[nt] = add2(l[nt], pr);
+              // (a masked token's logit is -infinity: weight 0)
               if constexpr (FMT == CF_E4M3) {
-                const __half2 hh = __floats2half2_rn(w[0], w[1]);
+                const float2 y = add2(sv[mt][e], vdown);
+                const __half2 hh = __floats2half2_rn(ex2(y.x), ex2(y.y));
                 pf[mt][nt][e] = movm(*reinterpret_cast<const uint32_t*>(&hh));
               } else {
-                const __nv_bfloat162 hh = __floats2bfloat162_rn(w[0], w[1]);
+                const __nv_bfloat162 hh = __float22bfloat162_rn(pr);
                 pf[mt][nt][e] = movm(*reinterpret_cast<const uint32_t*>(&hh));
               }
             }
-          if (__any_sync(0xFFFFFFFFu, fall[0] != 1.f || fall[1] != 1.f))
+          if (__any_sync(0xFFFFFFFFu, fall.x != 1.f || fall.y != 1.f))
 #pragma unroll
             for (int c = 0; c < KSTEPS; ++c)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[c][nt][e] *= fall[e & 1];
+              for (int e = 0; e < 2; ++e) acc[c][nt][e] = mul2(acc[c][nt][e], fall);
         }
         // ---- values: lane holds dims lane / 4 and + 8 of each 16 (E4M3: 2 (lane / 4) and + 1)
 #pragma unroll
@@ -591,7 +626,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
               uint32_t a[4];
               ldsm4t(a, vt + chunk_at<FMT, ROW>(16 * mt + (lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_bf16(acc[c][nt], a, pf[mt][nt][0], pf[mt][nt][1], acc[c][nt]);
+              for (int nt = 0; nt < NT; ++nt) mma2_bf16(acc[c][nt], a, pf[mt][nt]);
             }
           } else {
 #pragma unroll
@@ -606,7 +641,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
                 e4m3x4_f16x4(__byte_perm(v[2 * e + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(acc[c + e][nt], a, pf[mt][nt][0], pf[mt][nt][1], acc[c + e][nt]);
+                  mma2_f16(acc[c + e][nt], a, pf[mt][nt]);
               }
             }
           }
@@ -618,22 +653,26 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       // ---- the end of a part: join the warps, then write the result or leave a record
       const DecAt now = at;
       at.next(p, ulog);
-      if (at.x >= end || now.u == now.nu - 1) {
+      if (!at.in(end, whole_units) || now.u == now.nu - 1) {
         const bool whole = part_u0 == 0 && now.u == now.nu - 1;
         const int64_t row0 = (int64_t)now.b * p.Hq + head0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][h], o);
-            if (lane < 4) {
-              float* x = s_ml + (warp * HEADS + nt * 8 + 2 * lane + h) * 3;
-              x[0] = m[nt][h];
-              x[1] = l[nt][h];
-              x[2] = FMT == CF_E4M3 ? vm[nt][h] : m[nt][h];
-            }
+          for (int o = 4; o < 32; o <<= 1) {
+            l[nt].x += __shfl_xor_sync(0xFFFFFFFFu, l[nt].x, o);
+            l[nt].y += __shfl_xor_sync(0xFFFFFFFFu, l[nt].y, o);
           }
+          if (lane < 4) {
+            float* const x = s_ml + (warp * HEADS + nt * 8 + 2 * lane) * 3;
+            x[0] = m[nt].x;
+            x[1] = l[nt].x;
+            x[2] = FMT == CF_E4M3 ? vm[nt].x : m[nt].x;
+            x[3] = m[nt].y;
+            x[4] = l[nt].y;
+            x[5] = FMT == CF_E4M3 ? vm[nt].y : m[nt].y;
+          }
+        }
         float* const rec = p.parts + (2 * worker + part_slot) * C::REC;
         const int w0 = team << wlog;
         __syncwarp();  // all lanes have read the tile
@@ -649,11 +688,12 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 #pragma unroll
               for (int c = 0; c < KSTEPS; ++c) {
                 if constexpr (FMT == CF_BF16) {
-                  x[(16 * c + lane / 4) ^ ((lane & 3) << 3)] = acc[c][n0 + n][h];
-                  x[(16 * c + lane / 4 + 8) ^ ((lane & 3) << 3)] = acc[c][n0 + n][2 + h];
+                  x[(16 * c + lane / 4) ^ ((lane & 3) << 3)] = h ? acc[c][n0 + n][0].y : acc[c][n0 + n][0].x;
+                  x[(16 * c + lane / 4 + 8) ^ ((lane & 3) << 3)] = h ? acc[c][n0 + n][1].y : acc[c][n0 + n][1].x;
                 } else {
                   *reinterpret_cast<float2*>(x + ((16 * c + 2 * (lane / 4)) ^ ((lane & 3) << 3))) =
-                      make_float2(acc[c][n0 + n][h], acc[c][n0 + n][2 + h]);
+                      h ? make_float2(acc[c][n0 + n][0].y, acc[c][n0 + n][1].y)
+                        : make_float2(acc[c][n0 + n][0].x, acc[c][n0 + n][1].x);
                 }
               }
             }
@@ -736,7 +776,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             float4 v[BATCH];
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
-              // team c0's part is its first only where it begins there
+              // team c0's part is in its slot 0 where it begins at the team's first place
               const int at_second = j0 + j == 0 && x.i0 - x.c0 * chunk > 1;
               const float* y = p.parts + (2 * (int64_t)(x.c0 + j0 + j) + at_second) * C::REC;
               const bool on = j0 + j < x.parts;
