@@ -63,11 +63,11 @@ struct DecCfg {
   static constexpr int STAGE = KV + (FMT == CF_E4M3 ? 8 * TW : 0) + 16;  // rows, scales, mask
   static constexpr int HEADS = 8 * NT;
   static constexpr int RING = WARPS * STAGES * STAGE;
-  static constexpr int ML = WARPS * HEADS * 3 * 4;
+  static constexpr int ML = WARPS * HEADS * 2 * 4;
   static constexpr int SMEM = RING + ML + 1024;
   // n-tiles whose sums fit the stage of a tile that is read out (the join of a team's warps)
   static constexpr int PN = HEADS * DP * 4 <= KV ? NT : 1;
-  static constexpr int REC = HEADS * (DP + 2);  // floats of a record: sums, maxima, sums of weights
+  static constexpr int REC = HEADS * (DP + 2);  // floats of a record: sums, and each head's maximum and sum of weights
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && PN * 8 * DP * 4 <= KV, "does not fit");
 };
 
@@ -161,6 +161,11 @@ K3_DEVI int64_t div64(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
   return a / b;
 }
+// sum of a warp's non-negative numbers below 2^48
+K3_DEVI int64_t warp_sum(int64_t v) {
+  return ((int64_t)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)(v >> 24)) << 24) +
+         __reduce_add_sync(0xFFFFFFFFu, (uint32_t)v & 0xFFFFFFu);
+}
 // barrier of one team's threads
 K3_DEVI void team_sync(int team, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(team + 1), "r"(threads) : "memory");
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t ring = smem_u32(smem) + warp * STAGES * C::STAGE;
-  float* const s_ml = reinterpret_cast<float*>(smem + C::RING);  // [WARPS][HEADS] maxima, sums, value maxima
+  float* const s_ml = reinterpret_cast<float*>(smem + C::RING);  // [WARPS][HEADS] maxima, sums
   int64_t* const s_sum = reinterpret_cast<int64_t*>(smem + C::RING + C::ML);               // [WARPS]
   int64_t* const s_off = s_sum + DEC_MAX_WARPS;                                            // [teams]
   int32_t* const s_b = reinterpret_cast<int32_t*>(s_off + DEC_MAX_WARPS);                  // [teams]
@@ -275,20 +280,18 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   if (any_bad && blockIdx.x == 0) flag_status(p.status, K3ATTN_DEV_BAD_LENGTH);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    int64_t v = count[i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    const int64_t v = warp_sum(count[i]);
     if (lane == 0) s_count[warp * 4 + i] = v;
   }
   __syncthreads();
+  int64_t sums = lane < 4 * WARPS ? s_count[lane] : 0;  // lane i: of warp i / 4, of size i % 4; then of all warps
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) sums += __shfl_xor_sync(0xFFFFFFFFu, sums, o);
+  const int64_t v0 = __shfl_sync(0xFFFFFFFFu, sums, 0);
   int wlog = -1;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
-    int64_t v = 0, v0 = 0;
-    for (int w = 0; w < WARPS; ++w) {
-      v += s_count[w * 4 + i];
-      v0 += s_count[w * 4];
-    }
+    const int64_t v = __shfl_sync(0xFFFFFFFFu, sums, i);
     // the largest that wastes at most a quarter, or leaves warps idle anyway
     if (wlog < 0 && (1 << i) <= WARPS && (4 * v <= 5 * v0 || v * HR <= (int64_t)gridDim.x * WARPS)) wlog = i;
   }
@@ -354,7 +357,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     int32_t entry = 0, in_page = 0;
     uint32_t got[2] = {0, 0};  // arrivals before this team's (of its first thread)
 
-    constexpr int CPR = ROW / 16;  // 16-byte chunks of a row
+    // a copy takes LR 16-byte chunks (128 or 64 bytes) of each of 32 / LR rows
+    constexpr int CPR = ROW / 16, LR = CPR % 8 == 0 ? 8 : 4, RPI = 32 / LR;
     const int cpr = p.D * C::ES / 16;
     // row `lane` (of TW) of the tile at `ahead`
     auto row_token = [&]() { return ahead.first + (ahead.u * W + tw) * TW + (lane & (TW - 1)); };
@@ -369,12 +373,6 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     };
     auto issue = [&](int stage) {  // the copies of the tile at `ahead`
       const uint32_t st = ring + stage * C::STAGE;
-      if (ahead.u == 0 || ahead.x < 2) {  // a part's first tile: its queries will be wanted
-        const char* q = reinterpret_cast<const char*>(
-            p.q + ahead.b * p.q_stride + ((int64_t)ahead.kvh * p.G + ahead.grp * HEADS) * p.D);
-        const int bytes = min(HEADS, p.G - ahead.grp * HEADS) * p.D * 2;
-        for (int i = 128 * lane; i < bytes; i += 128 * 32) asm volatile("prefetch.global.L1 [%0];\n" ::"l"(q + i));
-      }
       const bool in = row_token() < ahead.n;
       const bool ok = in && entry >= 0 && entry < p.c.n_pages;
       if (in && !ok) flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
@@ -388,32 +386,37 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
         if (TW == 32 || lane < 16) cp_async4_or_zero(dst, p.c.ks + so, ok ? 4 : 0);
         if (TW == 32 || lane >= 16) cp_async4_or_zero(dst + 4 * TW, p.c.vs + so, ok ? 4 : 0);
       }
-      if (mask == 0xFFFFFFFFu && p.D == DP && 32 % CPR == 0 && __shfl_sync(0xFFFFFFFFu, in_page, 0) + TW <= p.c.page_size) {
+      if (mask == 0xFFFFFFFFu && p.D == DP && __shfl_sync(0xFFFFFFFFu, in_page, 0) + TW <= p.c.page_size) {
         // all rows there, on one page: they lie a token's stride apart
-        constexpr int RPI = 32 % CPR == 0 ? 32 / CPR : 1;
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + (lane / LR) * p.c.tok + 16 * (lane % LR);
         const int64_t step = RPI * p.c.tok;
-        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + (lane / CPR) * p.c.tok + 16 * (lane % CPR);
         const uint8_t *kp = p.c.k + o, *vp = p.c.v + o;
 #pragma unroll
-        for (int i = 0; i < TW * CPR / 32; ++i) {
-          const uint32_t dst = st + chunk_at<FMT, ROW>(i * RPI + lane / CPR, lane % CPR);
-          cp_async16(dst, kp);
-          cp_async16(dst + TW * ROW, vp);
+        for (int i = 0; i < TW / RPI; ++i) {
+          const uint32_t dst = st + chunk_at<FMT, ROW>(i * RPI + lane / LR, lane % LR);
+#pragma unroll
+          for (int c = 0; c < CPR / LR; ++c) {
+            cp_async16(dst + 16 * LR * c, kp + 16 * LR * c);
+            cp_async16(dst + TW * ROW + 16 * LR * c, vp + 16 * LR * c);
+          }
           kp += step;
           vp += step;
         }
         return;
       }
 #pragma unroll
-      for (int i = 0; i < TW * CPR / 32; ++i) {
-        const int r = (i * 32 + lane) / CPR, ch = (i * 32 + lane) % CPR;
-        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + 16 * ch;
-        const uint32_t n = (mask >> r) & 1u ? 16u : 0u;
-        if (ch < cpr) {
-          const uint32_t dst = st + chunk_at<FMT, ROW>(r, ch);
-          cp_async16_or_zero(dst, p.c.k + (n ? o : 0), n);
-          cp_async16_or_zero(dst + TW * ROW, p.c.v + (n ? o : 0), n);
-        }
+      for (int i = 0; i < TW / RPI; ++i) {
+        const int r = i * RPI + lane / LR;
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + 16 * (lane % LR);
+        const uint32_t n = (mask >> r) & 1u ? 16u : 0u;  // (a row that is not there: its place is zeroed)
+        const uint8_t *kp = p.c.k + (n ? o : 0), *vp = p.c.v + (n ? o : 0);
+        const uint32_t dst = st + chunk_at<FMT, ROW>(r, lane % LR);
+#pragma unroll
+        for (int c = 0; c < CPR / LR; ++c)
+          if (LR * c + lane % LR < cpr) {
+            cp_async16_or_zero(dst + 16 * LR * c, n ? kp + 16 * LR * c : kp, n);
+            cp_async16_or_zero(dst + TW * ROW + 16 * LR * c, n ? vp + 16 * LR * c : vp, n);
+          }
       }
     };
     // copies the tile at `ahead` (if it is the team's) and fetches the entries of the next
@@ -431,6 +434,35 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 
     float2 acc[KSTEPS][NT][2], m[NT], l[NT], vm[NT], qs[NT];  // pairs: of two heads
     uint32_t qf[KSTEPS][NT][2];
+    // a part's queries as they are, bf16 (step 4 j + i of an E4M3 contraction holds dims
+    // 64 j + 16 (lane % 4) + 4 i .. + 3).  bf16: loaded while the part before is joined (32 x 2000
+    // tokens, 24 query heads a key head: 35.9 us, 39.4 without); E4M3: at the part's start, as the
+    // registers' longer life costs its inner loop more (2 x 262143 tokens: 126.5 us, 138.7 early)
+    constexpr bool EARLY = FMT == CF_BF16;
+    auto load_queries = [&](const DecAt& a) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = a.grp * HEADS + nt * 8 + lane / 4;
+        const uint16_t* q = p.q + a.b * p.q_stride + ((int64_t)a.kvh * p.G + h) * p.D;
+        const bool on = h < p.G;
+#pragma unroll
+        for (int c = 0; c < KSTEPS; ++c) {
+          if constexpr (FMT == CF_BF16) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int d = 16 * c + 8 * e + 2 * (lane & 3);
+              qf[c][nt][e] = on && d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
+            }
+          } else {
+            const int d = 64 * (c / 4) + 16 * (lane & 3) + 4 * (c & 3);
+            const uint2 w = on && d < p.D ? ldg64(q + d) : make_uint2(0, 0);
+            qf[c][nt][0] = w.x;
+            qf[c][nt][1] = w.y;
+          }
+        }
+      }
+    };
+    if (EARLY) load_queries(at);
     int32_t part_u0 = 0, part_slot = 0;
     int stage = 0;
     for (bool begun = false; at.in(end, whole_units); begun = true) {
@@ -441,48 +473,33 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       const int64_t head0 = (int64_t)at.kvh * p.G + at.grp * HEADS;
 
       if (!begun || at.u == 0) {  // a new part: its queries, empty sums
+        if (!EARLY) load_queries(at);
         part_u0 = at.u;
         part_slot = at.u == 0 && at.x > 1;  // not the team's first place of all
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int h = nt * 8 + lane / 4;
-          const uint16_t* q = p.q + at.b * p.q_stride + (head0 + h) * p.D;
-          const bool on = h < heads;
-          if constexpr (FMT == CF_BF16) {
+          qs[nt] = make_float2(p.scale, p.scale);
+          if constexpr (FMT == CF_E4M3) {
+            // to fp16, scaled by the power of two that brings the row's largest into [2^14, 2^15)
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < KSTEPS; ++c)
+              mx = __vmaxu2(mx, __vmaxu2(qf[c][nt][0] & 0x7FFF7FFFu, qf[c][nt][1] & 0x7FFF7FFFu));
+            mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            const int pw = act_exp_from_max(max(mx & 0xFFFF0000u, mx << 16));
+            const float f1 = pow2f(pw >> 1), f2 = pow2f(pw - (pw >> 1));
 #pragma unroll
             for (int c = 0; c < KSTEPS; ++c)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int d = 16 * c + 8 * e + 2 * (lane & 3);
-                qf[c][nt][e] = on && d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
-              }
-            qs[nt] = make_float2(p.scale, p.scale);
-          } else {
-            // fp16, scaled by the power of two that brings the row's largest into [2^14, 2^15);
-            // step 4 j + i of the contraction holds dims 64 j + 16 (lane % 4) + 4 i .. + 3
-            uint2 raw[KSTEPS];
-            uint32_t mx = 0;
-#pragma unroll
-            for (int c = 0; c < KSTEPS; ++c) {
-              const int d = 64 * (c / 4) + 16 * (lane & 3) + 4 * (c & 3);
-              raw[c] = on && d < p.D ? ldg64(q + d) : make_uint2(0, 0);
-              mx = max(max(mx, raw[c].x & 0x7FFFu), max((raw[c].x >> 16) & 0x7FFFu, raw[c].y & 0x7FFFu));
-              mx = max(mx, (raw[c].y >> 16) & 0x7FFFu);
-            }
-            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            const int pw = act_exp_from_max(mx << 16);
-            const float f1 = pow2f(pw >> 1), f2 = pow2f(pw - (pw >> 1));
-#pragma unroll
-            for (int c = 0; c < KSTEPS; ++c) {
-              const uint32_t w[2] = {raw[c].x, raw[c].y};
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const __half2 hh = __floats2half2_rn(__uint_as_float(w[e] << 16) * f1 * f2,
-                                                     __uint_as_float(w[e] & 0xFFFF0000u) * f1 * f2);
+                const uint32_t w = qf[c][nt][e];
+                const float2 x = mul2(mul2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)),
+                                           make_float2(f1, f1)),
+                                      make_float2(f2, f2));
+                const __half2 hh = __float22half2_rn(x);
                 qf[c][nt][e] = *reinterpret_cast<const uint32_t*>(&hh);
               }
-            }
             // the scale's inverse, for the two heads whose logits this lane holds
             // (not below the normal numbers: a masked logit's -infinity times it stays one)
             const float inv = fmaxf(p.scale * pow2f(-(pw >> 1)) * pow2f((pw >> 1) - pw), 0x1p-126f);
@@ -656,6 +673,10 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       if (!at.in(end, whole_units) || now.u == now.nu - 1) {
         const bool whole = part_u0 == 0 && now.u == now.nu - 1;
         const int64_t row0 = (int64_t)now.b * p.Hq + head0;
+        float* const rec = p.parts + (2 * worker + part_slot) * C::REC;
+        // the warps trade maxima and sums of weights, bring their sums to the team's maximum and
+        // lay them out in the stage, where the team adds them up
+        const int w0 = team << wlog;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -663,77 +684,90 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             l[nt].x += __shfl_xor_sync(0xFFFFFFFFu, l[nt].x, o);
             l[nt].y += __shfl_xor_sync(0xFFFFFFFFu, l[nt].y, o);
           }
-          if (lane < 4) {
-            float* const x = s_ml + (warp * HEADS + nt * 8 + 2 * lane) * 3;
-            x[0] = m[nt].x;
-            x[1] = l[nt].x;
-            x[2] = FMT == CF_E4M3 ? vm[nt].x : m[nt].x;
-            x[3] = m[nt].y;
-            x[4] = l[nt].y;
-            x[5] = FMT == CF_E4M3 ? vm[nt].y : m[nt].y;
+          if (lane < 4)
+            *reinterpret_cast<float4*>(s_ml + 2 * (warp * HEADS + nt * 8 + 2 * lane)) =
+                make_float4(m[nt].x, l[nt].x, m[nt].y, l[nt].y);
+        }
+        team_sync(team, tthreads);
+        float2 f[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float4 ml[WARPS];
+          float2 top = make_float2(-INFINITY, -INFINITY), sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) {
+            ml[w] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            if (w < W) ml[w] = *reinterpret_cast<const float4*>(s_ml + 2 * ((w0 + w) * HEADS + nt * 8 + 2 * (lane & 3)));
+            top = make_float2(fmaxf(top.x, ml[w].x), fmaxf(top.y, ml[w].z));
+          }
+          const float2 base = make_float2(top.x == -INFINITY ? 0.f : top.x, top.y == -INFINITY ? 0.f : top.y);
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) {
+            sum.x = fmaf(ml[w].y, ex2(ml[w].x - base.x), sum.x);
+            sum.y = fmaf(ml[w].w, ex2(ml[w].z - base.y), sum.y);
+          }
+          if constexpr (FMT == CF_E4M3)
+            f[nt] = make_float2(ex2(vm[nt].x - base.x), ex2(vm[nt].y - base.y));
+          else
+            f[nt] = make_float2(ex2(m[nt].x - base.x), ex2(m[nt].y - base.y));
+          if (whole) {  // (a sum of 0: nothing was attended to, the sums are 0 too)
+            f[nt].x = sum.x == 0.f ? 0.f : f[nt].x / sum.x;
+            f[nt].y = sum.y == 0.f ? 0.f : f[nt].y / sum.y;
+          }
+          const int h = nt * 8 + 2 * (lane & 3);
+          if (tw == 0 && lane < 4 && h < heads) {
+            if (!whole) {
+              *reinterpret_cast<float2*>(rec + HEADS * DP + 2 * h) = make_float2(top.x, sum.x);
+              *reinterpret_cast<float2*>(rec + HEADS * DP + 2 * h + 2) = make_float2(top.y, sum.y);
+            } else if (p.lse) {
+              p.lse[row0 + h] = lse_of(base.x, sum.x);
+              if (h + 1 < heads) p.lse[row0 + h + 1] = lse_of(base.y, sum.y);
+            }
           }
         }
-        float* const rec = p.parts + (2 * worker + part_slot) * C::REC;
-        const int w0 = team << wlog;
-        __syncwarp();  // all lanes have read the tile
+        float* const mine_out = reinterpret_cast<float*>(smem + warp * STAGES * C::STAGE + used);
 #pragma unroll
         for (int n0 = 0; n0 < NT; n0 += C::PN) {
           // dim d of head h at d ^ (h / 2 % 4 * 8): the heads of a fragment lie in different banks
 #pragma unroll
           for (int n = 0; n < C::PN; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float* const x = reinterpret_cast<float*>(smem + warp * STAGES * C::STAGE + used) +
-                               (8 * n + 2 * (lane & 3) + h) * DP;
-#pragma unroll
-              for (int c = 0; c < KSTEPS; ++c) {
-                if constexpr (FMT == CF_BF16) {
-                  x[(16 * c + lane / 4) ^ ((lane & 3) << 3)] = h ? acc[c][n0 + n][0].y : acc[c][n0 + n][0].x;
-                  x[(16 * c + lane / 4 + 8) ^ ((lane & 3) << 3)] = h ? acc[c][n0 + n][1].y : acc[c][n0 + n][1].x;
-                } else {
-                  *reinterpret_cast<float2*>(x + ((16 * c + 2 * (lane / 4)) ^ ((lane & 3) << 3))) =
-                      h ? make_float2(acc[c][n0 + n][0].y, acc[c][n0 + n][1].y)
-                        : make_float2(acc[c][n0 + n][0].x, acc[c][n0 + n][1].x);
-                }
+            for (int c = 0; c < KSTEPS; ++c) {
+              const float2 a = mul2(acc[c][n0 + n][0], f[n0 + n]), b = mul2(acc[c][n0 + n][1], f[n0 + n]);
+              float* const x = mine_out + (8 * n + 2 * (lane & 3)) * DP;
+              if constexpr (FMT == CF_BF16) {
+                const int d0 = (16 * c + lane / 4) ^ ((lane & 3) << 3), d1 = (16 * c + lane / 4 + 8) ^ ((lane & 3) << 3);
+                x[d0] = a.x;
+                x[d1] = b.x;
+                x[DP + d0] = a.y;
+                x[DP + d1] = b.y;
+              } else {
+                const int d0 = (16 * c + 2 * (lane / 4)) ^ ((lane & 3) << 3);
+                *reinterpret_cast<float2*>(x + d0) = make_float2(a.x, b.x);
+                *reinterpret_cast<float2*>(x + DP + d0) = make_float2(a.y, b.y);
               }
             }
+          if (EARLY && n0 + C::PN >= NT && at.in(end, whole_units)) load_queries(at);
           team_sync(team, tthreads);
           const int hs = min(heads - 8 * n0, 8 * C::PN);
+#pragma unroll 2
           for (int i = tthread; i < hs * (DP / 4); i += tthreads) {
             const int hp = i / (DP / 4), h = 8 * n0 + hp, d = 4 * (i % (DP / 4));
-            float top = -INFINITY;
+            const uint8_t* const x = smem + w0 * STAGES * C::STAGE + used + 4 * (hp * DP + (d ^ ((hp >> 1 & 3) << 3)));
+            float4 o = *reinterpret_cast<const float4*>(x);
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w)
-              if (w < W) top = fmaxf(top, s_ml[((w0 + w) * HEADS + h) * 3]);
-            const float base = top == -INFINITY ? 0.f : top;
-            float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
+            for (int w = 1; w < WARPS; ++w) {
               if (w >= W) continue;
-              const float* x = s_ml + ((w0 + w) * HEADS + h) * 3;
-              sum += x[1] * ex2(x[0] - base);
-              const float f = ex2(x[2] - base);
-              const float4 v = *reinterpret_cast<const float4*>(
-                  reinterpret_cast<const float*>(smem + (w0 + w) * STAGES * C::STAGE + used) + hp * DP +
-                  (d ^ ((hp >> 1 & 3) << 3)));
-              o[0] = fmaf(v.x, f, o[0]);
-              o[1] = fmaf(v.y, f, o[1]);
-              o[2] = fmaf(v.z, f, o[2]);
-              o[3] = fmaf(v.w, f, o[3]);
+              const float4 v = *reinterpret_cast<const float4*>(x + w * STAGES * C::STAGE);
+              o.x += v.x;
+              o.y += v.y;
+              o.z += v.z;
+              o.w += v.w;
             }
-            if (whole) {  // (a sum of 0: nothing was attended to)
-              const float r = sum == 0.f ? 0.f : 1.f / sum;
-              if (d < p.D)
-                *reinterpret_cast<uint2*>(p.out + (row0 + h) * p.D + d) =
-                    bf16x4(o[0] * r, o[1] * r, o[2] * r, o[3] * r);
-              if (d == 0 && p.lse) p.lse[row0 + h] = lse_of(base, sum);
-            } else {
-              __stcg(reinterpret_cast<float4*>(rec + h * DP + d), make_float4(o[0], o[1], o[2], o[3]));
-              if (d == 0) {
-                __stcg(rec + HEADS * DP + h, top);
-                __stcg(rec + HEADS * DP + HEADS + h, sum);
-              }
-            }
+            if (!whole)
+              *reinterpret_cast<float4*>(rec + h * DP + d) = o;
+            else if (d < p.D)
+              *reinterpret_cast<uint2*>(p.out + (row0 + h) * p.D + d) = bf16x4(o.x, o.y, o.z, o.w);
           }
           team_sync(team, tthreads);
         }
@@ -766,45 +800,67 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       if (s_last[team]) {
         const DecPart x = s_part[2 * team + slot];
         if (tthread == 0) p.arrived[x.c0] = 0;
-        constexpr int BATCH = 8;
-        for (int i = tthread; i < x.heads * (DP / 4); i += tthreads) {
-          const int h = i / (DP / 4), d = 4 * (i % (DP / 4));
-          if (d >= p.D) continue;
-          float top = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        // SIDE quads of dims a thread and BATCH records at a time, whose loads are in flight together
+        constexpr int QUADS = HEADS * DP / 4 / THREADS, SIDE = QUADS >= 4 ? 4 : QUADS >= 2 ? 2 : 1, BATCH = 8 / SIDE;
+        for (int i0 = tthread; i0 < x.heads * (DP / 4); i0 += SIDE * tthreads) {
+          float top[SIDE], sum[SIDE], o[SIDE][4];
+          int h[SIDE], d[SIDE];
+#pragma unroll
+          for (int s = 0; s < SIDE; ++s) {
+            const int i = i0 + s * tthreads;
+            h[s] = i / (DP / 4);
+            d[s] = 4 * (i % (DP / 4));
+            top[s] = -INFINITY;
+            sum[s] = o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
+          }
           for (int j0 = 0; j0 < x.parts; j0 += BATCH) {
-            float mj[BATCH], lj[BATCH];
-            float4 v[BATCH];
+            float2 ml[SIDE][BATCH];
+            float4 v[SIDE][BATCH];
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
               // team c0's part is in its slot 0 where it begins at the team's first place
               const int at_second = j0 + j == 0 && x.i0 - x.c0 * chunk > 1;
               const float* y = p.parts + (2 * (int64_t)(x.c0 + j0 + j) + at_second) * C::REC;
-              const bool on = j0 + j < x.parts;
-              mj[j] = on ? __ldcg(y + HEADS * DP + h) : -INFINITY;
-              lj[j] = on ? __ldcg(y + HEADS * DP + HEADS + h) : 0.f;
-              v[j] = on ? __ldcg(reinterpret_cast<const float4*>(y + h * DP + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int s = 0; s < SIDE; ++s) {
+                ml[s][j] = make_float2(-INFINITY, 0.f);
+                v[s][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < x.parts && h[s] < x.heads) {
+                  ml[s][j] = __ldcg(reinterpret_cast<const float2*>(y + HEADS * DP + 2 * h[s]));
+                  v[s][j] = __ldcg(reinterpret_cast<const float4*>(y + h[s] * DP + d[s]));
+                }
+              }
             }
-            float m1 = top;
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) m1 = fmaxf(m1, mj[j]);
-            const float base = m1 == -INFINITY ? 0.f : m1, fall = ex2(top - base);
-            top = m1;
-            sum *= fall;
+            for (int s = 0; s < SIDE; ++s) {
+              float m1 = top[s];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] *= fall;
+              for (int j = 0; j < BATCH; ++j) m1 = fmaxf(m1, ml[s][j].x);
+              const float base = m1 == -INFINITY ? 0.f : m1, fall = ex2(top[s] - base);
+              top[s] = m1;
+              sum[s] *= fall;
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-              const float f = ex2(mj[j] - base);
-              sum = fmaf(lj[j], f, sum);
-              o[0] = fmaf(v[j].x, f, o[0]);
-              o[1] = fmaf(v[j].y, f, o[1]);
-              o[2] = fmaf(v[j].z, f, o[2]);
-              o[3] = fmaf(v[j].w, f, o[3]);
+              for (int e = 0; e < 4; ++e) o[s][e] *= fall;
+#pragma unroll
+              for (int j = 0; j < BATCH; ++j) {
+                const float f = ex2(ml[s][j].x - base);
+                sum[s] = fmaf(ml[s][j].y, f, sum[s]);
+                o[s][0] = fmaf(v[s][j].x, f, o[s][0]);
+                o[s][1] = fmaf(v[s][j].y, f, o[s][1]);
+                o[s][2] = fmaf(v[s][j].z, f, o[s][2]);
+                o[s][3] = fmaf(v[s][j].w, f, o[s][3]);
+              }
             }
           }
-          const float r = sum == 0.f ? 0.f : 1.f / sum;
-          *reinterpret_cast<uint2*>(p.out + (x.row + h) * p.D + d) = bf16x4(o[0] * r, o[1] * r, o[2] * r, o[3] * r);
-          if (d == 0 && p.lse) p.lse[x.row + h] = lse_of(top, sum);
+#pragma unroll
+          for (int s = 0; s < SIDE; ++s) {
+            if (h[s] >= x.heads) continue;
+            const float r = sum[s] == 0.f ? 0.f : 1.f / sum[s];
+            if (d[s] < p.D)
+              *reinterpret_cast<uint2*>(p.out + (x.row + h[s]) * p.D + d[s]) =
+                  bf16x4(o[s][0] * r, o[s][1] * r, o[s][2] * r, o[s][3] * r);
+            if (d[s] == 0 && p.lse) p.lse[x.row + h[s]] = lse_of(top[s], sum[s]);
+          }
         }
       }
       team_sync(team, tthreads);
