@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   int32_t* const s_b = reinterpret_cast<int32_t*>(s_off + DEC_MAX_WARPS);                  // [teams]
   volatile int32_t* const s_last = s_b + DEC_MAX_WARPS;                                    // [teams]
   int64_t* const s_count = reinterpret_cast<int64_t*>(smem + C::RING + C::ML + 256);       // [WARPS][4]
-  DecPart* const s_part = reinterpret_cast<DecPart*>(smem + C::RING + C::ML + 256);        // [teams][2]
-  static_assert(2 * DEC_MAX_WARPS * sizeof(DecPart) <= 768 && DEC_MAX_WARPS * 32 <= 256, "shared layout");
+  DecPart* const s_part = reinterpret_cast<DecPart*>(smem + C::RING + C::ML + 512);        // [teams][2]
+  static_assert(2 * DEC_MAX_WARPS * sizeof(DecPart) <= 512 && DEC_MAX_WARPS * 32 <= 256, "shared layout");
 
   // dims past D: zero in every stage, never written again
   if (p.D < DP)
@@ -263,14 +263,17 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- the teams' size: the tiles that teams of 1, 2, 4 and 8 warps would take, with the idle
-  // warps of every sequence's last unit
+  // ---- the teams' size, and the units of this team: every thread counts its sequences' tiles as
+  // teams of 1, 2, 4 and 8 warps would take them (with the idle warps of a sequence's last unit).
+  // Up to 32 sequences: a lane has one, every warp has them all; more: the block has them.
   const int32_t HR = p.Hkv * p.groups;
-  const int seqs = (p.B + THREADS - 1) / THREADS;
-  const int b_lo = min(p.B, (int)threadIdx.x * seqs), b_hi = min(p.B, b_lo + seqs);
+  const bool few = p.B <= 32;
+  const int seqs = few ? 1 : (p.B + THREADS - 1) / THREADS, first_b = few ? lane : (int)threadIdx.x * seqs;
+  const int b_lo = min(p.B, first_b), b_hi = min(p.B, b_lo + seqs);
   DecAt at;
   int64_t count[4] = {0, 0, 0, 0}, some = 0;
   bool any_bad = false;
+  at.nu = at.n = at.first = 0;
   for (at.b = b_lo; at.b < b_hi; ++at.b) {
     any_bad |= !at.open(p, C::TLOG);
 #pragma unroll
@@ -278,72 +281,91 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     some += at.nu > 0;
   }
   if (any_bad && blockIdx.x == 0) flag_status(p.status, K3ATTN_DEV_BAD_LENGTH);
+  int64_t sums[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t v = warp_sum(count[i]);
-    if (lane == 0) s_count[warp * 4 + i] = v;
+  for (int i = 0; i < 4; ++i) sums[i] = warp_sum(count[i]);
+  if (!few) {
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_count[warp * 4 + i] = sums[i];
+    __syncthreads();
+    int64_t v = lane < 4 * WARPS ? s_count[lane] : 0;  // lane i: of warp i / 4, of size i % 4; then of all warps
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[i] = __shfl_sync(0xFFFFFFFFu, v, i);
   }
-  __syncthreads();
-  int64_t sums = lane < 4 * WARPS ? s_count[lane] : 0;  // lane i: of warp i / 4, of size i % 4; then of all warps
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) sums += __shfl_xor_sync(0xFFFFFFFFu, sums, o);
-  const int64_t v0 = __shfl_sync(0xFFFFFFFFu, sums, 0);
   int wlog = -1;
 #pragma unroll
-  for (int i = 3; i >= 0; --i) {
-    const int64_t v = __shfl_sync(0xFFFFFFFFu, sums, i);
-    // the largest that wastes at most a quarter, or leaves warps idle anyway
-    if (wlog < 0 && (1 << i) <= WARPS && (4 * v <= 5 * v0 || v * HR <= (int64_t)gridDim.x * WARPS)) wlog = i;
-  }
+  for (int i = 3; i >= 0; --i)  // the largest that wastes at most a quarter, or leaves warps idle anyway
+    if (wlog < 0 && (1 << i) <= WARPS && (4 * sums[i] <= 5 * sums[0] || sums[i] * HR <= (int64_t)gridDim.x * WARPS))
+      wlog = i;
   const int W = 1 << wlog, ulog = C::TLOG + wlog, teams = WARPS >> wlog, team = warp >> wlog, tw = warp & (W - 1);
   const int whole_units = DEC_WHOLE >> wlog;
   const int tthreads = 32 << wlog, tthread = threadIdx.x & (tthreads - 1);
 
-  // ---- the teams' units: the sequences that hold their first ones
   const int64_t mine = ((wlog == 0 ? count[0] : wlog == 1 ? count[1] : wlog == 2 ? count[2] : count[3]) >> wlog) + some;
-  int64_t upto = mine;
+  int64_t upto = mine, total;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
     if (lane >= o) upto += v;
   }
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < WARPS; ++w) {
-    if (w == warp) upto += total;
-    total += s_sum[w];
+  if (few) {
+    total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  } else {
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w == warp) upto += total;
+      total += s_sum[w];
+    }
   }
   total *= HR;
   const int64_t workers = (int64_t)gridDim.x * teams, chunk = max((int64_t)1, div64(total + workers - 1, workers));
-  if (mine > 0) {
-    const int64_t lo = (upto - mine) * HR, hi = upto * HR;
-    for (int i = 0; i < teams; ++i) {
-      const int64_t x = ((int64_t)blockIdx.x * teams + i) * chunk;
-      if (x < lo || x >= hi) continue;
-      int64_t before = lo;
-      for (at.b = b_lo;; ++at.b) {
-        at.open(p, ulog);
-        const int64_t here = at.nu > 0 ? (int64_t)(at.nu + 1) * HR : 0;
-        if (x < before + here) break;
-        before += here;
+  const int64_t worker = (int64_t)blockIdx.x * teams + team, unit0 = worker * chunk;
+  const int64_t lo = (upto - mine) * HR, hi = upto * HR;  // this thread's units
+  int64_t off = 0;  // the team's first unit, from the first one of its sequence
+  if (few) {
+    const uint32_t has = __ballot_sync(0xFFFFFFFFu, mine > 0 && unit0 >= lo && unit0 < hi);
+    const int from = has ? __ffs(has) - 1 : 0;
+    off = unit0 - __shfl_sync(0xFFFFFFFFu, lo, from);
+    at.b = from;
+    at.n = __shfl_sync(0xFFFFFFFFu, at.n, from);
+    at.first = __shfl_sync(0xFFFFFFFFu, at.first, from);
+    at.nu = (int32_t)(((uint32_t)(at.n - at.first) + (1u << ulog) - 1) >> ulog);
+  } else {
+    if (mine > 0) {
+      for (int i = 0; i < teams; ++i) {
+        const int64_t x = ((int64_t)blockIdx.x * teams + i) * chunk;
+        if (x < lo || x >= hi) continue;
+        int64_t before = lo;
+        for (at.b = b_lo;; ++at.b) {
+          at.open(p, ulog);
+          const int64_t here = at.nu > 0 ? (int64_t)(at.nu + 1) * HR : 0;
+          if (x < before + here) break;
+          before += here;
+        }
+        s_b[i] = at.b;
+        s_off[i] = x - before;
       }
-      s_b[i] = at.b;
-      s_off[i] = x - before;
+    }
+    __syncthreads();
+    if (unit0 < total) {
+      at.b = s_b[team];
+      off = s_off[team];
+      at.open(p, ulog);
     }
   }
-  __syncthreads();
 
-  const int64_t worker = (int64_t)blockIdx.x * teams + team, unit0 = worker * chunk;
   const int32_t end = (int32_t)max((int64_t)0, min(min(total - unit0, chunk), (int64_t)INT32_MAX));
   if (tthread < 2) s_part[2 * team + tthread].there = 0;
   if (end > 0) {
-    at.b = s_b[team];
-    at.open(p, ulog);
-    const int32_t hr = (int32_t)div64(s_off[team], at.nu + 1);
+    const int32_t hr = (int32_t)div64(off, at.nu + 1);
     at.kvh = hr / p.groups;
     at.grp = hr - at.kvh * p.groups;
-    at.u = (int32_t)(s_off[team] - (int64_t)hr * (at.nu + 1)) - 1;
+    at.u = (int32_t)(off - (int64_t)hr * (at.nu + 1)) - 1;
     at.x = 0;
     if (at.u < 0) {  // a sequence's start
       at.u = 0;
