@@ -86,30 +86,21 @@ def declared_functions() -> list:
 
 
 # ------------------------------------------------------------------------------ checks
-# (a decode step's call takes a few microseconds on the GPU: the checks are comparisons alone,
-# and a message is put together only where one fails)
+# (a decode step's call takes a few microseconds on the GPU: the operators below check in line,
+# by comparisons alone, and a message is put together only where one fails)
 _bf16, _f32, _i32, _f64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.float64, torch.uint8
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _refuse(t, name, dtype, shape, how=""):
+def _refuse(t, name, dtype, shape, how=", contiguous"):
     got = f"{list(t.shape)} (strides {list(t.stride())}) of {t.dtype} on {t.device}" if torch.is_tensor(t) else repr(t)
     raise ValueError(f"{name}: a CUDA tensor {list(shape)} of {dtype}{how} is needed, got {got}")
 
 
-def _dense(t, name, dtype, shape):
-    """Pointer of a contiguous tensor."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, ", contiguous")
-    return t.data_ptr()
-
-
 def _rows(t, name, T, heads, D):
     """Pointer and token stride of a [T, heads, D] bf16 tensor whose tokens' rows are dense."""
-    if not (t.dtype is _bf16 and t.shape == (T, heads, D) and t.is_cuda):
-        _refuse(t, name, _bf16, (T, heads, D))
-    sT, sH, sD = t.stride()
-    if sD != 1 or (sH != D and heads != 1):
+    sT, sH, sD = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if not (t.dtype is _bf16 and t.shape == (T, heads, D) and t.is_cuda and sD == 1 and (sH == D or heads == 1)):
         _refuse(t, name, _bf16, (T, heads, D), ", the heads of a token dense,")
     return t.data_ptr(), sT if T > 1 else heads * D
 
@@ -120,15 +111,15 @@ def _ws(ws):
     return ws.data_ptr(), ws.numel()
 
 
-def _launch(fn, t, stream, *args):
-    """Calls fn(*args, stream): on `stream`, or the current stream of t's device."""
+def _on(t, stream):
+    """The stream of a call: `stream`, or the current one of t's device."""
     if stream is None:
-        s = _raw_stream(t.device.index)
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-    code = fn(*args, s)
-    if code:
-        raise K3MoEError(code, fn.__name__)
+        return _raw_stream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _fail(code, what):
+    raise K3MoEError(code, what)
 
 
 # ------------------------------------------------------------------------------ what a program keeps
@@ -148,7 +139,9 @@ def workspace(d: Dims, device="cuda"):
 
 def workspace_init(ws, stream=None):
     """k3attn_workspace_init: readies a workspace (also clears its status word)."""
-    _launch(_funcs().k3attn_workspace_init, ws, stream, *_ws(ws))
+    code = _funcs().k3attn_workspace_init(*_ws(ws), _on(ws, stream))
+    if code:
+        _fail(code, "k3attn_workspace_init")
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
@@ -202,8 +195,20 @@ def _cache(d, cache):
 
 
 # ------------------------------------------------------------------------------ the operators
-def _freq(d, inv_freq):
-    return _dense(inv_freq, "inv_freq", _f64, (d.rot_dim // 2,)) if d.rot_dim else None
+def _norm_args(d, T, D, positions, inv_freq, q_w, k_w):
+    """Pointers of what the norms and the rotation read beside the rows."""
+    if not (positions.dtype is _i32 and positions.shape == (T,) and positions.is_cuda and positions.is_contiguous()):
+        _refuse(positions, "positions", _i32, (T,))
+    if not (q_w.dtype is _f32 and q_w.shape == (D,) and q_w.is_cuda and q_w.is_contiguous()):
+        _refuse(q_w, "q_w", _f32, (D,))
+    if not (k_w.dtype is _f32 and k_w.shape == (D,) and k_w.is_cuda and k_w.is_contiguous()):
+        _refuse(k_w, "k_w", _f32, (D,))
+    R = d.rot_dim
+    if R == 0:
+        return positions.data_ptr(), None, q_w.data_ptr(), k_w.data_ptr()
+    if not (inv_freq.dtype is _f64 and inv_freq.shape == (R // 2,) and inv_freq.is_cuda and inv_freq.is_contiguous()):
+        _refuse(inv_freq, "inv_freq", _f64, (R // 2,))
+    return positions.data_ptr(), inv_freq.data_ptr(), q_w.data_ptr(), k_w.data_ptr()
 
 
 def qk_norm_rope(d: Dims, q, k, positions, inv_freq, q_w, k_w, q_out, k_out, stream=None):
@@ -211,17 +216,30 @@ def qk_norm_rope(d: Dims, q, k, positions, inv_freq, q_w, k_w, q_out, k_out, str
     will do) -> q_out, k_out, dense, normed per head and rotated.  inv_freq may be None when
     d.rot_dim is 0."""
     T, Hq, Hkv, D = q.shape[0], d.n_heads, d.n_kv_heads, d.head_dim
-    _launch(_funcs().k3attn_qk_norm_rope, q, stream, d.ref, T, *_rows(q, "q", T, Hq, D), *_rows(k, "k", T, Hkv, D),
-            _dense(positions, "positions", _i32, (T,)), _freq(d, inv_freq), _dense(q_w, "q_w", _f32, (D,)),
-            _dense(k_w, "k_w", _f32, (D,)), _dense(q_out, "q_out", _bf16, (T, Hq, D)),
-            _dense(k_out, "k_out", _bf16, (T, Hkv, D)))
+    qp, qs = _rows(q, "q", T, Hq, D)
+    kp, ks = _rows(k, "k", T, Hkv, D)
+    pos, freq, qw, kw = _norm_args(d, T, D, positions, inv_freq, q_w, k_w)
+    if not (q_out.dtype is _bf16 and q_out.shape == (T, Hq, D) and q_out.is_cuda and q_out.is_contiguous()):
+        _refuse(q_out, "q_out", _bf16, (T, Hq, D))
+    if not (k_out.dtype is _bf16 and k_out.shape == (T, Hkv, D) and k_out.is_cuda and k_out.is_contiguous()):
+        _refuse(k_out, "k_out", _bf16, (T, Hkv, D))
+    code = _funcs().k3attn_qk_norm_rope(d.ref, T, qp, qs, kp, ks, pos, freq, qw, kw, q_out.data_ptr(),
+                                        k_out.data_ptr(), _on(q, stream))
+    if code:
+        _fail(code, "k3attn_qk_norm_rope")
 
 
 def kv_write(d: Dims, k, v, slots, cache: KVCache, ws, stream=None):
     """k3attn_kv_write: k, v [T, Hkv, D] bf16 into the cache at slots [T] int32 (-1: not written)."""
     T, Hkv, D = k.shape[0], d.n_kv_heads, d.head_dim
-    _launch(_funcs().k3attn_kv_write, k, stream, d.ref, T, *_rows(k, "k", T, Hkv, D), *_rows(v, "v", T, Hkv, D),
-            _dense(slots, "slots", _i32, (T,)), _cache(d, cache), *_ws(ws))
+    kp, ks = _rows(k, "k", T, Hkv, D)
+    vp, vs = _rows(v, "v", T, Hkv, D)
+    if not (slots.dtype is _i32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()):
+        _refuse(slots, "slots", _i32, (T,))
+    code = _funcs().k3attn_kv_write(d.ref, T, kp, ks, vp, vs, slots.data_ptr(), _cache(d, cache), *_ws(ws),
+                                    _on(k, stream))
+    if code:
+        _fail(code, "k3attn_kv_write")
 
 
 def kv_append(d: Dims, q, k, v, positions, slots, inv_freq, q_w, k_w, cache: KVCache, q_out, ws, k_out=None,
@@ -229,26 +247,59 @@ def kv_append(d: Dims, q, k, v, positions, slots, inv_freq, q_w, k_w, cache: KVC
     """k3attn_kv_append: qk_norm_rope of q into q_out and of k, and the write of k and v into the
     cache, in one pass; k_out (optional) also receives the keys."""
     T, Hq, Hkv, D = q.shape[0], d.n_heads, d.n_kv_heads, d.head_dim
-    _launch(_funcs().k3attn_kv_append, q, stream, d.ref, T, *_rows(q, "q", T, Hq, D), *_rows(k, "k", T, Hkv, D),
-            *_rows(v, "v", T, Hkv, D), _dense(positions, "positions", _i32, (T,)),
-            _dense(slots, "slots", _i32, (T,)), _freq(d, inv_freq), _dense(q_w, "q_w", _f32, (D,)),
-            _dense(k_w, "k_w", _f32, (D,)), _cache(d, cache), _dense(q_out, "q_out", _bf16, (T, Hq, D)),
-            None if k_out is None else _dense(k_out, "k_out", _bf16, (T, Hkv, D)), *_ws(ws))
+    qp, qs = _rows(q, "q", T, Hq, D)
+    kp, ks = _rows(k, "k", T, Hkv, D)
+    vp, vs = _rows(v, "v", T, Hkv, D)
+    pos, freq, qw, kw = _norm_args(d, T, D, positions, inv_freq, q_w, k_w)
+    if not (slots.dtype is _i32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()):
+        _refuse(slots, "slots", _i32, (T,))
+    if not (q_out.dtype is _bf16 and q_out.shape == (T, Hq, D) and q_out.is_cuda and q_out.is_contiguous()):
+        _refuse(q_out, "q_out", _bf16, (T, Hq, D))
+    ko = None
+    if k_out is not None:
+        if not (k_out.dtype is _bf16 and k_out.shape == (T, Hkv, D) and k_out.is_cuda and k_out.is_contiguous()):
+            _refuse(k_out, "k_out", _bf16, (T, Hkv, D))
+        ko = k_out.data_ptr()
+    code = _funcs().k3attn_kv_append(d.ref, T, qp, qs, kp, ks, vp, vs, pos, slots.data_ptr(), freq, qw, kw,
+                                     _cache(d, cache), q_out.data_ptr(), ko, *_ws(ws), _on(q, stream))
+    if code:
+        _fail(code, "k3attn_kv_append")
 
 
 def kv_read(d: Dims, slots, cache: KVCache, k_out, v_out, ws, stream=None):
     """k3attn_kv_read: the rows at slots [T] int32 as bf16, k_out and v_out [T, Hkv, D]."""
     T, Hkv, D = slots.shape[0], d.n_kv_heads, d.head_dim
-    _launch(_funcs().k3attn_kv_read, slots, stream, d.ref, T, _dense(slots, "slots", _i32, (T,)), _cache(d, cache),
-            _dense(k_out, "k_out", _bf16, (T, Hkv, D)), _dense(v_out, "v_out", _bf16, (T, Hkv, D)), *_ws(ws))
+    if not (slots.dtype is _i32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()):
+        _refuse(slots, "slots", _i32, (T,))
+    if not (k_out.dtype is _bf16 and k_out.shape == (T, Hkv, D) and k_out.is_cuda and k_out.is_contiguous()):
+        _refuse(k_out, "k_out", _bf16, (T, Hkv, D))
+    if not (v_out.dtype is _bf16 and v_out.shape == (T, Hkv, D) and v_out.is_cuda and v_out.is_contiguous()):
+        _refuse(v_out, "v_out", _bf16, (T, Hkv, D))
+    code = _funcs().k3attn_kv_read(d.ref, T, slots.data_ptr(), _cache(d, cache), k_out.data_ptr(), v_out.data_ptr(),
+                                   *_ws(ws), _on(slots, stream))
+    if code:
+        _fail(code, "k3attn_kv_read")
 
 
 def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None):
     """k3attn_decode: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
     of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32."""
     B, Hq, D = q.shape[0], d.n_heads, d.head_dim
+    qp, qs = _rows(q, "q", B, Hq, D)
     width = page_table.shape[-1]
-    _launch(_funcs().k3attn_decode, q, stream, d.ref, B, *_rows(q, "q", B, Hq, D), _cache(d, cache),
-            _dense(page_table, "page_table", _i32, (B, width)), width, _dense(lens, "lens", _i32, (B,)),
-            _dense(out, "out", _bf16, (B, Hq, D)), None if lse is None else _dense(lse, "lse", _f32, (B, Hq)),
-            *_ws(ws))
+    if not (page_table.dtype is _i32 and page_table.shape == (B, width) and page_table.is_cuda
+            and page_table.is_contiguous()):
+        _refuse(page_table, "page_table", _i32, (B, "width"))
+    if not (lens.dtype is _i32 and lens.shape == (B,) and lens.is_cuda and lens.is_contiguous()):
+        _refuse(lens, "lens", _i32, (B,))
+    if not (out.dtype is _bf16 and out.shape == (B, Hq, D) and out.is_cuda and out.is_contiguous()):
+        _refuse(out, "out", _bf16, (B, Hq, D))
+    lp = None
+    if lse is not None:
+        if not (lse.dtype is _f32 and lse.shape == (B, Hq) and lse.is_cuda and lse.is_contiguous()):
+            _refuse(lse, "lse", _f32, (B, Hq))
+        lp = lse.data_ptr()
+    code = _funcs().k3attn_decode(d.ref, B, qp, qs, _cache(d, cache), page_table.data_ptr(), width, lens.data_ptr(),
+                                  out.data_ptr(), lp, *_ws(ws), _on(q, stream))
+    if code:
+        _fail(code, "k3attn_decode")
