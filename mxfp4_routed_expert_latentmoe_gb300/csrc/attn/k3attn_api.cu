@@ -213,6 +213,12 @@ static_assert(kRecords % 16 == 0, "the records are written 16 bytes at a time");
 // padded head dim and head group (8 NT query heads of a key head) of the decode instance
 int dec_dp(const k3attn_dims& d) { return (d.head_dim + 63) / 64 * 64; }
 int dec_nt(const k3attn_dims& d) { return d.n_heads / d.n_kv_heads <= 8 ? 1 : 2; }
+// E4M3 heads past 192 dims: 8 query heads at a time, as 16 do not fit the registers (16 x 20000
+// tokens of 2 key heads with 16 queries each, D 256: 68 us, 79 at 16 a time; the second pass
+// over the rows finds most of them in L2.  bf16, which fits but for a few words: 114, 100 us)
+int dec_nt_of(const k3attn_dims& d, int format) {
+  return format == K3ATTN_E4M3 && d.head_dim > 192 ? 1 : dec_nt(d);
+}
 
 template <int FMT, int DP, int NT>
 cudaError_t launch_decode_t(DecodeParams p, int dev, int sms, cudaStream_t s) {
@@ -232,7 +238,8 @@ cudaError_t launch_decode(const DecodeParams& p, int dp, int nt, int dev, int sm
     case 384: return launch_decode_t<FMT, 192, 1>(p, dev, sms, s);
     case 385: return launch_decode_t<FMT, 192, 2>(p, dev, sms, s);
     case 512: return launch_decode_t<FMT, 256, 1>(p, dev, sms, s);
-    case 513: return launch_decode_t<FMT, 256, 2>(p, dev, sms, s);
+    case 513:
+      if constexpr (FMT != CF_E4M3) return launch_decode_t<FMT, 256, 2>(p, dev, sms, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -394,8 +401,9 @@ k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q
   p.arrived = reinterpret_cast<uint32_t*>(w + kCounters);
   p.parts = reinterpret_cast<float*>(w + kRecords);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_decode<CF_E4M3>(p, dec_dp(d), dec_nt(d), dev, sms, s)
-                                        : launch_decode<CF_BF16>(p, dec_dp(d), dec_nt(d), dev, sms, s)));
+  const int dp = dec_dp(d), nt = dec_nt_of(d, cache->format);
+  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_decode<CF_E4M3>(p, dp, nt, dev, sms, s)
+                                        : launch_decode<CF_BF16>(p, dp, nt, dev, sms, s)));
   return K3MOE_OK;
 }
 
