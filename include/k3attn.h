@@ -70,7 +70,8 @@ typedef struct {
  * token_stride D, head_stride page_size * D, page_stride Hkv * page_size * D; any other
  * order of pages, heads and tokens is described by its strides (rows must not overlap).
  * A row must start at a multiple of 16 bytes: strides are multiples of 16 elements
- * (K3ATTN_E4M3) or 8 (K3ATTN_BF16). */
+ * (K3ATTN_E4M3) or 8 (K3ATTN_BF16).  n_pages * page_size is below 2^31 (slots are int32);
+ * offsets in the cache may pass 32 bits. */
 typedef struct {
   void* k;
   void* v;
@@ -136,10 +137,11 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
                             uint16_t* k_out, uint16_t* v_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Attention of one new token for each of B sequences.
- *   q [B] rows of Hq * D bf16, q_stride elements apart
+ *   q [B] rows of Hq * D bf16, q_stride elements apart;  B at most 65535
  *   page_table [B, table_width] int32: the pages of each sequence in order; entries past its
  *     last attended token, and before its first one, are not read
- *   lens [B] int32: cached tokens of each sequence, the new one included
+ *   lens [B] int32: cached tokens of each sequence, the new one included; table_width *
+ *     page_size is below 2^31.  They must not change while the call runs
  *   out [B, Hq, D] bf16;  lse [B, Hq] f32 or NULL
  * The work is split evenly over the SMs whatever the lengths, which are read on the device
  * (a captured call replays with new ones).  The result does not depend on the order in which

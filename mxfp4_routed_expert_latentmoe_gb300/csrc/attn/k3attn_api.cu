@@ -180,9 +180,9 @@ cudaError_t launch_norm_t(QkvParams p, int sms, cudaStream_t s) {
     p.kv_warps = (p.Hkv + kv_warp - 1) / kv_warp;
     if (p.kv_warps > warps) p.kv_warps = warps;
     p.kv_tokens = warps / p.kv_warps < QKV_TOKENS ? warps / p.kv_warps : QKV_TOKENS;
-    p.kv_blocks = (p.T + p.kv_tokens - 1) / p.kv_tokens;
+    p.kv_blocks = (int32_t)(((int64_t)p.T + p.kv_tokens - 1) / p.kv_tokens);
   }
-  const int64_t grid = p.kv_blocks + (int64_t)((p.T + p.tokens - 1) / p.tokens) * p.parts;
+  const int64_t grid = p.kv_blocks + ((int64_t)p.T + p.tokens - 1) / p.tokens * p.parts;
   if constexpr (ROWS > 1)
     if (grid < sms) return launch_norm_t<FMT, 1>(p, sms, s);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
