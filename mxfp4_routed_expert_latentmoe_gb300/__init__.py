@@ -8,6 +8,7 @@ raises.
 """
 from __future__ import annotations
 
+import concurrent.futures as cf
 import ctypes
 import os
 import subprocess
@@ -21,6 +22,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _HEADER = os.path.join(_ROOT, "include", "k3moe.h")
 _ATTN = os.path.join(_CSRC, "attn")  # the attention operators (attn.py)
 _ATTN_HEADER = os.path.join(_ROOT, "include", "k3attn.h")
+_ATTN_BINDING = os.path.join(_BUILD, "k3attn_binding.so")  # attn.py's native side
 _lock = threading.Lock()
 _lib = None
 
@@ -45,22 +47,39 @@ def _sources():
             if f.endswith((".cu", ".cuh"))] + [_HEADER, _ATTN_HEADER]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/ and csrc/attn/ into _build/libk3moe.so for sm_103a (in-tree)."""
-    os.makedirs(_BUILD, exist_ok=True)
-    newest = max(os.path.getmtime(f) for f in _sources())
-    if not force and os.path.exists(_SO) and os.path.getmtime(_SO) >= newest:
-        return _SO
-    nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
-    tmp = _SO + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-t", "2", "-o", tmp, os.path.join(_CSRC, "k3moe_api.cu"),
-           os.path.join(_ATTN, "k3attn_api.cu")]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _compile(cmd, out: str, sources, force: bool, verbose: bool) -> None:
+    """Run cmd (which writes to its last argument) unless `out` is newer than its sources."""
+    newest = max(os.path.getmtime(f) for f in sources)
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + r.stdout + r.stderr)
     if verbose:
         print(r.stdout + r.stderr)
-    os.replace(tmp, _SO)
+    os.replace(tmp, out)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/ and csrc/attn/ into _build/libk3moe.so for sm_103a, and the native side of
+    attn.py (a host extension against torch's headers) into _build/k3attn_binding.so (in-tree)."""
+    import sysconfig
+
+    import torch
+    os.makedirs(_BUILD, exist_ok=True)
+    cuda, tdir = os.environ.get("CUDA_HOME", "/usr/local/cuda"), os.path.dirname(torch.__file__)
+    binding = os.path.join(_ATTN, "k3attn_binding.cpp")
+    jobs = [([os.path.join(cuda, "bin", "nvcc"), *NVCC_FLAGS, "-t", "2", os.path.join(_CSRC, "k3moe_api.cu"),
+              os.path.join(_ATTN, "k3attn_api.cu")], _SO, _sources()),
+            (["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+              "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(tdir, "include"),
+              "-I" + os.path.join(cuda, "include"), binding, "-L" + os.path.join(tdir, "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], _ATTN_BINDING, [binding, _HEADER, _ATTN_HEADER])]
+    with cf.ThreadPoolExecutor(max_workers=2) as ex:
+        for f in [ex.submit(_compile, *job, force, verbose) for job in jobs]:
+            f.result()
     return _SO
 
 

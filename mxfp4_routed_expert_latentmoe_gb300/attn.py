@@ -5,7 +5,8 @@ norms of queries and keys per head with the position rotation, the paged key-val
 Thin binding over the C ABI declared in ``include/k3attn.h``, which has the formulas.  Every
 function checks its tensors (ValueError), passes pointers and strides, and launches on the
 current CUDA stream or on ``stream``; device-detected conditions (DEV_BAD_*) are read with
-``device_status(ws)``.
+``device_status(ws)``.  The operators' checks and calls are native (csrc/attn/k3attn_binding.cpp):
+a decode step's kernels take no longer than they would in Python.
 
     d = attn.dims(n_heads=64, n_kv_heads=8, head_dim=128, rot_dim=128)
     cache = attn.KVCache.empty(d, n_pages=4096, page_size=64, fmt="e4m3")
@@ -19,12 +20,13 @@ import ctypes
 
 import torch
 
-from . import K3MoEError, device_status, lib  # noqa: F401  (device_status: the status word of ws)
+from . import _ATTN_BINDING, _check, _stream, device_status, lib  # noqa: F401  (device_status: the status word of ws)
 
 BF16, E4M3 = 0, 1  # K3ATTN_BF16, K3ATTN_E4M3
 MIN_WORKSPACE = 256  # K3ATTN_MIN_WORKSPACE
 DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_BAD_LENGTH = 0x1, 0x2, 0x4
 _fns = None
+_native = None  # the extension module, loaded by the first operator
 
 
 class Dims(ctypes.Structure):
@@ -34,7 +36,7 @@ class Dims(ctypes.Structure):
 
     def __init__(self, *args):
         super().__init__(*args)
-        self.ref = ctypes.byref(self)
+        self.addr = ctypes.addressof(self)
 
 
 def dims(n_heads, n_kv_heads, head_dim, rot_dim=None, rot_interleaved=False, rms_eps=1e-6, softmax_scale=None,
@@ -77,6 +79,26 @@ def _funcs():
     return _fns
 
 
+def _load():
+    """The native side, bound to the library's operators."""
+    global _native
+    if _native is None:
+        import importlib.util
+        import os
+
+        from . import build
+        L = _funcs()
+        if not os.path.exists(_ATTN_BINDING):
+            build()
+        spec = importlib.util.spec_from_file_location("k3attn_binding", _ATTN_BINDING)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(getattr(L, "k3attn_" + n), ctypes.c_void_p).value
+                   for n in ("qk_norm_rope", "kv_write", "kv_append", "kv_read", "decode")))
+        _native = mod
+    return _native
+
+
 def declared_functions() -> list:
     """Function names declared in include/k3attn.h."""
     import re
@@ -85,45 +107,10 @@ def declared_functions() -> list:
     return sorted(set(re.findall(r"\b(k3attn_[a-z0-9_]+)\s*\(", open(_ATTN_HEADER).read())))
 
 
-# ------------------------------------------------------------------------------ checks
-# (a decode step's call takes a few microseconds on the GPU: the operators below check in line,
-# by comparisons alone, and a message is put together only where one fails)
-_bf16, _f32, _i32, _f64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.float64, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _refuse(t, name, dtype, shape, how=", contiguous"):
-    got = f"{list(t.shape)} (strides {list(t.stride())}) of {t.dtype} on {t.device}" if torch.is_tensor(t) else repr(t)
-    raise ValueError(f"{name}: a CUDA tensor {list(shape)} of {dtype}{how} is needed, got {got}")
-
-
-def _rows(t, name, T, heads, D):
-    """Pointer and token stride of a [T, heads, D] bf16 tensor whose tokens' rows are dense."""
-    sT, sH, sD = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if not (t.dtype is _bf16 and t.shape == (T, heads, D) and t.is_cuda and sD == 1 and (sH == D or heads == 1)):
-        _refuse(t, name, _bf16, (T, heads, D), ", the heads of a token dense,")
-    return t.data_ptr(), sT if T > 1 else heads * D
-
-
-def _ws(ws):
-    if not (ws.dtype is _u8 and ws.is_cuda and ws.is_contiguous()):
-        _refuse(ws, "ws", _u8, ("bytes",))
-    return ws.data_ptr(), ws.numel()
-
-
-def _on(t, stream):
-    """The stream of a call: `stream`, or the current one of t's device."""
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _fail(code, what):
-    raise K3MoEError(code, what)
-
-
 # ------------------------------------------------------------------------------ what a program keeps
 def workspace_bytes(d: Dims) -> int:
+    """Bytes of workspace that decode needs with these dims (0: unsupported); the other operators
+    take any of at least MIN_WORKSPACE."""
     return int(_funcs().k3attn_workspace_bytes(ctypes.byref(d)))
 
 
@@ -139,9 +126,9 @@ def workspace(d: Dims, device="cuda"):
 
 def workspace_init(ws, stream=None):
     """k3attn_workspace_init: readies a workspace (also clears its status word)."""
-    code = _funcs().k3attn_workspace_init(*_ws(ws), _on(ws, stream))
-    if code:
-        _fail(code, "k3attn_workspace_init")
+    if ws.dtype != torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous uint8 CUDA tensor is needed")
+    _check(_funcs().k3attn_workspace_init(ws.data_ptr(), ws.numel(), _stream(stream)), "k3attn_workspace_init")
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
@@ -155,26 +142,31 @@ class KVCache:
     values dense); for E4M3 k_scale, v_scale [n_pages, Hkv, page_size] f32."""
 
     def __init__(self, d: Dims, k, v, k_scale=None, v_scale=None):
-        shape = (k.shape[0], d.n_kv_heads, k.shape[2], d.head_dim) if k.dim() == 4 else ("n_pages", "Hkv", "page", "D")
-        fmt = E4M3 if k.dtype is torch.float8_e4m3fn else BF16
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("k: [n_pages, Hkv, page_size, D] of bfloat16 or float8_e4m3fn is needed")
+        fmt = E4M3 if k.dtype == torch.float8_e4m3fn else BF16
+        shape = (k.shape[0], d.n_kv_heads, k.shape[2], d.head_dim)
         for t, name in ((k, "k"), (v, "v")):
-            if not (t.dtype is (torch.float8_e4m3fn if fmt == E4M3 else _bf16) and t.shape == shape and t.is_cuda
-                    and t.stride(3) == 1 and t.stride() == k.stride()):
-                _refuse(t, name, "bfloat16 or float8_e4m3fn", shape, ", a row's values dense, strides as k's,")
+            if (t.dtype != k.dtype or t.shape != shape or not t.is_cuda or t.stride(3) != 1
+                    or t.stride() != k.stride()):
+                raise ValueError(f"{name}: a CUDA tensor {list(shape)} of {k.dtype}, a row's values dense, with the "
+                                 f"strides of k, is needed, got {list(t.shape)} (strides {list(t.stride())}) of "
+                                 f"{t.dtype} on {t.device}")
         n, page, ss = shape[0], shape[2], (0, 0, 0)
         if fmt == E4M3:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if t is None or not (t.dtype is _f32 and t.shape == shape[:3] and t.is_cuda
-                                     and t.stride() == k_scale.stride()):
-                    _refuse(t, name, _f32, shape[:3], ", strides as k_scale's,")
+                if (t is None or t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_cuda
+                        or t.stride() != k_scale.stride()):
+                    raise ValueError(f"{name}: a CUDA tensor {list(shape[:3])} of float32, with the strides of "
+                                     "k_scale, is needed for an E4M3 cache")
             ss = k_scale.stride()
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.page_size, self.head_shape = n, page, (d.n_kv_heads, d.head_dim)
+        self.n_pages, self.page_size = n, page
         self.c = CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt == E4M3 else None,
                         v_scale.data_ptr() if fmt == E4M3 else None, fmt, n, page, 0, *k.stride()[:3], *ss)
-        self.ref = ctypes.byref(self.c)
+        self.addr, self.rows = ctypes.addressof(self.c), d.n_kv_heads * 65536 + d.head_dim
 
     @classmethod
     def empty(cls, d: Dims, n_pages: int, page_size: int, fmt: str = "bf16", device="cuda"):
@@ -188,118 +180,49 @@ class KVCache:
         return cls(d, *codes, *(torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
 
 
-def _cache(d, cache):
-    if cache.head_shape != (d.n_kv_heads, d.head_dim):
-        raise ValueError(f"the cache's (Hkv, D) are {cache.head_shape}, the dims' {(d.n_kv_heads, d.head_dim)}")
-    return cache.ref
-
-
 # ------------------------------------------------------------------------------ the operators
-def _norm_args(d, T, D, positions, inv_freq, q_w, k_w):
-    """Pointers of what the norms and the rotation read beside the rows."""
-    if not (positions.dtype is _i32 and positions.shape == (T,) and positions.is_cuda and positions.is_contiguous()):
-        _refuse(positions, "positions", _i32, (T,))
-    if not (q_w.dtype is _f32 and q_w.shape == (D,) and q_w.is_cuda and q_w.is_contiguous()):
-        _refuse(q_w, "q_w", _f32, (D,))
-    if not (k_w.dtype is _f32 and k_w.shape == (D,) and k_w.is_cuda and k_w.is_contiguous()):
-        _refuse(k_w, "k_w", _f32, (D,))
-    R = d.rot_dim
-    if R == 0:
-        return positions.data_ptr(), None, q_w.data_ptr(), k_w.data_ptr()
-    if not (inv_freq.dtype is _f64 and inv_freq.shape == (R // 2,) and inv_freq.is_cuda and inv_freq.is_contiguous()):
-        _refuse(inv_freq, "inv_freq", _f64, (R // 2,))
-    return positions.data_ptr(), inv_freq.data_ptr(), q_w.data_ptr(), k_w.data_ptr()
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def qk_norm_rope(d: Dims, q, k, positions, inv_freq, q_w, k_w, q_out, k_out, stream=None):
     """k3attn_qk_norm_rope: q [T, Hq, D], k [T, Hkv, D] bf16 (slices of one projection's output
     will do) -> q_out, k_out, dense, normed per head and rotated.  inv_freq may be None when
     d.rot_dim is 0."""
-    T, Hq, Hkv, D = q.shape[0], d.n_heads, d.n_kv_heads, d.head_dim
-    qp, qs = _rows(q, "q", T, Hq, D)
-    kp, ks = _rows(k, "k", T, Hkv, D)
-    pos, freq, qw, kw = _norm_args(d, T, D, positions, inv_freq, q_w, k_w)
-    if not (q_out.dtype is _bf16 and q_out.shape == (T, Hq, D) and q_out.is_cuda and q_out.is_contiguous()):
-        _refuse(q_out, "q_out", _bf16, (T, Hq, D))
-    if not (k_out.dtype is _bf16 and k_out.shape == (T, Hkv, D) and k_out.is_cuda and k_out.is_contiguous()):
-        _refuse(k_out, "k_out", _bf16, (T, Hkv, D))
-    code = _funcs().k3attn_qk_norm_rope(d.ref, T, qp, qs, kp, ks, pos, freq, qw, kw, q_out.data_ptr(),
-                                        k_out.data_ptr(), _on(q, stream))
+    code = (_native or _load()).qk_norm_rope(d.addr, q, k, positions, inv_freq, q_w, k_w, q_out, k_out,
+                                             _handle(stream))
     if code:
-        _fail(code, "k3attn_qk_norm_rope")
+        _check(code, "k3attn_qk_norm_rope")
 
 
 def kv_write(d: Dims, k, v, slots, cache: KVCache, ws, stream=None):
     """k3attn_kv_write: k, v [T, Hkv, D] bf16 into the cache at slots [T] int32 (-1: not written)."""
-    T, Hkv, D = k.shape[0], d.n_kv_heads, d.head_dim
-    kp, ks = _rows(k, "k", T, Hkv, D)
-    vp, vs = _rows(v, "v", T, Hkv, D)
-    if not (slots.dtype is _i32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()):
-        _refuse(slots, "slots", _i32, (T,))
-    code = _funcs().k3attn_kv_write(d.ref, T, kp, ks, vp, vs, slots.data_ptr(), _cache(d, cache), *_ws(ws),
-                                    _on(k, stream))
+    code = (_native or _load()).kv_write(d.addr, k, v, slots, cache.addr, cache.rows, ws, _handle(stream))
     if code:
-        _fail(code, "k3attn_kv_write")
+        _check(code, "k3attn_kv_write")
 
 
 def kv_append(d: Dims, q, k, v, positions, slots, inv_freq, q_w, k_w, cache: KVCache, q_out, ws, k_out=None,
               stream=None):
     """k3attn_kv_append: qk_norm_rope of q into q_out and of k, and the write of k and v into the
     cache, in one pass; k_out (optional) also receives the keys."""
-    T, Hq, Hkv, D = q.shape[0], d.n_heads, d.n_kv_heads, d.head_dim
-    qp, qs = _rows(q, "q", T, Hq, D)
-    kp, ks = _rows(k, "k", T, Hkv, D)
-    vp, vs = _rows(v, "v", T, Hkv, D)
-    pos, freq, qw, kw = _norm_args(d, T, D, positions, inv_freq, q_w, k_w)
-    if not (slots.dtype is _i32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()):
-        _refuse(slots, "slots", _i32, (T,))
-    if not (q_out.dtype is _bf16 and q_out.shape == (T, Hq, D) and q_out.is_cuda and q_out.is_contiguous()):
-        _refuse(q_out, "q_out", _bf16, (T, Hq, D))
-    ko = None
-    if k_out is not None:
-        if not (k_out.dtype is _bf16 and k_out.shape == (T, Hkv, D) and k_out.is_cuda and k_out.is_contiguous()):
-            _refuse(k_out, "k_out", _bf16, (T, Hkv, D))
-        ko = k_out.data_ptr()
-    code = _funcs().k3attn_kv_append(d.ref, T, qp, qs, kp, ks, vp, vs, pos, slots.data_ptr(), freq, qw, kw,
-                                     _cache(d, cache), q_out.data_ptr(), ko, *_ws(ws), _on(q, stream))
+    code = (_native or _load()).kv_append(d.addr, q, k, v, positions, slots, inv_freq, q_w, k_w, cache.addr,
+                                          cache.rows, q_out, k_out, ws, _handle(stream))
     if code:
-        _fail(code, "k3attn_kv_append")
+        _check(code, "k3attn_kv_append")
 
 
 def kv_read(d: Dims, slots, cache: KVCache, k_out, v_out, ws, stream=None):
     """k3attn_kv_read: the rows at slots [T] int32 as bf16, k_out and v_out [T, Hkv, D]."""
-    T, Hkv, D = slots.shape[0], d.n_kv_heads, d.head_dim
-    if not (slots.dtype is _i32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()):
-        _refuse(slots, "slots", _i32, (T,))
-    if not (k_out.dtype is _bf16 and k_out.shape == (T, Hkv, D) and k_out.is_cuda and k_out.is_contiguous()):
-        _refuse(k_out, "k_out", _bf16, (T, Hkv, D))
-    if not (v_out.dtype is _bf16 and v_out.shape == (T, Hkv, D) and v_out.is_cuda and v_out.is_contiguous()):
-        _refuse(v_out, "v_out", _bf16, (T, Hkv, D))
-    code = _funcs().k3attn_kv_read(d.ref, T, slots.data_ptr(), _cache(d, cache), k_out.data_ptr(), v_out.data_ptr(),
-                                   *_ws(ws), _on(slots, stream))
+    code = (_native or _load()).kv_read(d.addr, slots, cache.addr, cache.rows, k_out, v_out, ws, _handle(stream))
     if code:
-        _fail(code, "k3attn_kv_read")
+        _check(code, "k3attn_kv_read")
 
 
 def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None):
     """k3attn_decode: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
     of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32."""
-    B, Hq, D = q.shape[0], d.n_heads, d.head_dim
-    qp, qs = _rows(q, "q", B, Hq, D)
-    width = page_table.shape[-1]
-    if not (page_table.dtype is _i32 and page_table.shape == (B, width) and page_table.is_cuda
-            and page_table.is_contiguous()):
-        _refuse(page_table, "page_table", _i32, (B, "width"))
-    if not (lens.dtype is _i32 and lens.shape == (B,) and lens.is_cuda and lens.is_contiguous()):
-        _refuse(lens, "lens", _i32, (B,))
-    if not (out.dtype is _bf16 and out.shape == (B, Hq, D) and out.is_cuda and out.is_contiguous()):
-        _refuse(out, "out", _bf16, (B, Hq, D))
-    lp = None
-    if lse is not None:
-        if not (lse.dtype is _f32 and lse.shape == (B, Hq) and lse.is_cuda and lse.is_contiguous()):
-            _refuse(lse, "lse", _f32, (B, Hq))
-        lp = lse.data_ptr()
-    code = _funcs().k3attn_decode(d.ref, B, qp, qs, _cache(d, cache), page_table.data_ptr(), width, lens.data_ptr(),
-                                  out.data_ptr(), lp, *_ws(ws), _on(q, stream))
+    code = (_native or _load()).decode(d.addr, q, cache.addr, cache.rows, page_table, lens, out, lse, ws,
+                                       _handle(stream))
     if code:
-        _fail(code, "k3attn_decode")
+        _check(code, "k3attn_decode")

@@ -190,8 +190,11 @@ def test_workspace_init_validates_on_the_host():
 def test_the_binding_refuses_tensors_that_do_not_fit():
     d = _dims()
     cpu = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError):  # not on the GPU
+    with pytest.raises(ValueError, match="q: a CUDA tensor .1, 8, 128. of BFloat16"):  # not on the GPU
         attn.qk_norm_rope(d, cpu, cpu[:, :2], None, None, None, None, None, None)
+    for not_a_tensor in (None, 3, [1.0]):
+        with pytest.raises(ValueError):
+            attn.qk_norm_rope(d, not_a_tensor, cpu[:, :2], None, None, None, None, None, None)
     pool = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         attn.KVCache(d, pool, pool)
@@ -201,6 +204,18 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
         attn.KVCache.empty(d, 4, 16, fmt="int3")
     with pytest.raises(ValueError):
         attn.workspace(_dims(head_dim=100, rot_dim=0))
+
+
+def test_the_native_side_checks_its_arguments_count_and_structs():
+    native = attn._load()
+    for f, n in ((native.qk_norm_rope, 10), (native.kv_write, 8), (native.kv_append, 15), (native.kv_read, 8),
+                 (native.decode, 10), (native.bind, 5)):
+        with pytest.raises(TypeError):
+            f(*[None] * (n - 1))
+    with pytest.raises(ValueError):  # no dims at address 0
+        native.decode(0, *[None] * 9)
+    with pytest.raises(TypeError):  # not an address
+        native.decode("x", *[None] * 9)
 
 
 def test_rope_frequencies():

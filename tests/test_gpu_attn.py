@@ -475,3 +475,50 @@ def test_one_workspace_serves_other_shapes(attn):
         for _ in range(2):
             out, lse = _run_decode(attn, d, q, cache, table, lens_t, ws)
             _check_decode(attn, d, q, cache, slots, lens, out, lse, 16)
+
+
+def test_tensors_that_do_not_fit_are_refused_before_a_launch(attn):
+    from mxfp4_routed_expert_latentmoe_gb300 import K3MoEError
+    d, other = attn.dims(4, 2, 64), attn.dims(4, 2, 128)
+    q, cache, table, lens_t, slots, ws = _sequences(attn, d, [20, 5], 16, "e4m3", 30)
+    _, k, v = _qkv(2, 4, 2, 64, 31)
+    out, lse = torch.full((2, 4, 64), 7.0, device="cuda", dtype=torch.bfloat16), torch.empty(2, 4, device="cuda")
+    good = dict(q=q, cache=cache, page_table=table, lens=lens_t, out=out, ws=ws)
+    for bad in (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:1]), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)),
+                dict(page_table=table.long()), dict(page_table=table[:1]), dict(page_table=table[0]),
+                dict(page_table=table[:, ::2]), dict(lens=lens_t.cpu()), dict(lens=lens_t[:1]), dict(lens=None),
+                dict(out=out.half()), dict(out=out[:, :, :32]), dict(ws=ws.float()), dict(lse=lse.half()),
+                dict(lse=lse[:1]), dict(cache=attn.KVCache.empty(other, 2, 16))):
+        with pytest.raises(ValueError):
+            attn.decode(d, **{**good, **bad})
+    with pytest.raises(K3MoEError) as e:
+        attn.decode(d, **{**good, "ws": ws[:256]})
+    assert e.value.code == 4
+    two = torch.tensor([3, 4], device="cuda", dtype=torch.int32)
+    with pytest.raises(ValueError):
+        attn.kv_write(d, k, v, two.long(), cache, ws)
+    with pytest.raises(ValueError):
+        attn.kv_write(d, k, v[:1], two, cache, ws)
+    with pytest.raises(ValueError):
+        attn.kv_read(d, two, cache, out[:, :2], out[:, 2:], ws)  # not dense
+    with pytest.raises(K3MoEError) as e:
+        attn.kv_write(d, k, v, two, cache, ws[:255])
+    assert e.value.code == 4
+    w = torch.ones(64, device="cuda")
+    freq = attn.rope_frequencies(64)
+    args = dict(q=q, k=k, positions=two, inv_freq=freq, q_w=w, k_w=w, q_out=torch.empty_like(out),
+                k_out=torch.empty(2, 2, 64, device="cuda", dtype=torch.bfloat16))
+    for bad in (dict(positions=two[:1]), dict(inv_freq=freq.float()), dict(inv_freq=None), dict(q_w=w[:32]),
+                dict(k_w=w.half()), dict(q_out=out[:1]), dict(k_out=out), dict(k=k[:1])):
+        with pytest.raises(ValueError):
+            attn.qk_norm_rope(d, **{**args, **bad})
+    for wrong in (cache.k[:, :1], cache.k[..., :32], cache.k.to(torch.bfloat16)):
+        with pytest.raises(ValueError):
+            attn.KVCache(d, wrong, cache.v, cache.k_scale, cache.v_scale)
+    with pytest.raises(ValueError):
+        attn.KVCache(d, cache.k, cache.v)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and attn.device_status(ws) == 0
+    # no tokens, no sequences
+    attn.kv_write(d, k[:0], v[:0], two[:0], cache, ws)
+    attn.decode(d, q[:0], cache, table[:0], lens_t[:0], out[:0], ws)
