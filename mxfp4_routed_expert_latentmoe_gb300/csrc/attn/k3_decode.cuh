@@ -208,11 +208,12 @@ struct DecAt {
   }
   // whether the unit is the team's whose range ends in front of `end`
   K3_DEVI bool in(int32_t end, int32_t whole) const { return (nu <= whole ? x - u - 1 : x) < end; }
-  K3_DEVI void next(const DecodeParams& p, int ulog) {
+  K3_DEVI void next(const DecodeParams& p, int ulog, int32_t end) {
     ++x;
     if (++u < nu) return;
     ++x;
     u = 0;
+    if (x > end) return;  // (its start is past the range already, whatever it is)
     if (++grp < p.groups) return;
     grp = 0;
     if (++kvh < p.Hkv) return;
@@ -376,11 +377,12 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     } else if (at.nu <= whole_units) {  // another team's
       at.x = at.nu - 1 - at.u;
       at.u = at.nu - 1;
-      at.next(p, ulog);
+      at.next(p, ulog, end);
     }
     DecAt ahead = at;  // the tile whose page entries are in `entry`, with the rows' places in them
     int32_t entry = 0, in_page = 0;
     uint32_t got[2] = {0, 0};  // arrivals before this team's (of its first thread)
+    bool cut = false;          // there is a part that is not a whole sequence
 
     // a copy takes LR 16-byte chunks (128 or 64 bytes) of each of 32 / LR rows
     constexpr int CPR = ROW / 16, LR = CPR % 8 == 0 ? 8 : 4, RPI = 32 / LR;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     auto advance = [&](int stage) {
       if (ahead.in(end, whole_units)) {
         issue(stage);
-        ahead.next(p, ulog);
+        ahead.next(p, ulog, end);
         if (ahead.in(end, whole_units)) fetch();
       }
       cp_async_commit();
@@ -694,9 +696,10 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 
       // ---- the end of a part: join the warps, then write the result or leave a record
       const DecAt now = at;
-      at.next(p, ulog);
+      at.next(p, ulog, end);
       if (!at.in(end, whole_units) || now.u == now.nu - 1) {
         const bool whole = part_u0 == 0 && now.u == now.nu - 1;
+        cut |= !whole;
         const int64_t row0 = (int64_t)now.b * p.Hq + head0;
         float* const rec = p.parts + (2 * worker + part_slot) * C::REC;
         // the warps trade maxima and sums of weights, bring their sums to the team's maximum and
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 
     // ---- parts: the team that arrived last joins a sequence's records
 #pragma unroll
-    for (int slot = 0; slot < 2; ++slot) {
+    for (int slot = 0; slot < 2 && cut; ++slot) {
       __syncwarp();
       if (tthread == 0)
         s_last[team] = s_part[2 * team + slot].there && got[slot] == (uint32_t)(s_part[2 * team + slot].parts - 1);
