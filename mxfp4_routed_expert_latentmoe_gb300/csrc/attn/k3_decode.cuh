@@ -5,10 +5,21 @@
 // the M side, so that a key head with few query heads wastes no rows:
 //   S^T [16 tokens x 8 heads]  = K  [16 tokens x D]  Q^T
 //   O^T [16 dims x 8 heads]   += V^T [16 dims x 16 tokens]  P^T
-// (mma.sync: the products are 2 G flops a cached byte, far below what they reach; the cache's
-// bytes bound the kernel.)  Each warp streams its own tiles of 16 or 32 tokens through a ring
-// in shared memory with cp.async, row by row through the page table (any page size, any
-// strides), and joins its block's other warps only at the end of a sequence's part.
+// Each warp streams its own tiles of 16 or 32 tokens through a ring in shared memory with
+// cp.async, row by row through the page table (any page size, any strides), and joins its
+// team's other warps only at the end of a sequence's part.
+//
+// What bounds it (GB300, copy rate 6789 GB/s).  Up to 8 query heads a key head, HBM: 2 x 262143
+// tokens, 8 E4M3 key heads of 128: 123 us, 92% of the copy rate; 64 sequences of up to 8192
+// tokens, bf16: 169 us, 87% (the copies alone reach 95%; the rest is the join at the 3 or 4
+// sequence ends of a block).  Up to 16 query heads: twice the matrix instructions and weights a
+// tile with the registers of 8 warps an SM used up, so that a warp's own instruction latency
+// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 75 us, 37%.  Few
+// short sequences: the chain of dependent reads (lengths, page table, rows, joined records),
+// 4.5 us for one token, 7.8 us for one sequence of 347.
+// mma.sync rather than tcgen05: the products are 2 G flops a cached byte (under 100 TFLOP/s at
+// the copy rate with 8 heads), E4M3 rows have to pass through registers on their way to fp16
+// anyway, and the softmax stays in the registers that the products leave it in.
 //
 // E4M3 rows become fp16 operands exactly; a key's scale multiplies its logit, a value's scale
 // goes into its weight's exponent, with a maximum of its own, so that weights of values of any
@@ -49,13 +60,13 @@ constexpr int DEC_MAX_WARPS = 8;
 constexpr int DEC_MAX_BLOCKS = 192;
 constexpr int DEC_MAX_TEAMS = DEC_MAX_BLOCKS * DEC_MAX_WARPS;
 
-// Shapes of one instance: the warps of a block, the tokens of a warp's tile, the ring's depth,
-// and the dims that one pass of the block's join takes (its buffer gets what the ring leaves).
+// Shapes of one instance: the warps of a block, the tokens of a warp's tile, the ring's depth
+// (192 KB of rows in all: two or more tiles a warp in flight, 128 KB an SM).
 template <int FMT, int DP, int NT>
 struct DecCfg {
   static constexpr int ES = FMT == CF_E4M3 ? 1 : 2;
   static constexpr int ROW = DP * ES;  // bytes of a row in shared memory
-    // 32 tokens a tile where eight warps' rings hold two of them, else 16: a tile's fixed work
+  // 32 tokens a tile where eight warps' rings hold two of them, else 16: a tile's fixed work
   // counts for more than the ring's depth (D 192, 12 KB a tile: 201 windowed sequences E4M3 80
   // -> 74 us, 16 x 10000 tokens bf16 55 -> 49 us)
   static constexpr int MT = 2 * ROW * 32 <= 12288 ? 2 : 1;

@@ -1,9 +1,13 @@
 // k3_qkv.cuh -- norms of queries and keys per head with the position rotation, and the rows of
 // the paged cache: written (bf16, or E4M3 codes with a row scale) and read back.
 //
-// All of it is bound by HBM: a row (a head of a token) is taken by 8, 16 or 32 lanes, eight
-// elements a lane (16-byte accesses), and a thread has the loads of up to QKV_ROWS rows in
-// flight before it waits for any.
+// All of it moves each byte once; HBM is the floor (GB300, copy rate 6789 GB/s).  Measured: read
+// of 100003 tokens of 8 E4M3 heads of 128 at 98% of the copy rate, import of 65536 at 84%
+// (issue slots: the quantisation), norms of 16381 tokens of 72 heads at 79% and the append of
+// 8192 tokens at 68% (issue slots, and warps waiting for their token's angles).
+//
+// A row (a head of a token) is taken by 8, 16 or 32 lanes, eight elements a lane, and a thread
+// has the loads of up to QKV_ROWS rows in flight before it waits for any.
 #pragma once
 
 #include <cuda_fp8.h>
