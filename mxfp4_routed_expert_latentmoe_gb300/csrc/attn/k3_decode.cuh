@@ -27,7 +27,7 @@
 //
 // The work is cut into units (W tiles of one (sequence, key head, head group), one for each of
 // the W warps of a team), and the units, in a line, are dealt out evenly to all teams, whatever
-// the lengths; a sequence's start counts as one more, and a sequence of at most DEC_WHOLE tiles
+// the lengths; a sequence's start counts as one or two more, and a sequence of at most DEC_WHOLE tiles
 // stays with the team that its start falls to.  A team joins its warps' sums at the end
 // of a sequence's part; a part that is not a whole sequence leaves an unnormalised record in the
 // workspace, and the team that arrives last joins a sequence's records, in order.  Long
@@ -200,6 +200,11 @@ K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
   return n < 0 ? 0 : (n > most ? (int32_t)most : n);
 }
 
+// Units that a sequence's start counts as (its queries, its join): for teams of 4 and 8 warps two
+// (64 sequences up to 4000 tokens, 12 query heads a key head, E4M3: 44.0 us, 46.2 at one), for
+// smaller ones one (200 sequences up to 100 tokens: 14.9 us, 17.9 at two)
+K3_DEVI int dec_start(int wlog) { return wlog >= 2 ? 2 : 1; }
+
 // Tiles of a sequence that is never cut: joining its records would take longer than they do (200
 // sequences up to 100 tokens, D 128, E4M3: 16.5 us, 18.3 if they are cut; with teams of a block,
 // where these are less than a unit, cutting stays right: 8 x 1000 tokens 11.3 us, 13.2 whole)
@@ -218,13 +223,13 @@ struct DecAt {
     return !bad;
   }
   // whether the unit is the team's whose range ends in front of `end`
-  K3_DEVI bool in(int32_t end, int32_t whole) const { return (nu <= whole ? x - u - 1 : x) < end; }
-  K3_DEVI void next(const DecodeParams& p, int ulog, int32_t end) {
+  K3_DEVI bool in(int32_t end, int32_t whole, int start) const { return (nu <= whole ? x - u - start : x) < end; }
+  K3_DEVI void next(const DecodeParams& p, int ulog, int32_t end, int start) {
     ++x;
     if (++u < nu) return;
-    ++x;
+    x += start;
     u = 0;
-    if (x > end) return;  // (its start is past the range already, whatever it is)
+    if (x - start >= end) return;  // (its start is past the range already, whatever it is)
     if (++grp < p.groups) return;
     grp = 0;
     if (++kvh < p.Hkv) return;
@@ -316,10 +321,10 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     if (wlog < 0 && (1 << i) <= WARPS && (4 * sums[i] <= 5 * sums[0] || sums[i] * HR <= (int64_t)gridDim.x * WARPS))
       wlog = i;
   const int W = 1 << wlog, ulog = C::TLOG + wlog, teams = WARPS >> wlog, team = warp >> wlog, tw = warp & (W - 1);
-  const int whole_units = DEC_WHOLE >> wlog;
+  const int whole_units = DEC_WHOLE >> wlog, start = dec_start(wlog);
   const int tthreads = 32 << wlog, tthread = threadIdx.x & (tthreads - 1);
 
-  const int64_t mine = ((wlog == 0 ? count[0] : wlog == 1 ? count[1] : wlog == 2 ? count[2] : count[3]) >> wlog) + some;
+  const int64_t mine = ((wlog == 0 ? count[0] : wlog == 1 ? count[1] : wlog == 2 ? count[2] : count[3]) >> wlog) + start * some;
   int64_t upto = mine, total;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
         int64_t before = lo;
         for (at.b = b_lo;; ++at.b) {
           at.open(p, ulog);
-          const int64_t here = at.nu > 0 ? (int64_t)(at.nu + 1) * HR : 0;
+          const int64_t here = at.nu > 0 ? (int64_t)(at.nu + start) * HR : 0;
           if (x < before + here) break;
           before += here;
         }
@@ -377,18 +382,18 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   const int32_t end = (int32_t)max((int64_t)0, min(min(total - unit0, chunk), (int64_t)INT32_MAX));
   if (tthread < 2) s_part[2 * team + tthread].there = 0;
   if (end > 0) {
-    const int32_t hr = (int32_t)div64(off, at.nu + 1);
+    const int32_t hr = (int32_t)div64(off, at.nu + start);
     at.kvh = hr / p.groups;
     at.grp = hr - at.kvh * p.groups;
-    at.u = (int32_t)(off - (int64_t)hr * (at.nu + 1)) - 1;
+    at.u = (int32_t)(off - (int64_t)hr * (at.nu + start)) - start;
     at.x = 0;
     if (at.u < 0) {  // a sequence's start
+      at.x = -at.u;
       at.u = 0;
-      at.x = 1;
     } else if (at.nu <= whole_units) {  // another team's
       at.x = at.nu - 1 - at.u;
       at.u = at.nu - 1;
-      at.next(p, ulog, end);
+      at.next(p, ulog, end, start);
     }
     DecAt ahead = at;  // the tile whose page entries are in `entry`, with the rows' places in them
     int32_t entry = 0, in_page = 0;
@@ -459,14 +464,14 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     };
     // copies the tile at `ahead` (if it is the team's) and fetches the entries of the next
     auto advance = [&](int stage) {
-      if (ahead.in(end, whole_units)) {
+      if (ahead.in(end, whole_units, start)) {
         issue(stage);
-        ahead.next(p, ulog, end);
-        if (ahead.in(end, whole_units)) fetch();
+        ahead.next(p, ulog, end, start);
+        if (ahead.in(end, whole_units, start)) fetch();
       }
       cp_async_commit();
     };
-    if (ahead.in(end, whole_units)) fetch();
+    if (ahead.in(end, whole_units, start)) fetch();
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) advance(s);
 
@@ -503,7 +508,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     if (EARLY) load_queries(at);
     int32_t part_u0 = 0, part_slot = 0;
     int stage = 0;
-    for (bool begun = false; at.in(end, whole_units); begun = true) {
+    for (bool begun = false; at.in(end, whole_units, start); begun = true) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
       advance(stage == 0 ? STAGES - 1 : stage - 1);
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       if (!begun || at.u == 0) {  // a new part: its queries, empty sums
         if (!EARLY) load_queries(at);
         part_u0 = at.u;
-        part_slot = at.u == 0 && at.x > 1;  // not the team's first place of all
+        part_slot = at.u == 0 && at.x > start;  // not the team's first place of all
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           qs[nt] = make_float2(p.scale, p.scale);
@@ -707,8 +712,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 
       // ---- the end of a part: join the warps, then write the result or leave a record
       const DecAt now = at;
-      at.next(p, ulog, end);
-      if (!at.in(end, whole_units) || now.u == now.nu - 1) {
+      at.next(p, ulog, end, start);
+      if (!at.in(end, whole_units, start) || now.u == now.nu - 1) {
         const bool whole = part_u0 == 0 && now.u == now.nu - 1;
         cut |= !whole;
         const int64_t row0 = (int64_t)now.b * p.Hq + head0;
@@ -786,7 +791,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
                 *reinterpret_cast<float2*>(x + DP + d0) = make_float2(a.y, b.y);
               }
             }
-          if (EARLY && n0 + C::PN >= NT && at.in(end, whole_units)) load_queries(at);
+          if (EARLY && n0 + C::PN >= NT && at.in(end, whole_units, start)) load_queries(at);
           team_sync(team, tthreads);
           const int hs = min(heads - 8 * n0, 8 * C::PN);
 #pragma unroll 2
@@ -858,7 +863,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
               // team c0's part is in its slot 0 where it begins at the team's first place
-              const int at_second = j0 + j == 0 && x.i0 - x.c0 * chunk > 1;
+              const int at_second = j0 + j == 0 && x.i0 - x.c0 * chunk > start;
               const float* y = p.parts + (2 * (int64_t)(x.c0 + j0 + j) + at_second) * C::REC;
 #pragma unroll
               for (int s = 0; s < SIDE; ++s) {
