@@ -320,6 +320,14 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   for (int i = 3; i >= 0; --i)  // the largest that wastes at most a quarter, or leaves warps idle anyway
     if (wlog < 0 && (1 << i) <= WARPS && (4 * sums[i] <= 5 * sums[0] || sums[i] * HR <= (int64_t)gridDim.x * WARPS))
       wlog = i;
+  // teams of half a block, where there are sequences enough for all (HR a sequence) with work for
+  // more than a moment, and their ends are frequent (at most 24 units of a block each): while one
+  // team joins, the other streams.  201 windowed sequences, D 192: 66 us, 78 with whole blocks;
+  // 128 up to 2000, D 64: 53, 57; but 64 up to 8192 (64 units each): 172, 168.
+  const int64_t parts_all = (int64_t)p.B * HR, warps_all = (int64_t)gridDim.x * WARPS;
+  if (wlog == 3 && 10 * parts_all >= 8 * (int64_t)gridDim.x && sums[0] * HR >= 4 * warps_all &&
+      sums[3] * HR <= 24 * 8 * parts_all)
+    wlog = 2;
   const int W = 1 << wlog, ulog = C::TLOG + wlog, teams = WARPS >> wlog, team = warp >> wlog, tw = warp & (W - 1);
   const int whole_units = DEC_WHOLE >> wlog, start = dec_start(wlog);
   const int tthreads = 32 << wlog, tthread = threadIdx.x & (tthreads - 1);
