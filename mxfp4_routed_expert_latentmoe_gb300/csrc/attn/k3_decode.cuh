@@ -240,6 +240,12 @@ struct DecAt {
     } while (nu == 0);
   }
 };
+// A lane's row of a tile, on its way to be copied: its page (an entry of the page table, still
+// being read), its place there, its key head; whether the tile and the row are there at all.
+struct DecRow {
+  int32_t entry, in_page, kvh;
+  bool tile, in;
+};
 // A part that is not a whole sequence, until its team asks who arrived last.
 struct DecPart {
   int64_t i0;           // the sequence's first unit of all
@@ -403,41 +409,43 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       at.u = at.nu - 1;
       at.next(p, ulog, end, start);
     }
-    DecAt ahead = at;  // the tile whose page entries are in `entry`, with the rows' places in them
-    int32_t entry = 0, in_page = 0;
+    DecAt ahead = at;  // the next tile whose page entries are to be read
     uint32_t got[2] = {0, 0};  // arrivals before this team's (of its first thread)
     bool cut = false;          // there is a part that is not a whole sequence
 
     // a copy takes LR 16-byte chunks (128 or 64 bytes) of each of 32 / LR rows
     constexpr int CPR = ROW / 16, LR = CPR % 8 == 0 ? 8 : 4, RPI = 32 / LR;
     const int cpr = p.D * C::ES / 16;
-    // row `lane` (of TW) of the tile at `ahead`
-    auto row_token = [&]() { return ahead.first + (ahead.u * W + tw) * TW + (lane & (TW - 1)); };
-    auto fetch = [&]() {  // the tile's page entries
-      const int32_t t = row_token();
-      entry = 0;
-      if (t < ahead.n) {
-        const uint32_t pg = p.c.by_page(t);
-        entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
-        in_page = t - (int32_t)(pg * (uint32_t)p.c.page_size);
+    // reads the page entries of the tile at `ahead` (if it is the team's) and moves on
+    auto fetch = [&]() {
+      DecRow r{0, 0, ahead.kvh, ahead.in(end, whole_units, start), false};
+      if (r.tile) {
+        const int32_t t = ahead.first + (ahead.u * W + tw) * TW + (lane & (TW - 1));
+        r.in = t < ahead.n;
+        if (r.in) {
+          const uint32_t pg = p.c.by_page(t);
+          r.entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
+          r.in_page = t - (int32_t)(pg * (uint32_t)p.c.page_size);
+        }
+        ahead.next(p, ulog, end, start);
       }
+      return r;
     };
-    auto issue = [&](int stage) {  // the copies of the tile at `ahead`
+    auto issue = [&](int stage, const DecRow& x) {  // the copies of a tile
       const uint32_t st = ring + stage * C::STAGE;
-      const bool in = row_token() < ahead.n;
-      const bool ok = in && entry >= 0 && entry < p.c.n_pages;
-      if (in && !ok) flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
+      const bool ok = x.in && x.entry >= 0 && x.entry < p.c.n_pages;
+      if (x.in && !ok) flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
       if (lane == 0) *reinterpret_cast<uint32_t*>(__cvta_shared_to_generic(st + C::STAGE - 16)) = mask;
       if (mask == 0) return;
-      const int64_t off = ok ? entry * p.c.page + ahead.kvh * p.c.head + in_page * p.c.tok : 0;
+      const int64_t off = ok ? x.entry * p.c.page + x.kvh * p.c.head + x.in_page * p.c.tok : 0;
       if constexpr (FMT == CF_E4M3) {
-        const int64_t so = ok ? entry * p.c.spage + ahead.kvh * p.c.shead + in_page * p.c.stok : 0;
+        const int64_t so = ok ? x.entry * p.c.spage + x.kvh * p.c.shead + x.in_page * p.c.stok : 0;
         const uint32_t dst = st + C::KV + 4 * (lane & (TW - 1));
         if (TW == 32 || lane < 16) cp_async4_or_zero(dst, p.c.ks + so, ok ? 4 : 0);
         if (TW == 32 || lane >= 16) cp_async4_or_zero(dst + 4 * TW, p.c.vs + so, ok ? 4 : 0);
       }
-      if (mask == 0xFFFFFFFFu && p.D == DP && __shfl_sync(0xFFFFFFFFu, in_page, 0) + TW <= p.c.page_size) {
+      if (mask == 0xFFFFFFFFu && p.D == DP && __shfl_sync(0xFFFFFFFFu, x.in_page, 0) + TW <= p.c.page_size) {
         // all rows there, on one page: they lie a token's stride apart
         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + (lane / LR) * p.c.tok + 16 * (lane % LR);
         const int64_t step = RPI * p.c.tok;
@@ -470,18 +478,17 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
           }
       }
     };
-    // copies the tile at `ahead` (if it is the team's) and fetches the entries of the next
-    auto advance = [&](int stage) {
-      if (ahead.in(end, whole_units, start)) {
-        issue(stage);
-        ahead.next(p, ulog, end, start);
-        if (ahead.in(end, whole_units, start)) fetch();
-      }
-      cp_async_commit();
-    };
-    if (ahead.in(end, whole_units, start)) fetch();
+    // the ring's first tiles: the page entries of all are read before the first copy waits for its
+    // own (one read's latency in front of the copies, not one a tile)
+    DecRow first[STAGES - 1];
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) advance(s);
+    for (int i = 0; i < STAGES - 1; ++i) first[i] = fetch();
+    DecRow ready = fetch();  // the tile to be copied next
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) {
+      if (first[i].tile) issue(i, first[i]);
+      cp_async_commit();
+    }
 
     float2 acc[KSTEPS][NT][2], m[NT], l[NT], vm[NT], qs[NT];  // pairs: of two heads
     uint32_t qf[KSTEPS][NT][2];
@@ -519,7 +526,11 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     for (bool begun = false; at.in(end, whole_units, start); begun = true) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
-      advance(stage == 0 ? STAGES - 1 : stage - 1);
+      if (ready.tile) {
+        issue(stage == 0 ? STAGES - 1 : stage - 1, ready);
+        ready = fetch();
+      }
+      cp_async_commit();
       const int32_t heads = min(HEADS, p.G - at.grp * HEADS);  // of this group
       const int64_t head0 = (int64_t)at.kvh * p.G + at.grp * HEADS;
 
