@@ -11,12 +11,12 @@
 //
 // What bounds it (GB300, copy rate 6789 GB/s).  Up to 8 query heads a key head, HBM: 2 x 262143
 // tokens, 8 E4M3 key heads of 128: 123 us, 92% of the copy rate; 64 sequences of up to 8192
-// tokens, bf16: 169 us, 87% (the copies alone reach 95%; the rest is the join at the 3 or 4
+// tokens, bf16: 166 us, 88% (the copies alone reach 95%; the rest is the join at the 3 or 4
 // sequence ends of a block).  Up to 16 query heads: twice the matrix instructions and weights a
 // tile with the registers of 8 warps an SM used up, so that a warp's own instruction latency
-// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 75 us, 37%.  Few
+// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 63 us, 44%.  Few
 // short sequences: the chain of dependent reads (lengths, page table, rows, joined records),
-// 4.5 us for one token, 7.8 us for one sequence of 347.
+// 4.6 us for one token, 7.9 us for one sequence of 347.
 // mma.sync rather than tcgen05: the products are 2 G flops a cached byte (under 100 TFLOP/s at
 // the copy rate with 8 heads), E4M3 rows have to pass through registers on their way to fp16
 // anyway, and the softmax stays in the registers that the products leave it in.
@@ -67,8 +67,9 @@ struct DecCfg {
   static constexpr int ES = FMT == CF_E4M3 ? 1 : 2;
   static constexpr int ROW = DP * ES;  // bytes of a row in shared memory
   // 32 tokens a tile where eight warps' rings hold two of them, else 16: a tile's fixed work
-  // counts for more than the ring's depth (D 192, 12 KB a tile: 201 windowed sequences E4M3 80
-  // -> 74 us, 16 x 10000 tokens bf16 55 -> 49 us)
+  // counts for more than the ring's depth (E4M3, D 192, 12 KB a tile: 201 windowed sequences 63 us,
+  // 69 at 16 tokens and a ring of 4; 16 x 20000 tokens 56, 61); and eight warps for the same
+  // reason (bf16, D 192: 16 x 10000 tokens 48 us, 55 with four warps and a ring of 4)
   static constexpr int MT = 2 * ROW * 32 <= 12288 ? 2 : 1;
   static constexpr int TW = 16 * MT, TLOG = 3 + MT;
   static constexpr int KV = 2 * TW * ROW;
@@ -201,13 +202,12 @@ K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
 }
 
 // Units that a sequence's start counts as (its queries, its join): for teams of 4 and 8 warps two
-// (64 sequences up to 4000 tokens, 12 query heads a key head, E4M3: 44.0 us, 46.2 at one), for
-// smaller ones one (200 sequences up to 100 tokens: 14.9 us, 17.9 at two)
+// (64 sequences up to 4000 tokens, 12 query heads a key head, E4M3: 40.7 us, 42.7 at one), for
+// smaller ones one (200 sequences up to 100 tokens: 14.7 us, 17.6 at two)
 K3_DEVI int dec_start(int wlog) { return wlog >= 2 ? 2 : 1; }
 
 // Tiles of a sequence that is never cut: joining its records would take longer than they do (200
-// sequences up to 100 tokens, D 128, E4M3: 16.5 us, 18.3 if they are cut; with teams of a block,
-// where these are less than a unit, cutting stays right: 8 x 1000 tokens 11.3 us, 13.2 whole)
+// sequences up to 100 tokens, D 128, E4M3: 14.7 us, 17.5 if they are cut)
 constexpr int DEC_WHOLE = 4;
 
 // A place in the order of the units: sequence b, key head kvh and group grp of its query heads,
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       wlog = i;
   // teams of half a block, where there are sequences enough for all (HR a sequence) with work for
   // more than a moment, and their ends are frequent (at most 24 units of a block each): while one
-  // team joins, the other streams.  201 windowed sequences, D 192: 66 us, 78 with whole blocks;
-  // 128 up to 2000, D 64: 53, 57; but 64 up to 8192 (64 units each): 172, 168.
+  // team joins, the other streams.  201 windowed sequences, D 192: 63 us, 76 with whole blocks;
+  // 128 up to 2000, D 64: 49.5, 53.9; but 64 up to 8192 (64 units each): 169.7, 166.3.
   const int64_t parts_all = (int64_t)p.B * HR, warps_all = (int64_t)gridDim.x * WARPS;
   if (wlog == 3 && 10 * parts_all >= 8 * (int64_t)gridDim.x && sums[0] * HR >= 4 * warps_all &&
       sums[3] * HR <= 24 * 8 * parts_all)
@@ -493,10 +493,11 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     float2 acc[KSTEPS][NT][2], m[NT], l[NT], vm[NT], qs[NT];  // pairs: of two heads
     uint32_t qf[KSTEPS][NT][2];
     // a part's queries as they are, bf16 (step 4 j + i of an E4M3 contraction holds dims
-    // 64 j + 16 (lane % 4) + 4 i .. + 3).  bf16: loaded while the part before is joined (32 x 2000
-    // tokens, 24 query heads a key head: 35.9 us, 39.4 without); E4M3: at the part's start, as the
-    // registers' longer life costs its inner loop more (2 x 262143 tokens: 126.5 us, 138.7 early)
-    constexpr bool EARLY = FMT == CF_BF16;
+    // 64 j + 16 (lane % 4) + 4 i .. + 3).  bf16: loaded while the part before is joined (128
+    // sequences up to 2000 tokens, D 64: 49.5 us, 52.5 without; 32 x 5000, 5 heads of 96: 48, 51);
+    // E4M3, and 16 bf16 heads of 256 dims: at the part's start, as the registers' longer life costs
+    // the inner loop more (2 x 262143 tokens, E4M3: 123 us, 138 early; 16 x 8000, D 256: 49.6, 52.1)
+    constexpr bool EARLY = FMT == CF_BF16 && KSTEPS * NT < 32;
     auto load_queries = [&](const DecAt& a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
