@@ -341,6 +341,25 @@ def test_decode(attn, Hq, Hkv, D, page, window, order, lens, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 1, 64), (24, 2, 96), (32, 2, 128), (60, 3, 128), (36, 3, 192), (24, 2, 256),
+                                      (17, 1, 256)])
+def test_decode_of_many_query_heads_with_room_in_the_page_table(attn, Hq, Hkv, D, fmt):
+    """Calls are shaped by the lengths that the table allows: the same ones with a table of just
+    the pages that the sequences have and with one for 2^20 tokens (its rest is never read)."""
+    d = attn.dims(Hq, Hkv, D)
+    for lens in (LENS, [0, 500, 2300]):
+        q, cache, table, lens_t, slots, ws = _sequences(attn, d, lens, 16, fmt, 28)
+        wide = torch.full((len(lens), 2 ** 16), -1, device="cuda", dtype=torch.int32)
+        wide[:, :table.shape[1]] = table
+        for t in (table, wide, table):
+            out, lse = _run_decode(attn, d, q, cache, t, lens_t, ws)
+            _check_decode(attn, d, q, cache, slots, lens, out, lse, 16)
+            out2, lse2 = _run_decode(attn, d, q, cache, t, lens_t, ws)
+            assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and torch.equal(lse, lse2)
+        assert attn.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_decode_sharp_logits_and_values_of_many_sizes(attn, fmt):
     """Logits of hundreds (one token takes all) and values whose rows differ by up to e^(4 * 4)
     in size."""
