@@ -144,8 +144,10 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
  *     page_size is below 2^31.  They must not change while the call runs
  *   out [B, Hq, D] bf16;  lse [B, Hq] f32 or NULL
  * The work is split evenly over the SMs whatever the lengths, which are read on the device
- * (a captured call replays with new ones).  The result does not depend on the order in which
- * the parts finish. */
+ * (a captured call replays with new ones).  With more than 8 query heads a key head the longest
+ * length that table_width and window allow decides between two ways to group the heads: a table
+ * much wider than the sequences is right, and slower for few short ones.  The result does not
+ * depend on the order in which the parts finish. */
 k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q, int64_t q_stride,
                            const k3attn_cache* cache, const int32_t* page_table, int32_t table_width,
                            const int32_t* lens, uint16_t* out, float* lse, void* ws, size_t ws_bytes,

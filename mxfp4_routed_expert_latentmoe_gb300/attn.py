@@ -221,7 +221,8 @@ def kv_read(d: Dims, slots, cache: KVCache, k_out, v_out, ws, stream=None):
 
 def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None):
     """k3attn_decode: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
-    of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32."""
+    of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32.  With more
+    than 8 query heads a key head a table just wide enough is faster for few short sequences."""
     code = (_native or _load()).decode(d.addr, q, cache.addr, cache.rows, page_table, lens, out, lse, ws,
                                        _handle(stream))
     if code:
