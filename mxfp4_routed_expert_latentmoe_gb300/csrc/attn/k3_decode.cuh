@@ -35,6 +35,8 @@
 // has its own sequence, and waits for nobody).
 #pragma once
 
+#include <type_traits>
+
 #include "k3_qkv.cuh"
 
 namespace k3 {
@@ -864,8 +866,11 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       if (s_last[team]) {
         const DecPart x = s_part[2 * team + slot];
         if (tthread == 0) p.arrived[x.c0] = 0;
-        // SIDE quads of dims a thread and BATCH records at a time, whose loads are in flight together
-        constexpr int QUADS = HEADS * DP / 4 / THREADS, SIDE = QUADS >= 4 ? 4 : QUADS >= 2 ? 2 : 1, BATCH = 8 / SIDE;
+        // SIDE quads of dims a thread and some records at a time, whose loads are in flight
+        // together: 8 / SIDE of few records, 32 / SIDE of more than 16 (1 x 64000 tokens, 8 heads,
+        // D 128, bf16 18.6 us, 22.0 at 8; E4M3 18.4, 19.6; but 8 x 1000 tokens 11.3, 10.5 at 8).
+        // 16 heads keep to 8: the registers cost them more (201 windowed sequences 64.6 us, 63.2)
+        constexpr int QUADS = HEADS * DP / 4 / THREADS, SIDE = QUADS >= 4 ? 4 : QUADS >= 2 ? 2 : 1;
         for (int i0 = tthread; i0 < x.heads * (DP / 4); i0 += SIDE * tthreads) {
           float top[SIDE], sum[SIDE], o[SIDE][4];
           int h[SIDE], d[SIDE];
@@ -877,7 +882,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             top[s] = -INFINITY;
             sum[s] = o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
           }
-          for (int j0 = 0; j0 < x.parts; j0 += BATCH) {
+          auto take = [&](int j0, auto at_once) {
+            constexpr int BATCH = decltype(at_once)::value;
             float2 ml[SIDE][BATCH];
             float4 v[SIDE][BATCH];
 #pragma unroll
@@ -915,7 +921,11 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
                 o[s][3] = fmaf(v[s][j].w, f, o[s][3]);
               }
             }
-          }
+          };
+          if (NT == 1 && x.parts > 16)
+            for (int j0 = 0; j0 < x.parts; j0 += 32 / SIDE) take(j0, std::integral_constant<int, 32 / SIDE>());
+          else
+            for (int j0 = 0; j0 < x.parts; j0 += 8 / SIDE) take(j0, std::integral_constant<int, 8 / SIDE>());
 #pragma unroll
           for (int s = 0; s < SIDE; ++s) {
             if (h[s] >= x.heads) continue;
