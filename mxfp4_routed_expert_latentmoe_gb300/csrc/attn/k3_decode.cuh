@@ -41,6 +41,8 @@
 
 namespace k3 {
 
+#define K3_HD __host__ __device__ __forceinline__  // also called by a test on the host
+
 struct DecodeParams {
   const uint16_t* q;
   int64_t q_stride;
@@ -87,6 +89,13 @@ struct DecCfg {
   static constexpr int REC = HEADS * (DP + 2);  // floats of a record: sums, and each head's maximum and sum of weights
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && PN * 8 * DP * 4 <= KV, "does not fit");
 };
+
+// zeros in a warp's ring, by its 32 lanes
+template <typename C>
+K3_HD void clear_ring(uint8_t* rings, int warp, int lane) {
+  uint4* const x = reinterpret_cast<uint4*>(rings + warp * (C::RING / C::WARPS));
+  for (int i = lane; i < C::RING / C::WARPS / 16; i += 32) x[i] = make_uint4(0, 0, 0, 0);
+}
 
 // D += A B on pairs of sums
 K3_DEVI void mma2_bf16(float2 (&d)[2], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -283,10 +292,12 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   DecPart* const s_part = reinterpret_cast<DecPart*>(smem + C::RING + C::ML + 512);        // [teams][2]
   static_assert(2 * DEC_MAX_WARPS * sizeof(DecPart) <= 512 && DEC_MAX_WARPS * 32 <= 256, "shared layout");
 
-  // dims past D: zero in every stage, never written again
-  if (p.D < DP)
-    for (int i = threadIdx.x; i < C::RING / 16; i += THREADS)
-      *reinterpret_cast<uint4*>(smem + 16 * i) = make_uint4(0, 0, 0, 0);
+  // dims past D: zero in every stage, and again wherever a join has written.  A warp clears its
+  // own ring: no other warp's zeros can land on rows or masks that it has copied by then
+  if (p.D < DP) {
+    clear_ring<C>(smem, warp, lane);
+    __syncwarp();
+  }
 
   grid_dep_wait();
   grid_dep_launch();

@@ -1,0 +1,48 @@
+// Host entries over parts of the decode kernel that decide which thread writes and reads what,
+// for tests without a GPU.
+#include "../mxfp4_routed_expert_latentmoe_gb300/csrc/attn/k3_decode.cuh"
+
+namespace {
+using namespace k3;
+
+template <typename F>
+bool with_config(int fmt, int dp, int nt, F&& f) {
+  switch (fmt * 1000 + dp * 2 + nt - 1) {
+    case 128: f(DecCfg<CF_BF16, 64, 1>()); return true;
+    case 129: f(DecCfg<CF_BF16, 64, 2>()); return true;
+    case 256: f(DecCfg<CF_BF16, 128, 1>()); return true;
+    case 257: f(DecCfg<CF_BF16, 128, 2>()); return true;
+    case 384: f(DecCfg<CF_BF16, 192, 1>()); return true;
+    case 385: f(DecCfg<CF_BF16, 192, 2>()); return true;
+    case 512: f(DecCfg<CF_BF16, 256, 1>()); return true;
+    case 513: f(DecCfg<CF_BF16, 256, 2>()); return true;
+    case 1128: f(DecCfg<CF_E4M3, 64, 1>()); return true;
+    case 1129: f(DecCfg<CF_E4M3, 64, 2>()); return true;
+    case 1256: f(DecCfg<CF_E4M3, 128, 1>()); return true;
+    case 1257: f(DecCfg<CF_E4M3, 128, 2>()); return true;
+    case 1384: f(DecCfg<CF_E4M3, 192, 1>()); return true;
+    case 1385: f(DecCfg<CF_E4M3, 192, 2>()); return true;
+    case 1512: f(DecCfg<CF_E4M3, 256, 1>()); return true;
+  }
+  return false;
+}
+}  // namespace
+
+extern "C" {
+
+// An instance's shape: warps, bytes of all rings, tokens of a tile.  0: no such instance.
+int replay_config(int fmt, int dp, int nt, int32_t* shape) {
+  return with_config(fmt, dp, nt, [&](auto c) {
+    using C = decltype(c);
+    shape[0] = C::WARPS;
+    shape[1] = C::RING;
+    shape[2] = C::TW;
+  });
+}
+
+// What one lane of a warp clears of the rings.
+void replay_clear(int fmt, int dp, int nt, uint8_t* rings, int warp, int lane) {
+  with_config(fmt, dp, nt, [&](auto c) { clear_ring<decltype(c)>(rings, warp, lane); });
+}
+
+}  // extern "C"
