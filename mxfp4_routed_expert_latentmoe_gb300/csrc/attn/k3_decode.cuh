@@ -233,6 +233,12 @@ struct DecAt {
     nu = (int32_t)(((uint32_t)(n - first) + (1u << ulog) - 1) >> ulog);
     return !bad;
   }
+  // the token of a row of the tile that a team's warp tw takes of the unit: past the sequence's last
+  // one it may be up to a unit more than n, which passes int32 next to the longest length
+  template <int TW>
+  K3_HD uint32_t token(int W, int tw, int row) const {
+    return (uint32_t)first + ((uint32_t)u * W + tw) * TW + row;
+  }
   // whether the unit is the team's whose range ends in front of `end`
   K3_DEVI bool in(int32_t end, int32_t whole, int start) const { return (nu <= whole ? x - u - start : x) < end; }
   K3_DEVI void next(const DecodeParams& p, int ulog, int32_t end, int start) {
@@ -433,12 +439,12 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     auto fetch = [&]() {
       DecRow r{0, 0, ahead.kvh, ahead.in(end, whole_units, start), false};
       if (r.tile) {
-        const int32_t t = ahead.first + (ahead.u * W + tw) * TW + (lane & (TW - 1));
-        r.in = t < ahead.n;
+        const uint32_t t = ahead.token<TW>(W, tw, lane & (TW - 1));
+        r.in = t < (uint32_t)ahead.n;
         if (r.in) {
           const uint32_t pg = p.c.by_page(t);
           r.entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
-          r.in_page = t - (int32_t)(pg * (uint32_t)p.c.page_size);
+          r.in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
         }
         ahead.next(p, ulog, end, start);
       }

@@ -45,4 +45,12 @@ void replay_clear(int fmt, int dp, int nt, uint8_t* rings, int warp, int lane) {
   with_config(fmt, dp, nt, [&](auto c) { clear_ring<decltype(c)>(rings, warp, lane); });
 }
 
+// The token of a row of a warp's tile of a unit, for tiles of 16 or 32 tokens.
+uint32_t replay_token(int32_t first, int32_t u, int W, int tw, int tile, int row) {
+  DecAt at{};
+  at.first = first;
+  at.u = u;
+  return tile == 16 ? at.token<16>(W, tw, row) : at.token<32>(W, tw, row);
+}
+
 }  // extern "C"

@@ -39,3 +39,17 @@ def test_a_warp_clears_its_own_ring_and_no_other(replay, config):
         each = size // warps
         assert (rings[w * each:(w + 1) * each] == 0).all()
         assert (rings[:w * each] == 0xFF).all() and (rings[(w + 1) * each:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("tile", [16, 32])
+@pytest.mark.parametrize("first", [0, 2 ** 31 - 101, 2 ** 31 - 2, 12345])
+def test_tokens_next_to_the_longest_length_do_not_wrap(replay, first, tile):
+    """A sequence of 2^31 - 1 tokens: the rows of its last unit that lie past it stay past it (a
+    negative token would count as one of the sequence's, and be looked up in front of the table)."""
+    replay.replay_token.restype = ctypes.c_uint32
+    n = 2 ** 31 - 1
+    for W in (1, 2, 4, 8):
+        last = -(-(n - first) // (W * tile)) - 1
+        for u in {0, last // 2, last}:
+            got = [replay.replay_token(first, u, W, tw, tile, row) for tw in range(W) for row in range(tile)]
+            assert got == [first + u * W * tile + i for i in range(W * tile)]

@@ -68,3 +68,31 @@ def test_decode_of_a_padded_head_dim_is_that_of_heads_with_zeros(attn, D, fmt):
         nan()
         out, lse2 = call()
         assert torch.equal(out, want[..., :D]) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [1, 16])
+def test_decode_of_windows_at_the_end_of_the_longest_sequences(attn, G, fmt):
+    """Lengths up to 2^31 - 2, over pages that repeat: the window's tokens alone, whose last tile
+    reaches past 2^31, as a short sequence of the same rows gives them."""
+    page, wide, D = 49981, 42966, 64
+    n = page * wide
+    assert n == 2 ** 31 - 2
+    q = torch.randn(3, G, D, generator=_gen(50), device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn(2 * page, 1, D, generator=_gen(s), device="cuda").to(torch.bfloat16) for s in (51, 52))
+    for window in (100, 1, 257):
+        d = attn.dims(G, 1, D, rot_dim=0, window=window)
+        cache = attn.KVCache.empty(d, 2, page, fmt)
+        ws = attn.workspace(d)
+        attn.kv_write(d, k, v, torch.arange(2 * page, device="cuda", dtype=torch.int32), cache, ws)
+        table = torch.zeros(3, wide, device="cuda", dtype=torch.int32)
+        table[:, -1] = 1
+        table[2, -1] = 0
+        lens = torch.tensor([n, n - 30, n], device="cuda", dtype=torch.int32)
+        out, lse = torch.zeros(3, G, D, device="cuda", dtype=torch.bfloat16), torch.zeros(3, G, device="cuda")
+        attn.decode(d, q, cache, table, lens, out, ws, lse=lse)
+        short = torch.tensor([[0, 1], [0, 1], [0, 0]], device="cuda", dtype=torch.int32)
+        out2, lse2 = torch.zeros_like(out), torch.zeros_like(lse)
+        attn.decode(d, q, cache, short, lens - (n - 2 * page), out2, ws, lse=lse2)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2) and torch.isfinite(lse).all()
+        assert attn.device_status(ws) == 0
