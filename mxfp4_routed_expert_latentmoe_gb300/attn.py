@@ -34,9 +34,9 @@ class Dims(ctypes.Structure):
                 ("rot_dim", ctypes.c_int32), ("rot_interleaved", ctypes.c_int32), ("rms_eps", ctypes.c_float),
                 ("softmax_scale", ctypes.c_float), ("window", ctypes.c_int32)]
 
-    def __init__(self, *args):
-        super().__init__(*args)
-        self.addr = ctypes.addressof(self)
+    @property
+    def addr(self):  # (of this object: a copy has its own)
+        return ctypes.addressof(self)
 
 
 def dims(n_heads, n_kv_heads, head_dim, rot_dim=None, rot_interleaved=False, rms_eps=1e-6, softmax_scale=None,
