@@ -3,8 +3,8 @@ norms of queries and keys per head with the position rotation, the paged key-val
 (bf16, or E4M3 with a scale per row), and the attention of one new token over its pages.
 
 Thin binding over the C ABI declared in ``include/k3attn.h``, which has the formulas.  Every
-function checks its tensors (ValueError), passes pointers and strides, and launches on the
-current CUDA stream or on ``stream``; device-detected conditions (DEV_BAD_*) are read with
+function checks its tensors (ValueError), which all have to be on one device, passes pointers and
+strides, and launches there, on that device's current stream or on ``stream``; device-detected conditions (DEV_BAD_*) are read with
 ``device_status(ws)``.  The operators' checks and calls are native (csrc/attn/k3attn_binding.cpp):
 a decode step's kernels take no longer than they would in Python.
 
@@ -20,7 +20,8 @@ import ctypes
 
 import torch
 
-from . import _ATTN_BINDING, _check, _stream, device_status, lib  # noqa: F401  (device_status: the status word of ws)
+from . import _ATTN_BINDING, _check, _stream, lib
+from . import device_status as _device_status
 
 BF16, E4M3 = 0, 1  # K3ATTN_BF16, K3ATTN_E4M3
 MIN_WORKSPACE = 256  # K3ATTN_MIN_WORKSPACE
@@ -128,7 +129,15 @@ def workspace_init(ws, stream=None):
     """k3attn_workspace_init: readies a workspace (also clears its status word)."""
     if ws.dtype != torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("ws: a contiguous uint8 CUDA tensor is needed")
-    _check(_funcs().k3attn_workspace_init(ws.data_ptr(), ws.numel(), _stream(stream)), "k3attn_workspace_init")
+    with torch.cuda.device(ws.device):
+        _check(_funcs().k3attn_workspace_init(ws.data_ptr(), ws.numel(), _stream(stream)), "k3attn_workspace_init")
+
+
+def device_status(ws, stream=None) -> int:
+    """DEV_BAD_* bits of the calls that used workspace `ws` since it was readied (waits for the
+    stream)."""
+    with torch.cuda.device(ws.device):
+        return _device_status(ws, stream)
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
@@ -147,18 +156,18 @@ class KVCache:
         fmt = E4M3 if k.dtype == torch.float8_e4m3fn else BF16
         shape = (k.shape[0], d.n_kv_heads, k.shape[2], d.head_dim)
         for t, name in ((k, "k"), (v, "v")):
-            if (t.dtype != k.dtype or t.shape != shape or not t.is_cuda or t.stride(3) != 1
+            if (t.dtype != k.dtype or t.shape != shape or not t.is_cuda or t.device != k.device or t.stride(3) != 1
                     or t.stride() != k.stride()):
                 raise ValueError(f"{name}: a CUDA tensor {list(shape)} of {k.dtype}, a row's values dense, with the "
-                                 f"strides of k, is needed, got {list(t.shape)} (strides {list(t.stride())}) of "
+                                 f"strides of k and on its device, is needed, got {list(t.shape)} (strides {list(t.stride())}) of "
                                  f"{t.dtype} on {t.device}")
         n, page, ss = shape[0], shape[2], (0, 0, 0)
         if fmt == E4M3:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if (t is None or t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_cuda
+                if (t is None or t.dtype != torch.float32 or t.shape != shape[:3] or t.device != k.device
                         or t.stride() != k_scale.stride()):
                     raise ValueError(f"{name}: a CUDA tensor {list(shape[:3])} of float32, with the strides of "
-                                     "k_scale, is needed for an E4M3 cache")
+                                     "k_scale and on the device of k, is needed for an E4M3 cache")
             ss = k_scale.stride()
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
@@ -166,7 +175,8 @@ class KVCache:
         self.n_pages, self.page_size = n, page
         self.c = CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt == E4M3 else None,
                         v_scale.data_ptr() if fmt == E4M3 else None, fmt, n, page, 0, *k.stride()[:3], *ss)
-        self.addr, self.rows = ctypes.addressof(self.c), d.n_kv_heads * 65536 + d.head_dim
+        self.addr = ctypes.addressof(self.c)
+        self.rows = (k.device.index << 32) + d.n_kv_heads * 65536 + d.head_dim  # what a call compares with its own
 
     @classmethod
     def empty(cls, d: Dims, n_pages: int, page_size: int, fmt: str = "bf16", device="cuda"):

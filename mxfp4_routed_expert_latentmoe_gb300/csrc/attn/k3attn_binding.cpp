@@ -2,13 +2,15 @@
 // device, strides) and calls the C ABI on their pointers.  A decode step's kernels take a few
 // microseconds; the same checks in Python took as long as they (append: 9.4 us of host time).
 //
-// Every function takes the address of the k3attn_dims (and of the k3attn_cache, with its heads
-// and head dim for comparison), the tensors, and a stream handle or None for the current stream
-// of the tensors' device.  It returns the k3moe_status, or raises ValueError for a tensor that
-// does not fit.  No C++ exception leaves it.
+// Every function takes the address of the k3attn_dims (and of the k3attn_cache, with its device,
+// heads and head dim for comparison), the tensors, which all have to be on one device, and a
+// stream handle or None for the current stream of that device.  The call is made with that device
+// current.  It returns the k3moe_status, or raises ValueError for a tensor that does not fit.  No
+// C++ exception leaves it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -35,7 +37,19 @@ std::string list_of(at::IntArrayRef v) {
   return s + "]";
 }
 
-[[noreturn]] void refuse(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, const char* how) {
+// The device of a call's tensors: that of the first one.
+struct Device {
+  int index = -1;
+  bool takes(const at::Tensor& t) {
+    const int i = (int)t.get_device();
+    if (index < 0) index = i;
+    return i == index;
+  }
+  std::string where() const { return index < 0 ? "" : ", on cuda:" + std::to_string(index) + ","; }
+};
+
+[[noreturn]] void refuse(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, const char* how,
+                         const Device& dev) {
   std::string got;
   if (THPVariable_Check(o)) {
     const at::Tensor& t = THPVariable_Unpack(o);
@@ -44,20 +58,20 @@ std::string list_of(at::IntArrayRef v) {
   } else {
     got = Py_TYPE(o)->tp_name;
   }
-  PyErr_Format(PyExc_ValueError, "%s: a CUDA tensor %s of %s%s is needed, got %s", name, list_of(shape).c_str(),
-               c10::toString(type), how, got.c_str());
+  PyErr_Format(PyExc_ValueError, "%s: a CUDA tensor %s of %s%s%s is needed, got %s", name, list_of(shape).c_str(),
+               c10::toString(type), how, dev.where().c_str(), got.c_str());
   throw Refused{};
 }
 
 // a contiguous tensor's pointer
 template <typename T>
-T* dense(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
+T* dense(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape, Device& dev) {
   if (THPVariable_Check(o)) {
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (t.scalar_type() == type && t.is_cuda() && t.sizes().equals(shape) && t.is_contiguous())
+    if (t.scalar_type() == type && t.is_cuda() && t.sizes().equals(shape) && t.is_contiguous() && dev.takes(t))
       return static_cast<T*>(t.data_ptr());
   }
-  refuse(o, name, type, shape, ", contiguous");
+  refuse(o, name, type, shape, ", contiguous", dev);
 }
 
 struct Rows {
@@ -65,14 +79,14 @@ struct Rows {
   int64_t stride;
 };
 // a [T, heads, D] bf16 tensor whose tokens' rows are dense: its pointer and token stride
-Rows rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_t D) {
+Rows rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_t D, Device& dev) {
   if (THPVariable_Check(o)) {
     const at::Tensor& t = THPVariable_Unpack(o);
     if (t.scalar_type() == at::kBFloat16 && t.is_cuda() && t.sizes().equals({T, heads, D}) && t.stride(2) == 1 &&
-        (t.stride(1) == D || heads == 1))
+        (t.stride(1) == D || heads == 1) && dev.takes(t))
       return {static_cast<const uint16_t*>(t.data_ptr()), T > 1 ? t.stride(0) : heads * D};
   }
-  refuse(o, name, at::kBFloat16, {T, heads, D}, ", the heads of a token dense,");
+  refuse(o, name, at::kBFloat16, {T, heads, D}, ", the heads of a token dense", dev);
 }
 
 // the first size of a tensor (the tokens of a call)
@@ -89,21 +103,29 @@ struct Work {
   void* p;
   size_t bytes;
 };
-Work workspace(PyObject* o) {
+Work workspace(PyObject* o, Device& dev) {
   if (THPVariable_Check(o)) {
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (t.scalar_type() == at::kByte && t.is_cuda() && t.is_contiguous()) return {t.data_ptr(), (size_t)t.numel()};
+    if (t.scalar_type() == at::kByte && t.is_cuda() && t.is_contiguous() && dev.takes(t))
+      return {t.data_ptr(), (size_t)t.numel()};
   }
-  PyErr_SetString(PyExc_ValueError, "ws: a contiguous uint8 CUDA tensor is needed");
+  PyErr_Format(PyExc_ValueError, "ws: a contiguous uint8 CUDA tensor%s is needed", dev.where().c_str());
   throw Refused{};
 }
 
-void* stream_of(PyObject* stream, PyObject* tensor) {
-  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(THPVariable_Unpack(tensor).get_device()).stream();
-  void* s = PyLong_AsVoidPtr(stream);
-  if (!s && PyErr_Occurred()) throw Refused{};
-  return s;
-}
+// The tensors' device made current, and the call's stream there.
+struct Stream {
+  c10::cuda::CUDAGuard guard;
+  void* handle;
+  Stream(PyObject* stream, const Device& dev) : guard((c10::DeviceIndex)dev.index) {
+    if (stream == Py_None) {
+      handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
+    } else {
+      handle = PyLong_AsVoidPtr(stream);
+      if (!handle && PyErr_Occurred()) throw Refused{};
+    }
+  }
+};
 
 template <typename T>
 const T* struct_at(PyObject* address) {
@@ -115,13 +137,18 @@ const T* struct_at(PyObject* address) {
   return p;
 }
 
-// the cache at `address` whose rows are `heads` x `D` (one number: heads * 65536 + D)
-const k3attn_cache* cache_at(PyObject* address, PyObject* shape, const k3attn_dims& d) {
-  const long s = PyLong_AsLong(shape);
-  if (s != (long)d.n_kv_heads * 65536 + d.head_dim) {
-    if (!PyErr_Occurred())
-      PyErr_Format(PyExc_ValueError, "the cache's (Hkv, D) are (%ld, %ld), the dims' (%d, %d)", s / 65536, s % 65536,
-                   (int)d.n_kv_heads, (int)d.head_dim);
+// the cache at `address` on the call's device, whose rows are `heads` x `D` (one number: device *
+// 2^32 + heads * 65536 + D)
+const k3attn_cache* cache_at(PyObject* address, PyObject* what, const k3attn_dims& d, const Device& dev) {
+  const long s = PyLong_AsLong(what), shape = s & 0xFFFFFFFFl;
+  if (PyErr_Occurred()) throw Refused{};
+  if (shape != (long)d.n_kv_heads * 65536 + d.head_dim) {
+    PyErr_Format(PyExc_ValueError, "the cache's (Hkv, D) are (%ld, %ld), the dims' (%d, %d)", shape / 65536,
+                 shape % 65536, (int)d.n_kv_heads, (int)d.head_dim);
+    throw Refused{};
+  }
+  if (s >> 32 != dev.index) {
+    PyErr_Format(PyExc_ValueError, "the cache is on cuda:%ld, the tensors are on cuda:%d", s >> 32, dev.index);
     throw Refused{};
   }
   return struct_at<k3attn_cache>(address);
@@ -133,12 +160,13 @@ struct Norm {
   const double* inv_freq;
   const float *q_w, *k_w;
 };
-Norm norm(const k3attn_dims& d, int64_t T, PyObject* positions, PyObject* inv_freq, PyObject* q_w, PyObject* k_w) {
+Norm norm(const k3attn_dims& d, int64_t T, PyObject* positions, PyObject* inv_freq, PyObject* q_w, PyObject* k_w,
+          Device& dev) {
   Norm n;
-  n.positions = dense<int32_t>(positions, "positions", at::kInt, {T});
-  n.inv_freq = d.rot_dim ? dense<double>(inv_freq, "inv_freq", at::kDouble, {d.rot_dim / 2}) : nullptr;
-  n.q_w = dense<float>(q_w, "q_w", at::kFloat, {d.head_dim});
-  n.k_w = dense<float>(k_w, "k_w", at::kFloat, {d.head_dim});
+  n.positions = dense<int32_t>(positions, "positions", at::kInt, {T}, dev);
+  n.inv_freq = d.rot_dim ? dense<double>(inv_freq, "inv_freq", at::kDouble, {d.rot_dim / 2}, dev) : nullptr;
+  n.q_w = dense<float>(q_w, "q_w", at::kFloat, {d.head_dim}, dev);
+  n.k_w = dense<float>(k_w, "k_w", at::kFloat, {d.head_dim}, dev);
   return n;
 }
 
@@ -163,13 +191,15 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
 PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&] {
     const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
+    Device dev;
     const int32_t T = first_size(a[1], "q");
-    const Rows q = rows(a[1], "q", T, d.n_heads, d.head_dim), k = rows(a[2], "k", T, d.n_kv_heads, d.head_dim);
-    const Norm m = norm(d, T, a[3], a[4], a[5], a[6]);
-    uint16_t* q_out = dense<uint16_t>(a[7], "q_out", at::kBFloat16, {T, d.n_heads, d.head_dim});
-    uint16_t* k_out = dense<uint16_t>(a[8], "k_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim});
+    const Rows q = rows(a[1], "q", T, d.n_heads, d.head_dim, dev),
+               k = rows(a[2], "k", T, d.n_kv_heads, d.head_dim, dev);
+    const Norm m = norm(d, T, a[3], a[4], a[5], a[6], dev);
+    uint16_t* q_out = dense<uint16_t>(a[7], "q_out", at::kBFloat16, {T, d.n_heads, d.head_dim}, dev);
+    uint16_t* k_out = dense<uint16_t>(a[8], "k_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim}, dev);
     return f_norm_rope(&d, T, q.p, q.stride, k.p, k.stride, m.positions, m.inv_freq, m.q_w, m.k_w, q_out, k_out,
-                       stream_of(a[9], a[1]));
+                       Stream(a[9], dev).handle);
   });
 }
 
@@ -177,12 +207,14 @@ PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&] {
     const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
+    Device dev;
     const int32_t T = first_size(a[1], "k");
-    const Rows k = rows(a[1], "k", T, d.n_kv_heads, d.head_dim), v = rows(a[2], "v", T, d.n_kv_heads, d.head_dim);
-    const int32_t* slots = dense<int32_t>(a[3], "slots", at::kInt, {T});
-    const k3attn_cache* c = cache_at(a[4], a[5], d);
-    const Work w = workspace(a[6]);
-    return f_write(&d, T, k.p, k.stride, v.p, v.stride, slots, c, w.p, w.bytes, stream_of(a[7], a[1]));
+    const Rows k = rows(a[1], "k", T, d.n_kv_heads, d.head_dim, dev),
+               v = rows(a[2], "v", T, d.n_kv_heads, d.head_dim, dev);
+    const int32_t* slots = dense<int32_t>(a[3], "slots", at::kInt, {T}, dev);
+    const k3attn_cache* c = cache_at(a[4], a[5], d, dev);
+    const Work w = workspace(a[6], dev);
+    return f_write(&d, T, k.p, k.stride, v.p, v.stride, slots, c, w.p, w.bytes, Stream(a[7], dev).handle);
   });
 }
 
@@ -190,19 +222,21 @@ PyObject* py_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 15, [&] {
     const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
+    Device dev;
     const int32_t T = first_size(a[1], "q");
-    const Rows q = rows(a[1], "q", T, d.n_heads, d.head_dim), k = rows(a[2], "k", T, d.n_kv_heads, d.head_dim),
-               v = rows(a[3], "v", T, d.n_kv_heads, d.head_dim);
-    const Norm m = norm(d, T, a[4], a[6], a[7], a[8]);
-    const int32_t* slots = dense<int32_t>(a[5], "slots", at::kInt, {T});
-    const k3attn_cache* c = cache_at(a[9], a[10], d);
-    uint16_t* q_out = dense<uint16_t>(a[11], "q_out", at::kBFloat16, {T, d.n_heads, d.head_dim});
+    const Rows q = rows(a[1], "q", T, d.n_heads, d.head_dim, dev),
+               k = rows(a[2], "k", T, d.n_kv_heads, d.head_dim, dev),
+               v = rows(a[3], "v", T, d.n_kv_heads, d.head_dim, dev);
+    const Norm m = norm(d, T, a[4], a[6], a[7], a[8], dev);
+    const int32_t* slots = dense<int32_t>(a[5], "slots", at::kInt, {T}, dev);
+    const k3attn_cache* c = cache_at(a[9], a[10], d, dev);
+    uint16_t* q_out = dense<uint16_t>(a[11], "q_out", at::kBFloat16, {T, d.n_heads, d.head_dim}, dev);
     uint16_t* k_out = a[12] == Py_None
                           ? nullptr
-                          : dense<uint16_t>(a[12], "k_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim});
-    const Work w = workspace(a[13]);
+                          : dense<uint16_t>(a[12], "k_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim}, dev);
+    const Work w = workspace(a[13], dev);
     return f_append(&d, T, q.p, q.stride, k.p, k.stride, v.p, v.stride, m.positions, slots, m.inv_freq, m.q_w, m.k_w, c,
-                    q_out, k_out, w.p, w.bytes, stream_of(a[14], a[1]));
+                    q_out, k_out, w.p, w.bytes, Stream(a[14], dev).handle);
   });
 }
 
@@ -210,13 +244,14 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&] {
     const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
+    Device dev;
     const int32_t T = first_size(a[1], "slots");
-    const int32_t* slots = dense<int32_t>(a[1], "slots", at::kInt, {T});
-    const k3attn_cache* c = cache_at(a[2], a[3], d);
-    uint16_t* k_out = dense<uint16_t>(a[4], "k_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim});
-    uint16_t* v_out = dense<uint16_t>(a[5], "v_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim});
-    const Work w = workspace(a[6]);
-    return f_read(&d, T, slots, c, k_out, v_out, w.p, w.bytes, stream_of(a[7], a[1]));
+    const int32_t* slots = dense<int32_t>(a[1], "slots", at::kInt, {T}, dev);
+    const k3attn_cache* c = cache_at(a[2], a[3], d, dev);
+    uint16_t* k_out = dense<uint16_t>(a[4], "k_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim}, dev);
+    uint16_t* v_out = dense<uint16_t>(a[5], "v_out", at::kBFloat16, {T, d.n_kv_heads, d.head_dim}, dev);
+    const Work w = workspace(a[6], dev);
+    return f_read(&d, T, slots, c, k_out, v_out, w.p, w.bytes, Stream(a[7], dev).handle);
   });
 }
 
@@ -224,19 +259,20 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&] {
     const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
+    Device dev;
     const int32_t B = first_size(a[1], "q");
-    const Rows q = rows(a[1], "q", B, d.n_heads, d.head_dim);
-    const k3attn_cache* c = cache_at(a[2], a[3], d);
+    const Rows q = rows(a[1], "q", B, d.n_heads, d.head_dim, dev);
+    const k3attn_cache* c = cache_at(a[2], a[3], d, dev);
     int64_t width = -1;
     if (THPVariable_Check(a[4]) && THPVariable_Unpack(a[4]).dim() == 2) width = THPVariable_Unpack(a[4]).size(1);
-    const int32_t* table = dense<int32_t>(a[4], "page_table", at::kInt, {B, width});
-    const int32_t* lens = dense<int32_t>(a[5], "lens", at::kInt, {B});
-    uint16_t* out = dense<uint16_t>(a[6], "out", at::kBFloat16, {B, d.n_heads, d.head_dim});
-    float* lse = a[7] == Py_None ? nullptr : dense<float>(a[7], "lse", at::kFloat, {B, d.n_heads});
-    const Work w = workspace(a[8]);
+    const int32_t* table = dense<int32_t>(a[4], "page_table", at::kInt, {B, width}, dev);
+    const int32_t* lens = dense<int32_t>(a[5], "lens", at::kInt, {B}, dev);
+    uint16_t* out = dense<uint16_t>(a[6], "out", at::kBFloat16, {B, d.n_heads, d.head_dim}, dev);
+    float* lse = a[7] == Py_None ? nullptr : dense<float>(a[7], "lse", at::kFloat, {B, d.n_heads}, dev);
+    const Work w = workspace(a[8], dev);
     if (width > INT32_MAX) return K3MOE_ERR_SHAPE;
     return f_decode(&d, B, q.p, q.stride, c, table, (int32_t)width, lens, out, lse, w.p, w.bytes,
-                    stream_of(a[9], a[1]));
+                    Stream(a[9], dev).handle);
   });
 }
 
