@@ -28,7 +28,7 @@
 // The work is cut into units (W tiles of one (sequence, key head, head group), one for each of
 // the W warps of a team), and the units, in a line, are dealt out evenly to all teams, whatever
 // the lengths; a sequence's start counts as one or two more, and a sequence of at most DEC_WHOLE tiles
-// stays with the team that its start falls to.  A team joins its warps' sums at the end
+// stays with the team that the first place of its start falls to.  A team joins its warps' sums at the end
 // of a sequence's part; a part that is not a whole sequence leaves an unnormalised record in the
 // workspace, and the team that arrives last joins a sequence's records, in order.  Long
 // sequences have teams of a whole block (few records), short ones of 4, 2 or 1 warps (a warp
@@ -183,7 +183,7 @@ K3_DEVI uint32_t chunk_at(int r, int c) {
 }
 
 // a / b of non-negative numbers (that are nearly always short)
-K3_DEVI int64_t div64(int64_t a, int64_t b) {
+K3_HD int64_t div64(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
   return a / b;
 }
@@ -205,8 +205,12 @@ K3_DEVI uint32_t arrive(uint32_t* counter) {
 }
 
 // length of sequence b within what its table can hold
-K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
+K3_HD int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
+#ifdef __CUDA_ARCH__
   const int32_t n = __ldg(p.lens + b);
+#else
+  const int32_t n = p.lens[b];
+#endif
   const int64_t most = (int64_t)p.table_width * p.c.page_size;
   bad = n < 0 || n > most;
   return n < 0 ? 0 : (n > most ? (int32_t)most : n);
@@ -215,7 +219,7 @@ K3_DEVI int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
 // Units that a sequence's start counts as (its queries, its join): for teams of 4 and 8 warps two
 // (64 sequences up to 4000 tokens, 12 query heads a key head, E4M3: 40.7 us, 42.7 at one), for
 // smaller ones one (200 sequences up to 100 tokens: 14.7 us, 17.6 at two)
-K3_DEVI int dec_start(int wlog) { return wlog >= 2 ? 2 : 1; }
+K3_HD int dec_start(int wlog) { return wlog >= 2 ? 2 : 1; }
 
 // Tiles of a sequence that is never cut: joining its records would take longer than they do (200
 // sequences up to 100 tokens, D 128, E4M3: 14.7 us, 17.5 if they are cut)
@@ -226,7 +230,7 @@ constexpr int DEC_WHOLE = 4;
 // (of each group) counted in front of its units.
 struct DecAt {
   int32_t b, kvh, grp, u, nu, first, n, x;
-  K3_DEVI bool open(const DecodeParams& p, int ulog) {  // sequence b's tokens and units; false: a bad length
+  K3_HD bool open(const DecodeParams& p, int ulog) {  // sequence b's tokens and units; false: a bad length
     bool bad;
     n = seq_len(p, b, bad);
     first = p.window > 0 && n > p.window ? n - p.window : 0;
@@ -240,8 +244,8 @@ struct DecAt {
     return (uint32_t)first + ((uint32_t)u * W + tw) * TW + row;
   }
   // whether the unit is the team's whose range ends in front of `end`
-  K3_DEVI bool in(int32_t end, int32_t whole, int start) const { return (nu <= whole ? x - u - start : x) < end; }
-  K3_DEVI void next(const DecodeParams& p, int ulog, int32_t end, int start) {
+  K3_HD bool in(int32_t end, int32_t whole, int start) const { return (nu <= whole ? x - u - start : x) < end; }
+  K3_HD void next(const DecodeParams& p, int ulog, int32_t end, int start) {
     ++x;
     if (++u < nu) return;
     x += start;
@@ -255,6 +259,22 @@ struct DecAt {
       if (++b >= p.B) return;
       open(p, ulog);
     } while (nu == 0);
+  }
+  // the team's first unit: its range begins `off` places after the first one of sequence b (open)
+  K3_HD void land(const DecodeParams& p, int ulog, int64_t off, int32_t end, int32_t whole, int start) {
+    const int32_t hr = (int32_t)div64(off, nu + start);
+    kvh = hr / p.groups;
+    grp = hr - kvh * p.groups;
+    u = (int32_t)(off - (int64_t)hr * (nu + start)) - start;
+    x = 0;
+    if (nu <= whole && u != -start) {  // behind the start's first place: another team's
+      x = nu - 1 - u;
+      u = nu - 1;
+      next(p, ulog, end, start);
+    } else if (u < 0) {  // at a start
+      x = -u;
+      u = 0;
+    }
   }
 };
 // A lane's row of a tile, on its way to be copied: its page (an entry of the page table, still
@@ -415,19 +435,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   const int32_t end = (int32_t)max((int64_t)0, min(min(total - unit0, chunk), (int64_t)INT32_MAX));
   if (tthread < 2) s_part[2 * team + tthread].there = 0;
   if (end > 0) {
-    const int32_t hr = (int32_t)div64(off, at.nu + start);
-    at.kvh = hr / p.groups;
-    at.grp = hr - at.kvh * p.groups;
-    at.u = (int32_t)(off - (int64_t)hr * (at.nu + start)) - start;
-    at.x = 0;
-    if (at.u < 0) {  // a sequence's start
-      at.x = -at.u;
-      at.u = 0;
-    } else if (at.nu <= whole_units) {  // another team's
-      at.x = at.nu - 1 - at.u;
-      at.u = at.nu - 1;
-      at.next(p, ulog, end, start);
-    }
+    at.land(p, ulog, off, end, whole_units, start);
     DecAt ahead = at;  // the next tile whose page entries are to be read
     uint32_t got[2] = {0, 0};  // arrivals before this team's (of its first thread)
     bool cut = false;          // there is a part that is not a whole sequence

@@ -53,4 +53,37 @@ uint32_t replay_token(int32_t first, int32_t u, int W, int tw, int tile, int row
   return tile == 16 ? at.token<16>(W, tw, row) : at.token<32>(W, tw, row);
 }
 
+// The units that a team takes, as (b, kvh, grp, u) each: its range begins `off` places after the
+// first one of sequence b and has `end` places.  Returns their number (at most `most` are written).
+int replay_team(const int32_t* lens, int B, int Hkv, int groups, int window, int longest, int tile_log, int wlog,
+                int whole, int start, int b, int64_t off, int32_t end, int32_t* units, int most) {
+  DecodeParams p{};
+  p.B = B;
+  p.Hkv = Hkv;
+  p.groups = groups;
+  p.window = window;
+  p.lens = lens;
+  p.table_width = longest;
+  p.c.page_size = 1;
+  DecAt at{};
+  at.b = b;
+  at.open(p, tile_log + wlog);
+  int n = 0;
+  for (at.land(p, tile_log + wlog, off, end, whole, start); at.in(end, whole, start); at.next(p, tile_log + wlog, end, start)) {
+    if (n < most) {
+      units[4 * n] = at.b;
+      units[4 * n + 1] = at.kvh;
+      units[4 * n + 2] = at.grp;
+      units[4 * n + 3] = at.u;
+    }
+    ++n;
+  }
+  return n;
+}
+
+// Places of a sequence's start, and the most units of a sequence that is not cut, for teams of
+// 2^wlog warps.
+int replay_start(int wlog) { return dec_start(wlog); }
+int replay_whole(int wlog) { return DEC_WHOLE >> wlog; }
+
 }  // extern "C"

@@ -53,3 +53,62 @@ def test_tokens_next_to_the_longest_length_do_not_wrap(replay, first, tile):
         for u in {0, last // 2, last}:
             got = [replay.replay_token(first, u, W, tw, tile, row) for tw in range(W) for row in range(tile)]
             assert got == [first + u * W * tile + i for i in range(W * tile)]
+
+
+def _deal(replay, lens, Hkv, groups, window, tile_log, wlog, teams):
+    """Every team's units, as the kernel deals them out."""
+    unit, start, whole = 1 << (tile_log + wlog), replay.replay_start(wlog), replay.replay_whole(wlog)
+    c_lens = (ctypes.c_int32 * len(lens))(*lens)
+    nu = [-(-(min(n, window) if window else n) // unit) for n in lens]
+    places = [(x + start) * Hkv * groups if x else 0 for x in nu]
+    first, total = [sum(places[:b]) for b in range(len(lens))], sum(places)
+    chunk = max(1, -(-total // teams))
+    most = total + 4
+    got, buf = [], (ctypes.c_int32 * (4 * most))()
+    for team in range(teams):
+        unit0 = team * chunk
+        if unit0 >= total:
+            got.append([])
+            continue
+        b = max(i for i in range(len(lens)) if places[i] and first[i] <= unit0)
+        n = replay.replay_team(c_lens, len(lens), Hkv, groups, window, 2 ** 31 - 1, tile_log, wlog, whole, start, b,
+                               ctypes.c_int64(unit0 - first[b]), min(total - unit0, chunk), buf, most)
+        assert n <= most
+        got.append([tuple(buf[4 * i:4 * i + 4]) for i in range(n)])
+    return got, nu, whole
+
+
+@pytest.mark.parametrize("wlog", [0, 1, 2, 3])
+@pytest.mark.parametrize("kind", ["short", "mixed", "long", "window"])
+def test_every_unit_is_dealt_to_one_team(replay, kind, wlog):
+    """Random batches: each unit of each (sequence, key head, head group) is taken once, in order;
+    a sequence of few units by one team; the teams of a cut one follow each other."""
+    rng = np.random.default_rng([11, wlog, len(kind)])
+    for it in range(60):
+        tile_log = 4 + it % 2
+        unit = 1 << (tile_log + wlog)
+        B = int(rng.integers(1, 90))
+        top = dict(short=unit, mixed=6 * unit, long=40 * unit, window=9 * unit)[kind]
+        lens = [int(x) for x in rng.integers(0, top + 1, B)]
+        if it % 5 == 0:
+            lens = [min(top, unit)] * B  # all alike: borders fall on every place of a start
+        window = int(rng.integers(1, 3 * unit)) if kind == "window" else 0
+        Hkv, groups = int(rng.integers(1, 5)), int(rng.integers(1, 3))
+        teams = int(rng.choice([1, 3, 19, 152, 304, 1216]))
+        got, nu, whole = _deal(replay, lens, Hkv, groups, window, tile_log, wlog, teams)
+        assert [u for team in got for u in team] == [(b, h, g, u) for b in range(B) for h in range(Hkv)
+                                                     for g in range(groups) for u in range(nu[b])], (it, teams)
+        for team in got:  # what is not cut comes whole
+            for b, h, g, u in team:
+                if nu[b] <= whole:
+                    assert all((b, h, g, i) in team for i in range(nu[b]))
+
+
+def test_short_sequences_at_every_border_are_dealt_once(replay):
+    """As many one-unit sequences as there are teams, and some more and less: a team's range may
+    begin at each place of a start."""
+    for wlog in (0, 1, 2, 3):
+        unit = 1 << (5 + wlog)
+        for B in (50, 200, 402, 700):
+            got, _, _ = _deal(replay, [unit] * B, 1, 1, 0, 5, wlog, 304)
+            assert sum(len(t) for t in got) == B
