@@ -301,6 +301,10 @@ K3_DEVI float lse_of(float base, float sum) {
   return sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
 }
 
+// The largest weight of E4M3 values is 2^15 (fp16's largest number is 65504), so that weights down to
+// 2^-40 of it count: 2^31 tokens of less weight each are lost with less than 2^-9 of the result.
+constexpr float TOP = 15.f;
+
 template <int FMT, int DP, int NT>
 __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_kernel(const DecodeParams p) {
   using C = DecCfg<FMT, DP, NT>;
@@ -640,83 +644,84 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             }
           }
         }
-        // ---- weights: the raw logits times the keys' scales; the factor qs of a head (softmax
-        // scale, log2(e), the scale of its fp16 queries) goes into the exponent's FMA
+        // ---- weights: 2^(logit - maximum), the logits (in powers of two) rounded before the maximum
+        // is taken off, so that the largest weight is 1 whatever their size.  E4M3: a value's scale is
+        // added to its weight's exponent, next to the maximum (beside a large logit it would have no
+        // digits left), and the sums of values have a maximum of their own (vm, on top of m)
         float lvs[MT][2];  // log2 of the values' scales
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 16 * mt + lane / 4 + 8 * e;
+            float ks = 1.f;
             if constexpr (FMT == CF_E4M3) {
-              const float ks = lds_f32(st + C::KV + 4 * r);
+              ks = lds_f32(st + C::KV + 4 * r);
               lvs[mt][e] = lg2(lds_f32(st + C::KV + 4 * (TW + r)));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) s[mt][nt][e] = mul2(s[mt][nt][e], make_float2(ks, ks));
             }
-            if (mask != 0xFFFFFFFFu) {
-              const bool ok = (mask >> r) & 1u;
+            const bool ok = (mask >> r) & 1u;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                if (!ok) s[mt][nt][e] = make_float2(-INFINITY, -INFINITY);
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (FMT == CF_E4M3) s[mt][nt][e] = mul2(s[mt][nt][e], make_float2(ks, ks));
+              s[mt][nt][e] = mul2(s[mt][nt][e], qs[nt]);
+              if (mask != 0xFFFFFFFFu && !ok) s[mt][nt][e] = make_float2(-INFINITY, -INFINITY);
             }
           }
         uint32_t pf[MT][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          // maxima: of the raw logits, and (E4M3) of the logits with the values' scales
-          float2 t = s[0][nt][0], tv = make_float2(-INFINITY, -INFINITY), sv[MT][2];
+          auto warp_max = [&](float2 t) {  // of the largest of s
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              t = make_float2(fmaxf(t.x, s[mt][nt][e].x), fmaxf(t.y, s[mt][nt][e].y));
-              if constexpr (FMT == CF_E4M3) {
-                sv[mt][e] = fma2(s[mt][nt][e], qs[nt], make_float2(lvs[mt][e], lvs[mt][e]));
-                tv = make_float2(fmaxf(tv.x, sv[mt][e].x), fmaxf(tv.y, sv[mt][e].y));
-              }
+              for (int e = 0; e < 2; ++e) t = make_float2(fmaxf(t.x, s[mt][nt][e].x), fmaxf(t.y, s[mt][nt][e].y));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              t.x = fmaxf(t.x, __shfl_xor_sync(0xFFFFFFFFu, t.x, o));
+              t.y = fmaxf(t.y, __shfl_xor_sync(0xFFFFFFFFu, t.y, o));
             }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            t.x = fmaxf(t.x, __shfl_xor_sync(0xFFFFFFFFu, t.x, o));
-            t.y = fmaxf(t.y, __shfl_xor_sync(0xFFFFFFFFu, t.y, o));
-            if constexpr (FMT == CF_E4M3) {
-              tv.x = fmaxf(tv.x, __shfl_xor_sync(0xFFFFFFFFu, tv.x, o));
-              tv.y = fmaxf(tv.y, __shfl_xor_sync(0xFFFFFFFFu, tv.y, o));
-            }
-          }
-          t = mul2(t, qs[nt]);
-          float2 fall, down, vdown;  // what old sums shrink by; the exponents' bases, negated
+            return t;
+          };
+          // a maximum moved to what is here now; f: what old sums shrink by, d: the exponents' base, negated
           auto rebase = [](float& top, float now, float& f, float& d) {
             const float m1 = fmaxf(top, now), base = m1 == -INFINITY ? 0.f : m1;
             f = ex2(top - base);
             top = m1;
             d = -base;
           };
+          const float2 t = warp_max(s[0][nt][0]), old = m[nt];
+          float2 fall, down;
           rebase(m[nt].x, t.x, fall.x, down.x);
           rebase(m[nt].y, t.y, fall.y, down.y);
           l[nt] = mul2(l[nt], fall);
-          if constexpr (FMT == CF_E4M3) {
-            rebase(vm[nt].x, tv.x, fall.x, vdown.x);
-            rebase(vm[nt].y, tv.y, fall.y, vdown.y);
-          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float2 x = fma2(s[mt][nt][e], qs[nt], down);
-              const float2 pr = make_float2(ex2(x.x), ex2(x.y));
-              l[nt] = add2(l[nt], pr);
-              // (a masked token's logit is -infinity: weight 0)
+              const float2 x = add2(s[mt][nt][e], down), pr = make_float2(ex2(x.x), ex2(x.y));
+              l[nt] = add2(l[nt], pr);  // (a masked token's logit is -infinity: weight 0)
               if constexpr (FMT == CF_E4M3) {
-                const float2 y = add2(sv[mt][e], vdown);
-                const __half2 hh = __floats2half2_rn(ex2(y.x), ex2(y.y));
-                pf[mt][nt][e] = movm(*reinterpret_cast<const uint32_t*>(&hh));
+                s[mt][nt][e] = add2(x, make_float2(lvs[mt][e], lvs[mt][e]));
               } else {
                 const __nv_bfloat162 hh = __float22bfloat162_rn(pr);
                 pf[mt][nt][e] = movm(*reinterpret_cast<const uint32_t*>(&hh));
               }
             }
+          if constexpr (FMT == CF_E4M3) {
+            const float2 tv = warp_max(s[0][nt][0]);
+            float2 vdown;
+            vm[nt] = add2(vm[nt], add2(old, down));
+            rebase(vm[nt].x, tv.x - TOP, fall.x, vdown.x);
+            rebase(vm[nt].y, tv.y - TOP, fall.y, vdown.y);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 y = add2(s[mt][nt][e], vdown);
+                const __half2 hh = __floats2half2_rn(ex2(y.x), ex2(y.y));
+                pf[mt][nt][e] = movm(*reinterpret_cast<const uint32_t*>(&hh));
+              }
+          }
           if (__any_sync(0xFFFFFFFFu, fall.x != 1.f || fall.y != 1.f))
 #pragma unroll
             for (int c = 0; c < KSTEPS; ++c)
@@ -798,7 +803,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             sum.y = fmaf(ml[w].w, ex2(ml[w].z - base.y), sum.y);
           }
           if constexpr (FMT == CF_E4M3)
-            f[nt] = make_float2(ex2(vm[nt].x - base.x), ex2(vm[nt].y - base.y));
+            f[nt] = make_float2(ex2(vm[nt].x + (m[nt].x - base.x)), ex2(vm[nt].y + (m[nt].y - base.y)));
           else
             f[nt] = make_float2(ex2(m[nt].x - base.x), ex2(m[nt].y - base.y));
           if (whole) {  // (a sum of 0: nothing was attended to, the sums are 0 too)
