@@ -22,7 +22,6 @@ _CSRC = os.path.join(_HERE, "csrc")
 _HEADER = os.path.join(_ROOT, "include", "k3moe.h")
 _ATTN = os.path.join(_CSRC, "attn")  # the attention operators (attn.py)
 _ATTN_HEADER = os.path.join(_ROOT, "include", "k3attn.h")
-_ATTN_BINDING = os.path.join(_BUILD, "k3attn_binding.so")  # attn.py's native side
 _lock = threading.Lock()
 _lib = None
 
@@ -47,11 +46,15 @@ def _sources():
             if f.endswith((".cu", ".cuh"))] + [_HEADER, _ATTN_HEADER]
 
 
+def _stale(out: str, sources) -> bool:
+    return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(f) for f in sources)
+
+
 def _compile(cmd, out: str, sources, force: bool, verbose: bool) -> None:
     """Run cmd (which writes to its last argument) unless `out` is newer than its sources."""
-    newest = max(os.path.getmtime(f) for f in sources)
-    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
+    if not force and not _stale(out, sources):
         return
+    os.makedirs(_BUILD, exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"
     r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
@@ -61,24 +64,58 @@ def _compile(cmd, out: str, sources, force: bool, verbose: bool) -> None:
     os.replace(tmp, out)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/ and csrc/attn/ into _build/libk3moe.so for sm_103a, and the native side of
-    attn.py (a host extension against torch's headers) into _build/k3attn_binding.so (in-tree)."""
+def _cuda() -> str:
+    return os.environ.get("CUDA_HOME", "/usr/local/cuda")
+
+
+def _nvcc() -> str:
+    return os.path.join(_cuda(), "bin", "nvcc")
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/ and csrc/attn/ into _build/libk3moe.so for sm_103a (in-tree; needs nvcc alone)."""
+    _compile([_nvcc(), *NVCC_FLAGS, "-t", "2", os.path.join(_CSRC, "k3moe_api.cu"),
+              os.path.join(_ATTN, "k3attn_api.cu")], _SO, _sources(), force, verbose)
+    return _SO
+
+
+def attn_binding_sources():
+    return [os.path.join(_ATTN, "k3attn_binding.cpp"), _HEADER, _ATTN_HEADER]
+
+
+def attn_binding_path() -> str:
+    """attn.py's native side for this Python and torch (it is compiled against both)."""
     import sysconfig
 
     import torch
-    os.makedirs(_BUILD, exist_ok=True)
-    cuda, tdir = os.environ.get("CUDA_HOME", "/usr/local/cuda"), os.path.dirname(torch.__file__)
-    binding = os.path.join(_ATTN, "k3attn_binding.cpp")
-    jobs = [([os.path.join(cuda, "bin", "nvcc"), *NVCC_FLAGS, "-t", "2", os.path.join(_CSRC, "k3moe_api.cu"),
-              os.path.join(_ATTN, "k3attn_api.cu")], _SO, _sources()),
-            (["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+    return os.path.join(_BUILD, f"k3attn_binding.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
+
+
+def build_attn_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile the native side of attn.py, a host extension against torch's headers (in-tree)."""
+    import sysconfig
+
+    import torch
+    tdir, out, sources = os.path.dirname(torch.__file__), attn_binding_path(), attn_binding_sources()
+    _compile(["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
               "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(tdir, "include"),
-              "-I" + os.path.join(cuda, "include"), binding, "-L" + os.path.join(tdir, "lib"),
-              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], _ATTN_BINDING, [binding, _HEADER, _ATTN_HEADER])]
+              "-I" + os.path.join(_cuda(), "include"), sources[0], "-L" + os.path.join(tdir, "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], out, sources, force, verbose)
+    return out
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """build_library, and where torch is installed build_attn_binding beside it; returns the
+    library's path.  A binding that does not compile raises once the library is built."""
+    jobs = [build_library]
+    try:
+        import torch  # noqa: F401
+        jobs.append(build_attn_binding)
+    except ImportError:
+        pass
     with cf.ThreadPoolExecutor(max_workers=2) as ex:
-        for f in [ex.submit(_compile, *job, force, verbose) for job in jobs]:
+        for f in [ex.submit(job, force, verbose) for job in jobs]:
             f.result()
     return _SO
 
@@ -98,12 +135,14 @@ class ExpertsC(ctypes.Structure):
 
 
 def lib():
-    """The loaded C library (built on first use if absent)."""
+    """The loaded C library (built on first use if absent, or older than its sources where there is
+    a compiler)."""
     global _lib
     with _lock:
         if _lib is None:
-            so = _SO if os.path.exists(_SO) else build()
-            L = ctypes.CDLL(so)
+            if not os.path.exists(_SO) or (_stale(_SO, _sources()) and os.path.exists(_nvcc())):
+                build_library()
+            L = ctypes.CDLL(_SO)
             p, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
             D = ctypes.POINTER(Dims)
             X = ctypes.POINTER(ExpertsC)

@@ -20,7 +20,7 @@ import ctypes
 
 import torch
 
-from . import _ATTN_BINDING, _check, _stream, lib
+from . import _check, _stream, lib
 from . import device_status as _device_status
 
 BF16, E4M3 = 0, 1  # K3ATTN_BF16, K3ATTN_E4M3
@@ -73,7 +73,9 @@ def _funcs():
             "k3attn_decode": ([D, i32, p, i64, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
-            f = getattr(L, name)
+            f = getattr(L, name, None)
+            if f is None:
+                raise RuntimeError(f"libk3moe.so has no {name}: it is older than this package, build() it")
             f.argtypes = args
             f.restype = res
         _fns = L
@@ -86,12 +88,13 @@ def _load():
     if _native is None:
         import importlib.util
         import os
+        import shutil
 
-        from . import build
-        L = _funcs()
-        if not os.path.exists(_ATTN_BINDING):
-            build()
-        spec = importlib.util.spec_from_file_location("k3attn_binding", _ATTN_BINDING)
+        from . import _stale, attn_binding_path, attn_binding_sources, build_attn_binding
+        L, path = _funcs(), attn_binding_path()
+        if not os.path.exists(path) or (_stale(path, attn_binding_sources()) and shutil.which("g++")):
+            build_attn_binding()
+        spec = importlib.util.spec_from_file_location("k3attn_binding", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.bind(*(ctypes.cast(getattr(L, "k3attn_" + n), ctypes.c_void_p).value

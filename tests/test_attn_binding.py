@@ -2,10 +2,13 @@
 tensors it refuses, and how its parts are built."""
 import copy
 import ctypes
+import os
 import pickle
+import sys
 
 import pytest
 
+import mxfp4_routed_expert_latentmoe_gb300 as k3
 from mxfp4_routed_expert_latentmoe_gb300 import attn
 
 torch = pytest.importorskip("torch")
@@ -114,3 +117,68 @@ def test_the_workspace_is_readied_and_read_on_its_own_device(monkeypatch):
     attn.workspace_init(Ws())
     assert attn.device_status(Ws()) == 0
     assert seen == [("k3attn_workspace_init", 1), ("status", 1)] and current == [0]
+
+
+# ------------------------------------------------------------------------------ the build
+@pytest.fixture
+def compiled(monkeypatch):
+    """The outputs that a build compiles, by their names (nothing is run)."""
+    seen = []
+    monkeypatch.setattr(k3, "_compile", lambda cmd, out, *_: seen.append(os.path.basename(out)))
+    return seen
+
+
+def test_the_library_is_built_without_torch(compiled, monkeypatch):
+    assert k3.build() == k3._SO
+    assert sorted(compiled) == sorted(["libk3moe.so", os.path.basename(k3.attn_binding_path())])
+    del compiled[:]
+    monkeypatch.setitem(sys.modules, "torch", None)  # (import torch raises)
+    assert k3.build() == k3._SO and compiled == ["libk3moe.so"]
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library_built(monkeypatch):
+    seen = []
+
+    def compile_(cmd, out, *_):
+        if "binding" in out:
+            raise RuntimeError("g++ failed: no Python.h")
+        seen.append(out)
+
+    monkeypatch.setattr(k3, "_compile", compile_)
+    with pytest.raises(RuntimeError, match="Python.h"):
+        k3.build()
+    assert seen == [k3._SO]
+
+
+def test_a_binding_belongs_to_one_torch_and_python(monkeypatch):
+    import sysconfig
+    paths = {k3.attn_binding_path()}
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    paths.add(k3.attn_binding_path())
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399")
+    paths.add(k3.attn_binding_path())
+    assert len(paths) == 3
+
+
+def test_a_library_older_than_its_sources_is_built_again(tmp_path, monkeypatch):
+    so, nvcc, compiled = tmp_path / "libk3moe.so", tmp_path / "nvcc", []
+    with open(k3.build_library(), "rb") as f:
+        so.write_bytes(f.read())
+    monkeypatch.setattr(k3, "_compile", lambda cmd, out, *_: compiled.append(os.path.basename(out)))
+    monkeypatch.setattr(k3, "_SO", str(so))
+    monkeypatch.setattr(k3, "_nvcc", lambda: str(nvcc))
+    for age, compiler, built in ((10, True, []), (-10, True, ["libk3moe.so"]), (-10, False, [])):
+        monkeypatch.setattr(k3, "_lib", None)
+        newest = max(os.path.getmtime(f) for f in k3._sources())
+        os.utime(so, (newest + age, newest + age))
+        nvcc.write_text("") if compiler else nvcc.unlink()
+        k3.lib()
+        assert compiled == built, (age, compiler)
+        del compiled[:]
+
+
+def test_a_library_without_the_operators_says_so(monkeypatch):
+    monkeypatch.setattr(attn, "_fns", None)
+    monkeypatch.setattr(attn, "lib", lambda: object())
+    with pytest.raises(RuntimeError, match="older than this package"):
+        attn.workspace_bytes(_dims())
