@@ -151,12 +151,6 @@ K3_DEVI uint32_t movm(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
-// two E4M3 codes (the low 16 bits) -> two fp16
-K3_DEVI uint32_t e4m3x2_f16x2(uint32_t w) {
-  uint32_t y;
-  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(y) : "r"(w));
-  return y;
-}
 // four E4M3 codes -> two words of two fp16
 K3_DEVI void e4m3x4_f16x4(uint32_t w, uint32_t& a, uint32_t& b) {
   asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
