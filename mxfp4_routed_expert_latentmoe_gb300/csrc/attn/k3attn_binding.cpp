@@ -113,11 +113,13 @@ Work workspace(PyObject* o, Device& dev) {
   throw Refused{};
 }
 
-// The tensors' device made current, and the call's stream there.
+// The tensors' device made current (where it is not: looking costs less than a guard's two changes),
+// and the call's stream there.
 struct Stream {
-  c10::cuda::CUDAGuard guard;
+  c10::cuda::OptionalCUDAGuard guard;
   void* handle;
-  Stream(PyObject* stream, const Device& dev) : guard((c10::DeviceIndex)dev.index) {
+  Stream(PyObject* stream, const Device& dev) {
+    if (c10::cuda::current_device() != dev.index) guard.set_index((c10::DeviceIndex)dev.index);
     if (stream == Py_None) {
       handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
     } else {
