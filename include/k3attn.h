@@ -108,8 +108,10 @@ k3moe_status k3attn_workspace_init(void* ws, size_t ws_bytes, void* stream);
  *   positions [T] int32;  inv_freq [R / 2] f64 (NULL when R = 0)
  *   q_w, k_w [D] f32 norm weights
  *   q_out [T, Hq, D], k_out [T, Hkv, D] bf16; either may be its input where that is dense
- * Everything is held in fp32 (angles in fp64, reduced to a turn) and rounded once.  T = 0 is
- * a no-op. */
+ * Everything is held in fp32 (angles in fp64, reduced to a turn) and rounded once.  A row whose
+ * sum of squares passes fp32's range (elements of about 1e18 and more) therefore comes out as
+ * zeros, and with rms_eps = 0 one whose sum vanishes there as infinities or NaN.  T = 0 is a
+ * no-op. */
 k3moe_status k3attn_qk_norm_rope(const k3attn_dims* dims, int32_t T, const uint16_t* q, int64_t q_stride,
                                  const uint16_t* k, int64_t k_stride, const int32_t* positions,
                                  const double* inv_freq, const float* q_w, const float* k_w, uint16_t* q_out,
@@ -147,7 +149,11 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
  * (a captured call replays with new ones).  With more than 8 query heads a key head the longest
  * length that table_width and window allow decides between two ways to group the heads: a table
  * much wider than the sequences is right, and slower for few short ones.  The result does not
- * depend on the order in which the parts finish. */
+ * depend on the order in which the parts finish.
+ * Logits, softmax statistics and sums are held in fp32, powers of two to 2^-22.  A token's weight
+ * enters the sum of values rounded to the type of its product, bf16 for a K3ATTN_BF16 cache (off
+ * by 2^-8 of itself at most), fp16 for K3ATTN_E4M3 (2^-11, or 2^-40 of the largest); the sum of
+ * weights is of the unrounded ones.  The result is rounded to bf16 once. */
 k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q, int64_t q_stride,
                            const k3attn_cache* cache, const int32_t* page_table, int32_t table_width,
                            const int32_t* lens, uint16_t* out, float* lse, void* ws, size_t ws_bytes,

@@ -10,13 +10,13 @@
 // team's other warps only at the end of a sequence's part.
 //
 // What bounds it (GB300, copy rate 6789 GB/s).  Up to 8 query heads a key head, HBM: 2 x 262143
-// tokens, 8 E4M3 key heads of 128: 123 us, 92% of the copy rate; 64 sequences of up to 8192
-// tokens, bf16: 166 us, 88% (the copies alone reach 95%; the rest is the join at the 3 or 4
+// tokens, 8 E4M3 key heads of 128: 126 us, 90% of the copy rate; 64 sequences of up to 8192
+// tokens, bf16: 168 us, 88% (the copies alone reach 95%; the rest is the join at the 3 or 4
 // sequence ends of a block).  Up to 16 query heads: twice the matrix instructions and weights a
 // tile with the registers of 8 warps an SM used up, so that a warp's own instruction latency
-// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 63 us, 44%.  Few
+// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 64 us, 43%.  Few
 // short sequences: the chain of dependent reads (lengths, page table, rows, joined records),
-// 4.6 us for one token, 7.9 us for one sequence of 347.
+// 4.7 us for one token, 7.9 us for one sequence of 347.
 // mma.sync rather than tcgen05: the products are 2 G flops a cached byte (under 100 TFLOP/s at
 // the copy rate with 8 heads), E4M3 rows have to pass through registers on their way to fp16
 // anyway, and the softmax stays in the registers that the products leave it in.
@@ -24,6 +24,15 @@
 // E4M3 rows become fp16 operands exactly; a key's scale multiplies its logit, a value's scale
 // goes into its weight's exponent, with a maximum of its own, so that weights of values of any
 // size keep fp16's full precision.  bf16 rows are multiplied as they are.
+//
+// Logits, maxima and sums are fp32.  Rounded to fewer bits: a weight to the type of the rows that it
+// multiplies, as both operands of a product have one type (bf16, half a step 2^-8 of the weight; fp16,
+// 2^-11, and 2^-40 of the largest): a second product with what the rounding left would double the
+// second half of the matrix work, and the result is rounded to bf16 anyway (64 sequences up to 8192,
+// bf16: results off by 1.75e-3 in the mean square, 1.65e-3 with fp32 weights; E4M3 1.65e-3 both ways;
+// the sum of weights is of the unrounded ones).  A query for E4M3 rows to fp16 after a power of two: exact but for elements below 2^-31 of
+// its row's largest.  ex2.approx and lg2.approx (2^-22) stand in for exp2f and log2f in weights and
+// scales: one instruction each, with an error far below a weight's rounding.
 //
 // The work is cut into units (W tiles of one (sequence, key head, head group), one for each of
 // the W warps of a team), and the units, in a line, are dealt out evenly to all teams, whatever
@@ -71,9 +80,9 @@ struct DecCfg {
   static constexpr int ES = FMT == CF_E4M3 ? 1 : 2;
   static constexpr int ROW = DP * ES;  // bytes of a row in shared memory
   // 32 tokens a tile where eight warps' rings hold two of them, else 16: a tile's fixed work
-  // counts for more than the ring's depth (E4M3, D 192, 12 KB a tile: 201 windowed sequences 63 us,
-  // 69 at 16 tokens and a ring of 4; 16 x 20000 tokens 56, 61); and eight warps for the same
-  // reason (bf16, D 192: 16 x 10000 tokens 48 us, 55 with four warps and a ring of 4)
+  // counts for more than the ring's depth (E4M3, D 192, 12 KB a tile: 201 windowed sequences 64 us,
+  // 70 at 16 tokens and a ring of 4; 16 x 20000 tokens 56, 62); and eight warps for the same
+  // reason (bf16, D 192: 16 x 10000 tokens 49 us, 55 with four warps and a ring of 4)
   static constexpr int MT = 2 * ROW * 32 <= 12288 ? 2 : 1;
   static constexpr int TW = 16 * MT, TLOG = 3 + MT;
   static constexpr int KV = 2 * TW * ROW;
@@ -211,12 +220,12 @@ K3_HD int32_t seq_len(const DecodeParams& p, int b, bool& bad) {
 }
 
 // Units that a sequence's start counts as (its queries, its join): for teams of 4 and 8 warps two
-// (64 sequences up to 4000 tokens, 12 query heads a key head, E4M3: 40.7 us, 42.7 at one), for
-// smaller ones one (200 sequences up to 100 tokens: 14.7 us, 17.6 at two)
+// (64 sequences up to 4000 tokens, 12 query heads a key head, E4M3: 42.0 us, 43.7 at one), for
+// smaller ones one (200 sequences up to 100 tokens: 14.9 us, 17.7 at two)
 K3_HD int dec_start(int wlog) { return wlog >= 2 ? 2 : 1; }
 
 // Tiles of a sequence that is never cut: joining its records would take longer than they do (200
-// sequences up to 100 tokens, D 128, E4M3: 14.7 us, 17.5 if they are cut)
+// sequences up to 100 tokens, D 128, E4M3: 14.9 us, 17.7 if they are cut)
 constexpr int DEC_WHOLE = 4;
 
 // A place in the order of the units: sequence b, key head kvh and group grp of its query heads,
@@ -365,8 +374,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       wlog = i;
   // teams of half a block, where there are sequences enough for all (HR a sequence) with work for
   // more than a moment, and their ends are frequent (at most 24 units of a block each): while one
-  // team joins, the other streams.  201 windowed sequences, D 192: 63 us, 76 with whole blocks;
-  // 128 up to 2000, D 64: 49.5, 53.9; but 64 up to 8192 (64 units each): 169.7, 166.3.
+  // team joins, the other streams.  201 windowed sequences, D 192: 64 us, 76 with whole blocks;
+  // 128 up to 2000, D 64: 50, 54; but 64 up to 8192 (64 units each) 170, 167.
   const int64_t parts_all = (int64_t)p.B * HR, warps_all = (int64_t)gridDim.x * WARPS;
   if (wlog == 3 && 10 * parts_all >= 8 * (int64_t)gridDim.x && sums[0] * HR >= 4 * warps_all &&
       sums[3] * HR <= 24 * 8 * parts_all)
@@ -519,9 +528,9 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     uint32_t qf[KSTEPS][NT][2];
     // a part's queries as they are, bf16 (step 4 j + i of an E4M3 contraction holds dims
     // 64 j + 16 (lane % 4) + 4 i .. + 3).  bf16: loaded while the part before is joined (128
-    // sequences up to 2000 tokens, D 64: 49.5 us, 52.5 without; 32 x 5000, 5 heads of 96: 48, 51);
+    // sequences up to 2000 tokens, D 64: 50.2 us, 52.8 without; 32 x 5000, 5 heads of 96: 48, 51);
     // E4M3, and 16 bf16 heads of 256 dims: at the part's start, as the registers' longer life costs
-    // the inner loop more (2 x 262143 tokens, E4M3: 123 us, 138 early; 16 x 8000, D 256: 49.6, 52.1)
+    // the inner loop more (2 x 262143 tokens, E4M3: 125 us, 141 early; 16 x 8000, D 256: 49.5, 52.3)
     constexpr bool EARLY = FMT == CF_BF16 && KSTEPS * NT < 32;
     auto load_queries = [&](const DecAt& a) {
 #pragma unroll
@@ -892,8 +901,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
         if (tthread == 0) p.arrived[x.c0] = 0;
         // SIDE quads of dims a thread and some records at a time, whose loads are in flight
         // together: 8 / SIDE of few records, 32 / SIDE of more than 16 (1 x 64000 tokens, 8 heads,
-        // D 128, bf16 18.6 us, 22.0 at 8; E4M3 18.4, 19.6; but 8 x 1000 tokens 11.3, 10.5 at 8).
-        // 16 heads keep to 8: the registers cost them more (201 windowed sequences 64.6 us, 63.2)
+        // D 128, bf16 18.7 us, 21.9 at 8; E4M3 18.5, 19.8; but 8 x 1000 tokens 11.2, 10.6 at 8).
+        // 16 heads keep to 8: the registers cost them more (201 windowed sequences 64.8 us, 63.5)
         constexpr int QUADS = HEADS * DP / 4 / THREADS, SIDE = QUADS >= 4 ? 4 : QUADS >= 2 ? 2 : 1;
         for (int i0 = tthread; i0 < x.heads * (DP / 4); i0 += SIDE * tthreads) {
           float top[SIDE], sum[SIDE], o[SIDE][4];

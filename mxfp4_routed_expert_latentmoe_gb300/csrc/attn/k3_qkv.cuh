@@ -2,9 +2,12 @@
 // the paged cache: written (bf16, or E4M3 codes with a row scale) and read back.
 //
 // All of it moves each byte once; HBM is the floor (GB300, copy rate 6789 GB/s).  Measured: read
-// of 100003 tokens of 8 E4M3 heads of 128 at 98% of the copy rate, import of 65536 at 84%
+// of 100003 tokens of 8 E4M3 heads of 128 at 98% of the copy rate, import of 65536 at 83%
 // (issue slots: the quantisation), norms of 16381 tokens of 72 heads at 79% and the append of
-// 8192 tokens at 68% (issue slots, and warps waiting for their token's angles).
+// 8192 tokens at 68% (warps waiting at the barrier for their token's angles, the largest stall; then
+// issue slots, 66 and 61% used; fp64 units 9 and 8%).  Few heads a token are bound by the fp64 units
+// that form the angles, twice a token in an append: 65536 tokens of 4 query heads and 1 key head of
+// 128 take 118 us into an E4M3 cache (23%; fp64 units 68% busy), norms alone 63 us (39%).
 //
 // A row (a head of a token) is taken by 8, 16 or 32 lanes, eight elements a lane, and a thread
 // has the loads of up to QKV_ROWS rows in flight before it waits for any.
@@ -79,7 +82,7 @@ constexpr int QKV_THREADS = 512;  // most threads of a block
 constexpr int QKV_ROWS = 4;       // rows of a thread in flight
 constexpr int QKV_TOKENS = 8;     // most tokens of a block of the norms
 // Registers of the norm kernel: warps in flight count for more than the few spilled words
-// (16381 tokens of 72 heads of 128: 111 us at 56 registers, 121 at 64, 114 at 52; the append of
+// (16381 tokens of 72 heads of 128: 112 us at 56 registers, 121 at 64, 114 at 52; the append of
 // 8192 tokens to an E4M3 cache: 69 us at 64, 75 at 56, 78 at 72).  One row a thread: all it asks.
 constexpr int qkv_registers(int fmt, int rows) { return rows == 1 ? 128 : (fmt == CF_NONE ? 56 : 64); }
 constexpr float E4M3_MAX = 448.0f;
@@ -430,7 +433,7 @@ __global__ void __maxnreg__(qkv_registers(FMT, ROWS)) k3_norm_kernel(const QkvPa
 // Rows of the cache written from dense k, v (WRITE) or read back: an item is a head of a token,
 // its key and its value, LPR lanes an item and ITEMS items a thread.  32 registers, so that an
 // SM holds all its warps: the read of 100003 tokens of 8 E4M3 heads of 128 takes 93 us (98% of
-// the copy rate; 100 us without the bound), the import of 65536 tokens 71 us (84%, against 85;
+// the copy rate; 100 us without the bound), the import of 65536 tokens 72 us (83%, against 85;
 // by then bound by the instructions of the quantisation).
 template <int LPR, int FMT, bool WRITE, int ITEMS>
 __global__ void __launch_bounds__(256, ITEMS > 1 ? 8 : 1) k3_rows_kernel(const QkvParams p) {

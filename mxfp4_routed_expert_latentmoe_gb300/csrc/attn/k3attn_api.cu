@@ -214,7 +214,7 @@ static_assert(kRecords % 16 == 0, "the records are written 16 bytes at a time");
 int dec_dp(const k3attn_dims& d) { return (d.head_dim + 63) / 64 * 64; }
 int dec_nt(const k3attn_dims& d) { return d.n_heads / d.n_kv_heads <= 8 ? 1 : 2; }
 // E4M3 heads past 192 dims: 8 query heads at a time, as 16 do not fit the registers (16 x 20000
-// tokens of 2 key heads with 16 queries each, D 256: 63 us, 84 at 16 a time; the second pass
+// tokens of 2 key heads with 16 queries each, D 256: 65 us, 84 at 16 a time; the second pass
 // over the rows finds most of them in L2.  bf16, which fits but for a few words: 114, 95 us)
 int dec_nt_of(const k3attn_dims& d, int format) {
   return format == K3ATTN_E4M3 && d.head_dim > 192 ? 1 : dec_nt(d);
@@ -224,15 +224,15 @@ int dec_nt_of(const k3attn_dims& d, int format) {
 // the tiles, but each instance's start and joins cost less than half, and a sequence has twice the
 // teams.  Lengths are on the device, so the rule takes the longest that table and window allow:
 // - a unit a block at most: 7 sequences up to 200 tokens, 16 heads a key head, D 128: bf16 8.1 us,
-//   9.5 at 16 a time, E4M3 6.4, 7.8; 100 up to 200, above it: 12.0, 8.9
+//   9.5 at 16 a time, E4M3 6.4, 7.9; 100 up to 200, above it: 12.4, 10.8, E4M3 12.1, 9.2
 // - parts for a fifth of the blocks at most, cut between many teams, up to 16 units a block: 4 up
-//   to 16000, D 128, bf16: 14.3 us, 20.2; 8 up to 8000, E4M3: 12.0, 15.6; but 18 up to 2000, 2 key
-//   heads: 17.0, 15.9
+//   to 16000, D 128, bf16: 13.6 us, 20.0; 8 up to 8000, E4M3: 12.0, 15.3; but 18 up to 2000, 2 key
+//   heads, bf16: 17.2, 15.8
 // - E4M3, with no more parts than blocks, up to 4 units a block: 30 up to 800, 2 key heads, D 192:
-//   15.4 us, 17.0, D 128: 12.3, 12.5; 30 up to 1600: 21.0, 20.6, D 128: 15.9, 15.2 (bf16 30 up to 800:
-//   13.1, 12.5)
+//   15.4 us, 16.6, D 128: 12.4, 12.7; 30 up to 1600: 21.1, 20.3, D 128: 16.2, 15.4 (bf16 30 up to 800:
+//   13.2, 12.5)
 // - bf16 heads past 192 dims, whose 16 spill and are joined in two passes, up to 32 units a block: 1
-//   up to 3000: 15.6 us, 35.6; 64 up to 1000: 33.3, 37.7; 200 up to 1000 (42): 47.0, 46.5
+//   up to 3000: 13.1 us, 33.3; 64 up to 1000: 32.7, 38.7; 200 up to 1000 (42): 45.8, 46.3
 template <int FMT, int DP>
 bool dec_narrow(const DecodeParams& p, int grid) {
   using C = DecCfg<FMT, DP, 1>;
