@@ -42,12 +42,14 @@ class K3MoEError(RuntimeError):
 
 
 def _sources():
-    return [os.path.join(d, f) for d in (_CSRC, _ATTN) for f in sorted(os.listdir(d))
+    return [os.path.join(d, f) for d in (_CSRC, _ATTN) if os.path.isdir(d) for f in sorted(os.listdir(d))
             if f.endswith((".cu", ".cuh"))] + [_HEADER, _ATTN_HEADER]
 
 
 def _stale(out: str, sources) -> bool:
-    return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(f) for f in sources)
+    """Whether `out` is absent, or older than one of its sources (as far as they are there)."""
+    return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out)
+                                          for f in sources if os.path.exists(f))
 
 
 def _compile(cmd, out: str, sources, force: bool, verbose: bool) -> None:

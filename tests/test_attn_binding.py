@@ -182,3 +182,13 @@ def test_a_library_without_the_operators_says_so(monkeypatch):
     monkeypatch.setattr(attn, "lib", lambda: object())
     with pytest.raises(RuntimeError, match="older than this package"):
         attn.workspace_bytes(_dims())
+
+
+def test_a_library_without_its_sources_is_loaded_as_it_is(tmp_path, monkeypatch):
+    k3.build_library()
+    for name in ("_CSRC", "_ATTN", "_HEADER", "_ATTN_HEADER"):
+        monkeypatch.setattr(k3, name, str(tmp_path / "not there"))
+    monkeypatch.setattr(k3, "_compile", lambda *a: pytest.fail("nothing can be built"))
+    monkeypatch.setattr(k3, "_lib", None)
+    assert k3.lib().k3moe_abi_version() > 0
+    assert not k3._stale(k3._SO, k3._sources())
