@@ -1,7 +1,7 @@
 /*
  * k3attn.h -- C ABI of the attention operators that stand before the routed-expert block
  * of a decoder layer when it serves tokens: norms of queries and keys for each head with
- * the position rotation, a paged key-value cache (16 bits, or quantised to 8 as it is
+ * the position rotation, a paged key-value cache (16 bits, or quantised to 8 or 4 as it is
  * written), and the attention of one new token over its pages.
  *
  * With D = head_dim, R = rot_dim, per token at position p and per head row x in R^D:
@@ -13,12 +13,20 @@
  *         pair i: elements i and i + R/2, or with rot_interleaved 2i and 2i + 1
  *
  * The cache holds, for each token and each of the Hkv key heads, a row of D values for K
- * and one for V, in one of two formats:
+ * and one for V, in one of three formats:
  *   K3ATTN_BF16  the row rounded to bf16
  *   K3ATTN_E4M3  D codes and one f32 scale:  s = max(amax / 448, 2^-100), amax = max |row|;
  *                code = e4m3(value * (1 / s)), rounded to nearest even and saturated at 448;
  *                the value read back is code * s.  A row with an infinity or a NaN gets a
  *                NaN scale and NaN codes: all of it reads back as NaN.
+ *   K3ATTN_MXFP4 D / 2 bytes of E2M1 codes, two to a byte with the even element low (as in the
+ *                expert weights), and for each 32 elements an E8M0 byte b, scale s = 2^(b - 127):
+ *                the smallest power of two, at least 2^-100, with amax <= 7 s, amax of the 32 (a
+ *                value between 6 s and 7 s becomes 6 s, no further off than the rounding below
+ *                it is; with amax <= 6 s rows of a normal distribution would be off by 0.116 of
+ *                their size, 0.112 so).  code = e2m1(value / s), rounded to nearest even; the value
+ *                read back is code * s.  32 elements with an infinity or a NaN among them get
+ *                b = 255 and read back as NaN.  head_dim is a multiple of 32
  * A token's place is its slot: page * page_size + place in the page.
  *
  * Attention of one new token per sequence b over the cached tokens f .. len_b - 1,
@@ -53,6 +61,7 @@ extern "C" {
 
 #define K3ATTN_BF16 0
 #define K3ATTN_E4M3 1
+#define K3ATTN_MXFP4 4
 
 typedef struct {
   int32_t n_heads;         /* Hq: query heads, 1..1024 */
@@ -70,20 +79,27 @@ typedef struct {
  * token_stride D, head_stride page_size * D, page_stride Hkv * page_size * D; any other
  * order of pages, heads and tokens is described by its strides (rows must not overlap).
  * A row must start at a multiple of 16 bytes: strides are multiples of 16 elements
- * (K3ATTN_E4M3) or 8 (K3ATTN_BF16).  n_pages * page_size is below 2^31 (slots are int32);
+ * (K3ATTN_E4M3), 8 (K3ATTN_BF16) or 32 (K3ATTN_MXFP4, whose elements are half bytes: dense pages
+ * have token_stride D as well).  K3ATTN_MXFP4: k_scale and v_scale point to the E8M0 bytes; a
+ * row's D / 32 of them lie in K3ATTN_MXFP4_SCALES(D) bytes, whole words of 4, of which those past
+ * D / 32 are neither written nor have a part in anything; their strides are in bytes, multiples of 4,
+ * at least a row.  n_pages * page_size is below 2^31 (slots are int32);
  * offsets in the cache may pass 32 bits. */
 typedef struct {
   void* k;
   void* v;
-  float* k_scale; /* K3ATTN_E4M3 only; else NULL */
+  float* k_scale; /* K3ATTN_E4M3; K3ATTN_MXFP4: uint8_t*, cast; else NULL */
   float* v_scale;
-  int32_t format; /* K3ATTN_BF16, K3ATTN_E4M3 */
+  int32_t format; /* K3ATTN_BF16, K3ATTN_E4M3, K3ATTN_MXFP4 */
   int32_t n_pages;
   int32_t page_size; /* tokens in a page, any positive number */
   int32_t reserved;  /* 0 */
   int64_t page_stride, head_stride, token_stride;
   int64_t scale_page_stride, scale_head_stride, scale_token_stride;
 } k3attn_cache;
+
+/* bytes that the scales of a K3ATTN_MXFP4 row of D elements take */
+#define K3ATTN_MXFP4_SCALES(D) (((D) + 127) / 128 * 4)
 
 /* Bits of the status word at the start of the workspace. */
 #define K3ATTN_DEV_BAD_SLOT 0x1u   /* a slot outside the cache (and not -1): a write was skipped, a
@@ -152,12 +168,21 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
  * depend on the order in which the parts finish.
  * Logits, softmax statistics and sums are held in fp32, powers of two to 2^-22.  A token's weight
  * enters the sum of values rounded to the type of its product, bf16 for a K3ATTN_BF16 cache (off
- * by 2^-8 of itself at most), fp16 for K3ATTN_E4M3 (2^-11, or 2^-40 of the largest); the sum of
- * weights is of the unrounded ones.  The result is rounded to bf16 once. */
+ * by 2^-8 of itself at most), fp16 for the others (2^-11, or 2^-40 of the largest); the sum of
+ * weights is of the unrounded ones.  K3ATTN_MXFP4: the 32 values of a row whose scale is 2^25 and
+ * more below the largest of the row's scales count as zeros.  The result is rounded to bf16 once. */
 k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q, int64_t q_stride,
                            const k3attn_cache* cache, const int32_t* page_table, int32_t table_width,
                            const int32_t* lens, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                            void* stream);
+
+/* k3attn_decode with the window's sequences also attending to their first n_sinks tokens: with a
+ * window, token t is attended to if t >= len_b - window or t < n_sinks (dims' window 0: to all, and
+ * n_sinks >= 0 changes nothing). */
+k3moe_status k3attn_decode_sinks(const k3attn_dims* dims, int32_t n_sinks, int32_t B, const uint16_t* q,
+                                 int64_t q_stride, const k3attn_cache* cache, const int32_t* page_table,
+                                 int32_t table_width, const int32_t* lens, uint16_t* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

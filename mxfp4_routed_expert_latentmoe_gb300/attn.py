@@ -1,6 +1,6 @@
 """The attention operators that stand before the routed-expert block when it serves tokens:
 norms of queries and keys per head with the position rotation, the paged key-value cache
-(bf16, or E4M3 with a scale per row), and the attention of one new token over its pages.
+(bf16, E4M3 with a scale per row, or MXFP4), and the attention of one new token over its pages.
 
 Thin binding over the C ABI declared in ``include/k3attn.h``, which has the formulas.  Every
 function checks its tensors (ValueError), which all have to be on one device, passes pointers and
@@ -23,7 +23,7 @@ import torch
 from . import _check, _stream, lib
 from . import device_status as _device_status
 
-BF16, E4M3 = 0, 1  # K3ATTN_BF16, K3ATTN_E4M3
+BF16, E4M3, MXFP4 = 0, 1, 4  # K3ATTN_BF16, K3ATTN_E4M3, K3ATTN_MXFP4
 MIN_WORKSPACE = 256  # K3ATTN_MIN_WORKSPACE
 DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_BAD_LENGTH = 0x1, 0x2, 0x4
 _fns = None
@@ -71,6 +71,7 @@ def _funcs():
             "k3attn_kv_append": ([D, i32, p, i64, p, i64, p, i64, p, p, p, p, p, C, p, p, p, sz, p], ctypes.c_int),
             "k3attn_kv_read": ([D, i32, p, C, p, p, p, sz, p], ctypes.c_int),
             "k3attn_decode": ([D, i32, p, i64, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
+            "k3attn_decode_sinks": ([D, i32, i32, p, i64, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
             f = getattr(L, name, None)
@@ -98,7 +99,7 @@ def _load():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.bind(*(ctypes.cast(getattr(L, "k3attn_" + n), ctypes.c_void_p).value
-                   for n in ("qk_norm_rope", "kv_write", "kv_append", "kv_read", "decode")))
+                   for n in ("qk_norm_rope", "kv_write", "kv_append", "kv_read", "decode_sinks")))
         _native = mod
     return _native
 
@@ -148,16 +149,28 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
     return theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
 
 
+def mxfp4_scales(head_dim: int) -> int:
+    """Bytes that the scales of an MXFP4 row take (K3ATTN_MXFP4_SCALES)."""
+    return (head_dim + 127) // 128 * 4
+
+
 class KVCache:
-    """A paged cache over the caller's tensors: k, v [n_pages, Hkv, page_size, D], bf16 or
-    float8_e4m3fn, with the same strides (any order of pages, heads and tokens; a row's D
-    values dense); for E4M3 k_scale, v_scale [n_pages, Hkv, page_size] f32."""
+    """A paged cache over the caller's tensors, k and v with the same strides (any order of pages,
+    heads and tokens; a row's values dense), k_scale and v_scale likewise:
+      bf16   k, v [n_pages, Hkv, page_size, D] bfloat16
+      E4M3   k, v likewise float8_e4m3fn; k_scale, v_scale [n_pages, Hkv, page_size] f32
+      MXFP4  k, v [n_pages, Hkv, page_size, D / 2] uint8, two codes to a byte; k_scale, v_scale
+             [n_pages, Hkv, page_size, mxfp4_scales(D)] uint8, E8M0, the first D / 32 of them used"""
 
     def __init__(self, d: Dims, k, v, k_scale=None, v_scale=None):
-        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-            raise ValueError("k: [n_pages, Hkv, page_size, D] of bfloat16 or float8_e4m3fn is needed")
-        fmt = E4M3 if k.dtype == torch.float8_e4m3fn else BF16
-        shape = (k.shape[0], d.n_kv_heads, k.shape[2], d.head_dim)
+        formats = {torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3, torch.uint8: MXFP4}
+        if k.dim() != 4 or k.dtype not in formats:
+            raise ValueError("k: [n_pages, Hkv, page_size, D] of bfloat16 or float8_e4m3fn, or [n_pages, Hkv, page_size, "
+                             "D / 2] of uint8, is needed")
+        fmt = formats[k.dtype]
+        if fmt == MXFP4 and d.head_dim % 32:
+            raise ValueError("an MXFP4 cache needs a head_dim that is a multiple of 32")
+        shape = (k.shape[0], d.n_kv_heads, k.shape[2], d.head_dim // (2 if fmt == MXFP4 else 1))
         for t, name in ((k, "k"), (v, "v")):
             if (t.dtype != k.dtype or t.shape != shape or not t.is_cuda or t.device != k.device or t.stride(3) != 1
                     or t.stride() != k.stride()):
@@ -165,30 +178,37 @@ class KVCache:
                                  f"strides of k and on its device, is needed, got {list(t.shape)} (strides {list(t.stride())}) of "
                                  f"{t.dtype} on {t.device}")
         n, page, ss = shape[0], shape[2], (0, 0, 0)
-        if fmt == E4M3:
+        if fmt != BF16:
+            wanted = shape[:3] + ((mxfp4_scales(d.head_dim),) if fmt == MXFP4 else ())
+            dtype = torch.uint8 if fmt == MXFP4 else torch.float32
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if (t is None or t.dtype != torch.float32 or t.shape != shape[:3] or t.device != k.device
-                        or t.stride() != k_scale.stride()):
-                    raise ValueError(f"{name}: a CUDA tensor {list(shape[:3])} of float32, with the strides of "
-                                     "k_scale and on the device of k, is needed for an E4M3 cache")
-            ss = k_scale.stride()
+                if (t is None or t.dtype != dtype or t.shape != wanted or t.device != k.device
+                        or t.stride() != k_scale.stride() or fmt == MXFP4 and t.stride(3) != 1):
+                    raise ValueError(f"{name}: a CUDA tensor {list(wanted)} of {dtype}, with the strides of "
+                                     f"k_scale and on the device of k, is needed for an {'MXFP4' if fmt == MXFP4 else 'E4M3'} cache")
+            ss = k_scale.stride()[:3]
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.page_size = n, page
-        self.c = CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt == E4M3 else None,
-                        v_scale.data_ptr() if fmt == E4M3 else None, fmt, n, page, 0, *k.stride()[:3], *ss)
+        strides = [x * (2 if fmt == MXFP4 else 1) for x in k.stride()[:3]]  # in elements
+        self.c = CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fmt != BF16 else None,
+                        v_scale.data_ptr() if fmt != BF16 else None, fmt, n, page, 0, *strides, *ss)
         self.addr = ctypes.addressof(self.c)
         self.rows = (k.device.index << 32) + d.n_kv_heads * 65536 + d.head_dim  # what a call compares with its own
 
     @classmethod
     def empty(cls, d: Dims, n_pages: int, page_size: int, fmt: str = "bf16", device="cuda"):
-        """A dense cache of zeros; fmt "bf16" or "e4m3"."""
-        if fmt not in ("bf16", "e4m3"):
-            raise ValueError("fmt is bf16 or e4m3")
+        """A dense cache of zeros; fmt "bf16", "e4m3" or "mxfp4"."""
+        if fmt not in ("bf16", "e4m3", "mxfp4"):
+            raise ValueError("fmt is bf16, e4m3 or mxfp4")
         shape = (n_pages, d.n_kv_heads, page_size, d.head_dim)
         if fmt == "bf16":
             return cls(d, *(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        if fmt == "mxfp4":
+            widths = [d.head_dim // 2] * 2 + [mxfp4_scales(d.head_dim)] * 2
+            k, v, ks, vs = (torch.zeros(*shape[:3], w, dtype=torch.uint8, device=device) for w in widths)
+            return cls(d, k, v, ks.fill_(127), vs.fill_(127))
         codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
         return cls(d, *codes, *(torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
 
@@ -232,11 +252,12 @@ def kv_read(d: Dims, slots, cache: KVCache, k_out, v_out, ws, stream=None):
         _check(code, "k3attn_kv_read")
 
 
-def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None):
-    """k3attn_decode: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
-    of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32.  With more
-    than 8 query heads a key head a table just wide enough is faster for few short sequences."""
+def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None, sinks=0):
+    """k3attn_decode_sinks: q [B, Hq, D] bf16, one new token per sequence, over the first lens[b] tokens
+    of the pages page_table[b] -> out [B, Hq, D] bf16 and, if given, lse [B, Hq] f32.  With d.window the
+    last d.window of them are attended to, and the first `sinks`.  With more than 8 query heads a key
+    head a table just wide enough is faster for few short sequences."""
     code = (_native or _load()).decode(d.addr, q, cache.addr, cache.rows, page_table, lens, out, lse, ws,
-                                       _handle(stream))
+                                       _handle(stream), sinks)
     if code:
         _check(code, "k3attn_decode")

@@ -55,7 +55,7 @@ namespace k3 {
 struct DecodeParams {
   const uint16_t* q;
   int64_t q_stride;
-  int32_t B, Hq, Hkv, G, D, window;
+  int32_t B, Hq, Hkv, G, D, window, sinks;
   int32_t groups;  // head groups of a key head: ceil(G / (8 NT))
   float scale;     // softmax_scale * log2(e): logits in powers of two
   CacheView c;
@@ -77,8 +77,7 @@ constexpr int DEC_MAX_TEAMS = DEC_MAX_BLOCKS * DEC_MAX_WARPS;
 // (192 KB of rows in all: two or more tiles a warp in flight, 128 KB an SM).
 template <int FMT, int DP, int NT>
 struct DecCfg {
-  static constexpr int ES = FMT == CF_E4M3 ? 1 : 2;
-  static constexpr int ROW = DP * ES;  // bytes of a row in shared memory
+  static constexpr int ROW = FMT == CF_MXFP4 ? DP / 2 : FMT == CF_E4M3 ? DP : 2 * DP;  // bytes of a row in shared memory
   // 32 tokens a tile where eight warps' rings hold two of them, else 16: a tile's fixed work
   // counts for more than the ring's depth (E4M3, D 192, 12 KB a tile: 201 windowed sequences 64 us,
   // 70 at 16 tokens and a ring of 4; 16 x 20000 tokens 56, 62); and eight warps for the same
@@ -87,12 +86,17 @@ struct DecCfg {
   static constexpr int TW = 16 * MT, TLOG = 3 + MT;
   static constexpr int KV = 2 * TW * ROW;
   static constexpr int WARPS = KV <= 12288 ? 8 : 4;
-  static constexpr int STAGES = 196608 / (WARPS * KV);
-  static constexpr int STAGE = KV + (FMT == CF_E4M3 ? 8 * TW : 0) + 16;  // rows, scales, mask
+  // (MXFP4: 6 at most, 160 KB an SM in flight at D 128)
+  static constexpr int STAGES = FMT == CF_MXFP4 && 196608 / (WARPS * KV) > 6 ? 6 : 196608 / (WARPS * KV);
+  static constexpr int SW = FMT == CF_MXFP4 ? (DP > 128 ? 8 : 4) : FMT == CF_E4M3 ? 4 : 0;  // bytes of a row's scales
+  static constexpr int STAGE = KV + 2 * SW * TW + 16;  // rows, scales, mask
   static constexpr int HEADS = 8 * NT;
   static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int ML = WARPS * HEADS * 2 * 4;
-  static constexpr int SMEM = RING + ML + 1024;
+  // MXFP4: what a warp makes of a tile's scales (ScalesAt)
+  static constexpr int NG = DP / 32;
+  static constexpr int PREP = FMT == CF_MXFP4 ? TW * (4 * NG + 2 * NG + 4) : 0;
+  static constexpr int SMEM = RING + ML + 1024 + WARPS * PREP;
   // n-tiles whose sums fit the stage of a tile that is read out (the join of a team's warps)
   static constexpr int PN = HEADS * DP * 4 <= KV ? NT : 1;
   static constexpr int REC = HEADS * (DP + 2);  // floats of a record: sums, and each head's maximum and sum of weights
@@ -174,7 +178,10 @@ K3_DEVI float lds_f32(uint32_t a) { return *reinterpret_cast<const float*>(__cvt
 // quarter warp reads 64 bytes of, lie in different banks.
 template <int FMT, int ROW>
 K3_DEVI uint32_t chunk_at(int r, int c) {
-  if constexpr (ROW % 128 == 0) {
+  if constexpr (FMT == CF_MXFP4) {
+    constexpr int SHIFT = ROW == 128 ? 0 : ROW == 64 ? 1 : 2, MASK = ROW == 128 ? 7 : ROW == 64 ? 3 : 1;
+    return r * ROW + ((c ^ ((r >> SHIFT) & MASK)) << 4);
+  } else if constexpr (ROW % 128 == 0) {
     if constexpr (FMT == CF_E4M3) {
       const int f = ((r & 1) << 2) | ((r >> 1) & 3);
       return r * ROW + ((c ^ f) << 4);
@@ -237,6 +244,7 @@ struct DecAt {
     bool bad;
     n = seq_len(p, b, bad);
     first = p.window > 0 && n > p.window ? n - p.window : 0;
+    first -= first < p.sinks ? first : p.sinks;  // the sinks stand in front of the window's tokens
     nu = (int32_t)(((uint32_t)(n - first) + (1u << ulog) - 1) >> ulog);
     return !bad;
   }
@@ -245,6 +253,10 @@ struct DecAt {
   template <int TW>
   K3_HD uint32_t token(int W, int tw, int row) const {
     return (uint32_t)first + ((uint32_t)u * W + tw) * TW + row;
+  }
+  // what token() stands for where it is one of the sinks: those come first of all
+  K3_HD uint32_t seen(const DecodeParams& p, uint32_t t) const {
+    return t - (uint32_t)first < (uint32_t)p.sinks ? t - (uint32_t)first : t;
   }
   // whether the unit is the team's whose range ends in front of `end`
   K3_HD bool in(int32_t end, int32_t whole, int start) const { return (nu <= whole ? x - u - start : x) < end; }
@@ -304,7 +316,52 @@ K3_DEVI float lse_of(float base, float sum) {
   return sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
 }
 
-// The largest weight of E4M3 values is 2^15 (fp16's largest number is 65504), so that weights down to
+// MXFP4: a tile's scales as the products take them, one token a lane.  At prep: the keys' scales, f32
+// [TW][NG]; the values' factors, f16 [TW / 2][NG][2], 2^(b - largest) with the largest b of the row's
+// groups (a group 2^25 and more below it counts as zeros: less than half of fp32's step of the row's
+// largest); f32 [TW], the largest as a power of two, for the weight's exponent.  255 gives NaN.
+K3_DEVI void sts32(uint32_t a, uint32_t v) { *reinterpret_cast<uint32_t*>(__cvta_shared_to_generic(a)) = v; }
+K3_DEVI void sts64(uint32_t a, uint32_t x, uint32_t y) { *reinterpret_cast<uint2*>(__cvta_shared_to_generic(a)) = make_uint2(x, y); }
+K3_DEVI void sts16(uint32_t a, uint32_t v) { *reinterpret_cast<uint16_t*>(__cvta_shared_to_generic(a)) = (uint16_t)v; }
+K3_DEVI uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <typename C>
+K3_DEVI void prepare_scales(uint32_t raw, uint32_t prep, int lane, int D) {
+  static_assert(C::TW == 32, "a token a lane");
+  constexpr int NG = C::NG, TW = C::TW;
+  const int groups = D / 32;
+  uint32_t kw[C::SW / 4], vw[C::SW / 4];
+#pragma unroll
+  for (int i = 0; i < C::SW / 4; ++i) {
+    kw[i] = lds32(raw + C::SW * lane + 4 * i);
+    vw[i] = lds32(raw + C::SW * TW + C::SW * lane + 4 * i);
+  }
+  int top = 0;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int b = vw[g / 4] >> (8 * (g % 4)) & 255;
+    if (g < groups && b != 255) top = max(top, b);
+  }
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int b = vw[g / 4] >> (8 * (g % 4)) & 255, below = top - b;
+    const uint32_t f = b == 255 ? 0x7E00u : below < 15 ? (uint32_t)(15 - below) << 10 : below < 25 ? 1u << (24 - below) : 0u;
+    sts16(prep + 4 * NG * TW + 4 * NG * (lane / 2) + 4 * g + 2 * (lane & 1), g < groups ? f : 0u);
+  }
+#pragma unroll
+  for (int g = 0; g < NG; g += 2) {
+    const uint32_t k0 = kw[g / 4] >> (8 * (g % 4)) & 255, k1 = kw[(g + 1) / 4] >> (8 * ((g + 1) % 4)) & 255;
+    sts64(prep + 4 * NG * lane + 4 * g, g < groups ? __float_as_uint(ue8m0_to_f32(k0)) : 0u,
+          g + 1 < groups ? __float_as_uint(ue8m0_to_f32(k1)) : 0u);
+  }
+  sts32(prep + 6 * NG * TW + 4 * lane, __float_as_uint((float)(top - 127)));
+  __syncwarp();
+}
+
+// The largest weight of E4M3 and MXFP4 values is 2^15 (fp16's largest number is 65504), so that weights down to
 // 2^-40 of it count: 2^31 tokens of less weight each are lost with less than 2^-9 of the result.
 constexpr float TOP = 15.f;
 
@@ -323,6 +380,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
   volatile int32_t* const s_last = s_b + DEC_MAX_WARPS;                                    // [teams]
   int64_t* const s_count = reinterpret_cast<int64_t*>(smem + C::RING + C::ML + 256);       // [WARPS][4]
   DecPart* const s_part = reinterpret_cast<DecPart*>(smem + C::RING + C::ML + 512);        // [teams][2]
+  const uint32_t prep = smem_u32(smem) + C::RING + C::ML + 1024 + warp * C::PREP;
   static_assert(2 * DEC_MAX_WARPS * sizeof(DecPart) <= 512 && DEC_MAX_WARPS * 32 <= 256, "shared layout");
 
   // dims past D: zero in every stage, and again wherever a join has written.  A warp clears its
@@ -448,15 +506,16 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     bool cut = false;          // there is a part that is not a whole sequence
 
     // a copy takes LR 16-byte chunks (128 or 64 bytes) of each of 32 / LR rows
-    constexpr int CPR = ROW / 16, LR = CPR % 8 == 0 ? 8 : 4, RPI = 32 / LR;
-    const int cpr = p.D * C::ES / 16;
+    constexpr int CPR = ROW / 16, LR = CPR % 8 == 0 ? 8 : CPR % 4 == 0 ? 4 : 2, RPI = 32 / LR;
+    const int cpr = FMT == CF_MXFP4 ? p.D / 32 : FMT == CF_E4M3 ? p.D / 16 : p.D / 8;
     // reads the page entries of the tile at `ahead` (if it is the team's) and moves on
     auto fetch = [&]() {
       DecRow r{0, 0, ahead.kvh, ahead.in(end, whole_units, start), false};
       if (r.tile) {
-        const uint32_t t = ahead.token<TW>(W, tw, lane & (TW - 1));
+        uint32_t t = ahead.token<TW>(W, tw, lane & (TW - 1));
         r.in = t < (uint32_t)ahead.n;
         if (r.in) {
+          t = ahead.seen(p, t);
           const uint32_t pg = p.c.by_page(t);
           r.entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
           r.in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
@@ -479,7 +538,25 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
         if (TW == 32 || lane < 16) cp_async4_or_zero(dst, p.c.ks + so, ok ? 4 : 0);
         if (TW == 32 || lane >= 16) cp_async4_or_zero(dst + 4 * TW, p.c.vs + so, ok ? 4 : 0);
       }
-      if (mask == 0xFFFFFFFFu && p.D == DP && __shfl_sync(0xFFFFFFFFu, x.in_page, 0) + TW <= p.c.page_size) {
+      if constexpr (FMT == CF_MXFP4) {
+        const int64_t so = ok ? x.entry * p.c.spage + x.kvh * p.c.shead + x.in_page * p.c.stok : 0;
+        const uint32_t dst = st + C::KV + C::SW * (lane & (TW - 1));
+#pragma unroll
+        for (int i = 0; i < C::SW; i += 4) {
+          const uint32_t n = ok && 32 * i < p.D ? 4 : 0;  // (a row's words: those that D has)
+          cp_async4_or_zero(dst + i, p.c.k_exps() + (n ? so + i : 0), n);
+          cp_async4_or_zero(dst + C::SW * TW + i, p.c.v_exps() + (n ? so + i : 0), n);
+        }
+      }
+      // the rows follow one another, the last one on the first one's page (sinks: the window's first
+      // token need not be next to the last of them)
+      auto in_line = [&]() {
+        const int32_t at0 = __shfl_sync(0xFFFFFFFFu, x.in_page, 0);
+        if (at0 + TW > p.c.page_size) return false;
+        return p.sinks == 0 || (__shfl_sync(0xFFFFFFFFu, x.in_page, TW - 1) == at0 + TW - 1 &&
+                                __shfl_sync(0xFFFFFFFFu, x.entry, TW - 1) == __shfl_sync(0xFFFFFFFFu, x.entry, 0));
+      };
+      if (mask == 0xFFFFFFFFu && p.D == DP && in_line()) {
         // all rows there, on one page: they lie a token's stride apart
         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + (lane / LR) * p.c.tok + 16 * (lane % LR);
         const int64_t step = RPI * p.c.tok;
@@ -527,7 +604,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
     float2 acc[KSTEPS][NT][2], m[NT], l[NT], vm[NT], qs[NT];  // pairs: of two heads
     uint32_t qf[KSTEPS][NT][2];
     // a part's queries as they are, bf16 (step 4 j + i of an E4M3 contraction holds dims
-    // 64 j + 16 (lane % 4) + 4 i .. + 3).  bf16: loaded while the part before is joined (128
+    // 64 j + 16 (lane % 4) + 4 i .. + 3, step 2 g + i of an MXFP4 one dims 32 g + 8 (lane % 4) + 4 i .. + 3).  bf16: loaded while the part before is joined (128
     // sequences up to 2000 tokens, D 64: 50.2 us, 52.8 without; 32 x 5000, 5 heads of 96: 48, 51);
     // E4M3, and 16 bf16 heads of 256 dims: at the part's start, as the registers' longer life costs
     // the inner loop more (2 x 262143 tokens, E4M3: 125 us, 141 early; 16 x 8000, D 256: 49.5, 52.3)
@@ -547,7 +624,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
               qf[c][nt][e] = on && d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
             }
           } else {
-            const int d = 64 * (c / 4) + 16 * (lane & 3) + 4 * (c & 3);
+            const int d = FMT == CF_MXFP4 ? 32 * (c / 2) + 8 * (lane & 3) + 4 * (c & 1)
+                                          : 64 * (c / 4) + 16 * (lane & 3) + 4 * (c & 3);
             const uint2 w = on && d < p.D ? ldg64(q + d) : make_uint2(0, 0);
             qf[c][nt][0] = w.x;
             qf[c][nt][1] = w.y;
@@ -576,7 +654,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           qs[nt] = make_float2(p.scale, p.scale);
-          if constexpr (FMT == CF_E4M3) {
+          if constexpr (FMT != CF_BF16) {
             // to fp16, scaled by the power of two that brings the row's largest into [2^14, 2^15)
             uint32_t mx = 0;
 #pragma unroll
@@ -613,6 +691,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
       const uint32_t st = ring + stage * C::STAGE;
       const uint32_t mask = lds32(st + C::STAGE - 16);
       if (mask != 0) {
+        if constexpr (FMT == CF_MXFP4) prepare_scales<C>(st + C::KV, prep, lane, p.D);
         // ---- logits: lane holds tokens lane / 4 and + 8 of each 16, heads 2 (lane % 4) and + 1
         float2 s[MT][NT][2];
 #pragma unroll
@@ -628,6 +707,37 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
               ldsm4(a, st + chunk_at<FMT, ROW>(16 * mt + (lane & 15), 2 * c + (lane >> 4)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma2_bf16(s[mt][nt], a, qf[c][nt]);
+            }
+          } else if constexpr (FMT == CF_MXFP4) {
+            // a group's two steps, then its sums times the group's scale of each of the lane's rows
+            float ks[2][C::NG];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int g = 0; g < C::NG; g += 2) {
+                const uint2 x = lds64(prep + C::NG * 4 * (16 * mt + 8 * e + lane / 4) + 4 * g);
+                ks[e][g] = __uint_as_float(x.x);
+                ks[e][g + 1] = __uint_as_float(x.y);
+              }
+#pragma unroll
+            for (int g = 0; g < C::NG; ++g) {
+              uint32_t w[2][4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                e2m1x8_to_f16x8(lds32(st + chunk_at<FMT, ROW>(16 * mt + 8 * e + lane / 4, g) + 4 * (lane & 3)), w[e]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float2 x[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t a[4] = {w[0][2 * i], w[1][2 * i], w[0][2 * i + 1], w[1][2 * i + 1]};
+                  mma2_f16(x, a, qf[2 * g + i][nt]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  s[mt][nt][e] = g == 0 ? mul2(x[e], make_float2(ks[e][0], ks[e][0]))
+                                        : fma2(x[e], make_float2(ks[e][g], ks[e][g]), s[mt][nt][e]);
+              }
             }
           } else {
 #pragma unroll
@@ -658,6 +768,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
           for (int e = 0; e < 2; ++e) {
             const int r = 16 * mt + lane / 4 + 8 * e;
             float ks = 1.f;
+            if constexpr (FMT == CF_MXFP4) lvs[mt][e] = lds_f32(prep + 6 * C::NG * TW + 4 * r);
             if constexpr (FMT == CF_E4M3) {
               ks = lds_f32(st + C::KV + 4 * r);
               lvs[mt][e] = lg2(lds_f32(st + C::KV + 4 * (TW + r)));
@@ -703,14 +814,14 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             for (int e = 0; e < 2; ++e) {
               const float2 x = add2(s[mt][nt][e], down), pr = make_float2(ex2(x.x), ex2(x.y));
               l[nt] = add2(l[nt], pr);  // (a masked token's logit is -infinity: weight 0)
-              if constexpr (FMT == CF_E4M3) {
+              if constexpr (FMT != CF_BF16) {
                 s[mt][nt][e] = add2(x, make_float2(lvs[mt][e], lvs[mt][e]));
               } else {
                 const __nv_bfloat162 hh = __float22bfloat162_rn(pr);
                 pf[mt][nt][e] = movm(*reinterpret_cast<const uint32_t*>(&hh));
               }
             }
-          if constexpr (FMT == CF_E4M3) {
+          if constexpr (FMT != CF_BF16) {
             const float2 tv = warp_max(s[0][nt][0]);
             float2 vdown;
             vm[nt] = add2(vm[nt], add2(old, down));
@@ -742,6 +853,38 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
               ldsm4t(a, vt + chunk_at<FMT, ROW>(16 * mt + (lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma2_bf16(acc[c][nt], a, pf[mt][nt]);
+            }
+          } else if constexpr (FMT == CF_MXFP4) {
+            uint32_t f[2][C::NG];  // the groups' factors of the lane's tokens, two at a time as pf has them
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int g = 0; g < C::NG; g += 2) {
+                const uint2 x = lds64(prep + 4 * C::NG * TW + 4 * C::NG * (8 * mt + 4 * e + (lane & 3)) + 4 * g);
+                f[e][g] = x.x;
+                f[e][g + 1] = x.y;
+              }
+#pragma unroll
+            for (int g = 0; g < C::NG; g += 2) {
+              // lane: four dims of group g (v[0], v[1]) and g + 1 of tokens 2 (lane % 4) and + 1, and + 8
+              uint32_t v[4];
+              ldsm4t(v, vt + chunk_at<FMT, ROW>(16 * mt + (lane & 15), g + (lane >> 4)));
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                // a byte of ev, od: a dim's codes of a token and the next one
+                const uint32_t x = __byte_perm(v[2 * i], v[2 * i + 1], 0x5410), y = __byte_perm(v[2 * i], v[2 * i + 1], 0x7632);
+                const uint32_t ev = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), od = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+                uint32_t a[4], b[4];
+                e2m1x8_to_f16x8(ev, a);
+                e2m1x8_to_f16x8(od, b);
+                const uint32_t a0[4] = {a[0], b[0], a[2], b[2]}, a1[4] = {a[1], b[1], a[3], b[3]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint32_t w[2] = {hmul2(pf[mt][nt][0], f[0][g + i]), hmul2(pf[mt][nt][1], f[1][g + i])};
+                  mma2_f16(acc[2 * (g + i)][nt], a0, w);
+                  mma2_f16(acc[2 * (g + i) + 1][nt], a1, w);
+                }
+              }
             }
           } else {
 #pragma unroll
@@ -805,7 +948,7 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
             sum.x = fmaf(ml[w].y, ex2(ml[w].x - base.x), sum.x);
             sum.y = fmaf(ml[w].w, ex2(ml[w].z - base.y), sum.y);
           }
-          if constexpr (FMT == CF_E4M3)
+          if constexpr (FMT != CF_BF16)
             f[nt] = make_float2(ex2(vm[nt].x + (m[nt].x - base.x)), ex2(vm[nt].y + (m[nt].y - base.y)));
           else
             f[nt] = make_float2(ex2(m[nt].x - base.x), ex2(m[nt].y - base.y));
@@ -841,7 +984,8 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
                 x[DP + d0] = a.y;
                 x[DP + d1] = b.y;
               } else {
-                const int d0 = (16 * c + 2 * (lane / 4)) ^ ((lane & 3) << 3);
+                const int d0 = (FMT == CF_MXFP4 ? 32 * (c / 2) + 4 * (lane / 4) + 2 * (c & 1) : 16 * c + 2 * (lane / 4)) ^
+                               ((lane & 3) << 3);
                 *reinterpret_cast<float2*>(x + d0) = make_float2(a.x, b.x);
                 *reinterpret_cast<float2*>(x + DP + d0) = make_float2(a.y, b.y);
               }

@@ -1,5 +1,5 @@
 // k3_qkv.cuh -- norms of queries and keys per head with the position rotation, and the rows of
-// the paged cache: written (bf16, or E4M3 codes with a row scale) and read back.
+// the paged cache: written (bf16, E4M3 codes with a row scale, or MXFP4) and read back.
 //
 // All of it moves each byte once; HBM is the floor (GB300, copy rate 6789 GB/s).  Measured: read
 // of 100003 tokens of 8 E4M3 heads of 128 at 98% of the copy rate, import of 65536 at 83%
@@ -20,7 +20,7 @@
 
 namespace k3 {
 
-enum { CF_NONE = -1, CF_BF16 = K3ATTN_BF16, CF_E4M3 = K3ATTN_E4M3 };
+enum { CF_NONE = -1, CF_BF16 = K3ATTN_BF16, CF_E4M3 = K3ATTN_E4M3, CF_MXFP4 = K3ATTN_MXFP4 };
 
 // two fp32 at once
 K3_DEVI float2 mul2(float2 a, float2 b) {
@@ -53,9 +53,12 @@ struct Divisor {
 };
 
 // the cache as the kernels address it: strides of the rows in bytes, of the scales in elements
+// (MXFP4: in bytes)
 struct CacheView {
   uint8_t *k, *v;
   float *ks, *vs;
+  K3_DEVI uint8_t* k_exps() const { return reinterpret_cast<uint8_t*>(ks); }
+  K3_DEVI uint8_t* v_exps() const { return reinterpret_cast<uint8_t*>(vs); }
   int64_t page, head, tok;
   int64_t spage, shead, stok;
   int32_t n_pages, page_size;
@@ -196,6 +199,63 @@ K3_DEVI uint2 codes_of(const float2 (&y)[4], float inv) {
   return e4m3x8(z);
 }
 
+// ---- MXFP4: the E8M0 byte of 32 elements from their largest magnitude (by its bits), the smallest
+// b with amax <= 7 * 2^(b - 127): amax's exponent, one more where its mantissa is above 7/4, less 2
+K3_DEVI uint32_t exp_of(uint32_t m) {
+  return m < 0x7F800000u ? max((int)((m + 0x1FFFFFu) >> 23) - 2, 27) : 255u;
+}
+// 2^(127 - b), for b in 27..253 (255, a group that reads as NaN whatever its codes are: any number)
+K3_DEVI float inverse_of(uint32_t b) { return __uint_as_float((254u - min(b, 253u)) << 23); }
+// four values times inv as E2M1 codes (rounded to nearest even, saturated), the first one lowest
+K3_DEVI uint32_t e2m1x4(float2 a, float2 b, float inv) {
+  a = mul2(a, make_float2(inv, inv));
+  b = mul2(b, make_float2(inv, inv));
+  uint32_t r;
+  asm("{\n.reg .b8 lo, hi;\ncvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n"
+      "mov.b32 %0, {lo, hi, 0, 0};\n}\n"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// a lane's eight neighbours of a row, four lanes to a group: their codes, the group's byte
+K3_DEVI uint32_t e2m1x8(const float2 (&y)[4], uint32_t b) {
+  const float inv = inverse_of(b);
+  return e2m1x4(y[0], y[1], inv) | e2m1x4(y[2], y[3], inv) << 16;
+}
+// eight E2M1 codes times 2^(b - 127), rounded to bf16
+K3_DEVI uint4 e2m1x8_bf16(uint32_t c, uint32_t b) {
+  uint32_t h[4];
+  e2m1x8_to_f16x8(c, h);
+  const float s = ue8m0_to_f32(b);
+  float2 x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h[k])), make_float2(s, s));
+  return pack8(x);
+}
+// The bytes of the groups that a lane's two pieces of four elements lie in (ga, gb: the groups), in
+// any layout of the pieces over the lanes of the row: each piece's largest goes through shared
+// memory (unit: the warp's, 64 words a row of up to 256 elements), where a group's eight lie together.
+template <int LPR>
+K3_DEVI void piece_exps(const float2 (&y)[4], int ea, int eb, bool on, uint32_t* unit, uint32_t& ba, uint32_t& bb) {
+  auto abs_bits = [](float v) { return __float_as_uint(v) & 0x7FFFFFFFu; };
+  uint32_t* const row = unit + (threadIdx.x % 32) / LPR * (2 * LPR);
+  if (on) {
+    row[ea / 4] = max(max(abs_bits(y[0].x), abs_bits(y[0].y)), max(abs_bits(y[1].x), abs_bits(y[1].y)));
+    row[eb / 4] = max(max(abs_bits(y[2].x), abs_bits(y[2].y)), max(abs_bits(y[3].x), abs_bits(y[3].y)));
+  }
+  __syncwarp();
+  auto largest = [&](int e) {
+    const uint4 a = *reinterpret_cast<const uint4*>(row + e / 32 * 8), b = *reinterpret_cast<const uint4*>(row + e / 32 * 8 + 4);
+    return max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w)));
+  };
+  ba = bb = 0;
+  if (on) {
+    ba = exp_of(largest(ea));
+    bb = ea / 32 == eb / 32 ? ba : exp_of(largest(eb));
+  }
+  __syncwarp();  // the next row's may be written
+}
+
 // What a lane multiplies its pieces of normed rows of one kind (queries or keys) of one token by:
 // y = x * co + z * si, z the other element of x's pair; without rotation co is the weight alone.
 struct Turn {
@@ -293,6 +353,7 @@ struct Pieces {
 template <int LPR, int FMT, int ROWS>
 __global__ void __maxnreg__(qkv_registers(FMT, ROWS)) k3_norm_kernel(const QkvParams p) {
   __shared__ __align__(16) float s_cos[QKV_TOKENS][128], s_sin[QKV_TOKENS][128];
+  __shared__ __align__(16) uint32_t s_unit[FMT == CF_MXFP4 ? QKV_THREADS / 32 : 1][64];  // piece_exps
   const int half = p.R / 2;
   const float over_d = 1.0f / (float)p.D;
   grid_dep_wait();
@@ -330,7 +391,7 @@ __global__ void __maxnreg__(qkv_registers(FMT, ROWS)) k3_norm_kernel(const QkvPa
       rotation(p.pos[t0 + g], p.inv_freq[j], s_cos[g][j], s_sin[g][j]);
     }
     const Place pl = place_of(p, slot, sub == 0 && li == 0);
-    const int64_t row0 = row_at(p, pl, 0), scale0 = FMT == CF_E4M3 ? scale_at(p, pl, 0) : 0;
+    const int64_t row0 = row_at(p, pl, 0), scale0 = FMT != CF_BF16 ? scale_at(p, pl, 0) : 0;
     __syncthreads();
     if (!mine) return;  // the whole warp
     Turn turn{};
@@ -358,6 +419,22 @@ __global__ void __maxnreg__(qkv_registers(FMT, ROWS)) k3_norm_kernel(const QkvPa
             *reinterpret_cast<uint2*>(p.c.k + row + 2 * pc.ea) = make_uint2(kb.x, kb.y);
             *reinterpret_cast<uint2*>(p.c.k + row + 2 * pc.eb) = make_uint2(kb.z, kb.w);
             *reinterpret_cast<uint4*>(p.c.v + row + 16 * li) = rv[i];
+          }
+        } else if constexpr (FMT == CF_MXFP4) {
+          uint32_t ba, bb;
+          piece_exps<LPR>(x, pc.ea, pc.eb, pc.on, s_unit[warp], ba, bb);
+          const uint32_t ca = e2m1x4(x[0], x[1], inverse_of(ba)), cb = e2m1x4(x[2], x[3], inverse_of(bb));
+          const uint32_t bv = exp_of(row_max<4>(rv[i]));
+          unpack8(rv[i], x);
+          const uint32_t vc = e2m1x8(x, bv);
+          if (keep && pl.ok) {
+            *reinterpret_cast<uint16_t*>(p.c.k + row + pc.ea / 2) = (uint16_t)ca;
+            *reinterpret_cast<uint16_t*>(p.c.k + row + pc.eb / 2) = (uint16_t)cb;
+            *reinterpret_cast<uint32_t*>(p.c.v + row + 4 * li) = vc;
+            const int64_t so = scale0 + h * p.c.shead;
+            if (pc.ea % 32 == 0) p.c.k_exps()[so + pc.ea / 32] = (uint8_t)ba;
+            if (pc.eb % 32 == 0) p.c.k_exps()[so + pc.eb / 32] = (uint8_t)bb;
+            if (li % 4 == 0) p.c.v_exps()[so + li / 4] = (uint8_t)bv;
           }
         } else {
           float s, ik, iv;
@@ -454,12 +531,14 @@ __global__ void __launch_bounds__(256, ITEMS > 1 ? 8 : 1) k3_rows_kernel(const Q
   }
   uint4 k[ITEMS], v[ITEMS];
   float ks[ITEMS], vs[ITEMS];
+  uint32_t kb[ITEMS], vb[ITEMS];
   Place pl[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     pl[i] = place_of(p, slot[i], li == 0);
     k[i] = v[i] = make_uint4(0, 0, 0, 0);
     ks[i] = vs[i] = 0.f;
+    kb[i] = vb[i] = 127;
     if (!on || !pl[i].ok) continue;
     if constexpr (WRITE) {
       const int32_t o = head[i] * p.D + 8 * li;
@@ -470,6 +549,12 @@ __global__ void __launch_bounds__(256, ITEMS > 1 ? 8 : 1) k3_rows_kernel(const Q
       if constexpr (FMT == CF_BF16) {
         k[i] = *reinterpret_cast<const uint4*>(p.c.k + o + 16 * li);
         v[i] = *reinterpret_cast<const uint4*>(p.c.v + o + 16 * li);
+      } else if constexpr (FMT == CF_MXFP4) {
+        k[i].x = *reinterpret_cast<const uint32_t*>(p.c.k + o + 4 * li);
+        v[i].x = *reinterpret_cast<const uint32_t*>(p.c.v + o + 4 * li);
+        const int64_t so = scale_at(p, pl[i], head[i]) + li / 4;
+        kb[i] = p.c.k_exps()[so];
+        vb[i] = p.c.v_exps()[so];
       } else {
         const uint2 kc = *reinterpret_cast<const uint2*>(p.c.k + o + 8 * li);
         const uint2 vc = *reinterpret_cast<const uint2*>(p.c.v + o + 8 * li);
@@ -490,6 +575,22 @@ __global__ void __launch_bounds__(256, ITEMS > 1 ? 8 : 1) k3_rows_kernel(const Q
           *reinterpret_cast<uint4*>(p.c.k + o + 16 * li) = k[i];
           *reinterpret_cast<uint4*>(p.c.v + o + 16 * li) = v[i];
         }
+      } else if constexpr (FMT == CF_MXFP4) {
+        const uint32_t bk = exp_of(row_max<4>(k[i])), bv = exp_of(row_max<4>(v[i]));
+        float2 x[4];
+        unpack8(k[i], x);
+        const uint32_t kc = e2m1x8(x, bk);
+        unpack8(v[i], x);
+        const uint32_t vc = e2m1x8(x, bv);
+        if (on && pl[i].ok) {
+          *reinterpret_cast<uint32_t*>(p.c.k + o + 4 * li) = kc;
+          *reinterpret_cast<uint32_t*>(p.c.v + o + 4 * li) = vc;
+          if (li % 4 == 0) {
+            const int64_t so = scale_at(p, pl[i], head[i]) + li / 4;
+            p.c.k_exps()[so] = (uint8_t)bk;
+            p.c.v_exps()[so] = (uint8_t)bv;
+          }
+        }
       } else {
         float s, ik, iv;
         scales_of(row_max<LPR>(k[i]), row_max<LPR>(v[i]), li, s, ik, iv);
@@ -508,6 +609,9 @@ __global__ void __launch_bounds__(256, ITEMS > 1 ? 8 : 1) k3_rows_kernel(const Q
       if constexpr (FMT == CF_E4M3) {
         k[i] = e4m3x8_bf16(make_uint2(k[i].x, k[i].y), ks[i]);
         v[i] = e4m3x8_bf16(make_uint2(v[i].x, v[i].y), vs[i]);
+      } else if constexpr (FMT == CF_MXFP4) {  // (a slot that is not there: zeros)
+        k[i] = e2m1x8_bf16(k[i].x, kb[i]);
+        v[i] = e2m1x8_bf16(v[i].x, vb[i]);
       }
       const int64_t o = ((int64_t)tok[i] * p.Hkv + head[i]) * p.D + 8 * li;
       *reinterpret_cast<uint4*>(p.k_out + o) = k[i];

@@ -2,6 +2,7 @@
 // validation and launches.  No allocation, no synchronisation.
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 #include <utility>
 
 #include "k3_decode.cuh"
@@ -37,14 +38,15 @@ k3moe_status check_dims(const k3attn_dims* d) {
 
 k3moe_status check_cache(const k3attn_cache* c, const k3attn_dims& d) {
   if (!c || !c->k || !c->v) return K3MOE_ERR_ARG;
-  if (c->format != K3ATTN_BF16 && c->format != K3ATTN_E4M3) return K3MOE_ERR_ARG;
-  const bool e4m3 = c->format == K3ATTN_E4M3;
-  if (e4m3 && (!c->k_scale || !c->v_scale)) return K3MOE_ERR_ARG;
+  if (c->format != K3ATTN_BF16 && c->format != K3ATTN_E4M3 && c->format != K3ATTN_MXFP4) return K3MOE_ERR_ARG;
+  const bool e4m3 = c->format == K3ATTN_E4M3, mxfp4 = c->format == K3ATTN_MXFP4;
+  if ((e4m3 || mxfp4) && (!c->k_scale || !c->v_scale)) return K3MOE_ERR_ARG;
   if (c->n_pages <= 0 || c->page_size <= 0 || c->reserved != 0) return K3MOE_ERR_ARG;
   if ((int64_t)c->n_pages * c->page_size > INT32_MAX) return K3MOE_ERR_SHAPE;  // slots are int32
   if (c->page_stride < d.head_dim || c->head_stride < d.head_dim || c->token_stride < d.head_dim)
     return K3MOE_ERR_SHAPE;
-  const int64_t unit = e4m3 ? 16 : 8;
+  if (mxfp4 && d.head_dim % 32) return K3MOE_ERR_SHAPE;
+  const int64_t unit = mxfp4 ? 32 : e4m3 ? 16 : 8;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->head_stride % unit ||
       c->token_stride % unit)
     return K3MOE_ERR_ALIGN;
@@ -52,19 +54,39 @@ k3moe_status check_cache(const k3attn_cache* c, const k3attn_dims& d) {
     if (c->scale_page_stride < 1 || c->scale_head_stride < 1 || c->scale_token_stride < 1) return K3MOE_ERR_SHAPE;
     if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return K3MOE_ERR_ALIGN;
   }
+  if (mxfp4) {
+    const int64_t row = K3ATTN_MXFP4_SCALES(d.head_dim);
+    if (c->scale_page_stride < row || c->scale_head_stride < row || c->scale_token_stride < row) return K3MOE_ERR_SHAPE;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || c->scale_page_stride % 4 || c->scale_head_stride % 4 ||
+        c->scale_token_stride % 4)
+      return K3MOE_ERR_ALIGN;
+  }
   return K3MOE_OK;
 }
 
+// f of the format as a constant
+template <typename F>
+cudaError_t with_format(int format, F&& f) {
+  switch (format) {
+    case K3ATTN_BF16: return f(std::integral_constant<int, CF_BF16>());
+    case K3ATTN_E4M3: return f(std::integral_constant<int, CF_E4M3>());
+    case K3ATTN_MXFP4: return f(std::integral_constant<int, CF_MXFP4>());
+  }
+  return cudaErrorInvalidValue;
+}
+
 CacheView view_of(const k3attn_cache& c) {
-  const int64_t b = c.format == K3ATTN_E4M3 ? 1 : 2;
+  auto bytes = [&](int64_t elements) {
+    return c.format == K3ATTN_MXFP4 ? elements / 2 : c.format == K3ATTN_E4M3 ? elements : 2 * elements;
+  };
   CacheView v{};
   v.k = static_cast<uint8_t*>(c.k);
   v.v = static_cast<uint8_t*>(c.v);
   v.ks = c.k_scale;
   v.vs = c.v_scale;
-  v.page = c.page_stride * b;
-  v.head = c.head_stride * b;
-  v.tok = c.token_stride * b;
+  v.page = bytes(c.page_stride);
+  v.head = bytes(c.head_stride);
+  v.tok = bytes(c.token_stride);
   v.spage = c.scale_page_stride;
   v.shead = c.scale_head_stride;
   v.stok = c.scale_token_stride;
@@ -217,7 +239,7 @@ int dec_nt(const k3attn_dims& d) { return d.n_heads / d.n_kv_heads <= 8 ? 1 : 2;
 // tokens of 2 key heads with 16 queries each, D 256: 65 us, 84 at 16 a time; the second pass
 // over the rows finds most of them in L2.  bf16, which fits but for a few words: 114, 95 us)
 int dec_nt_of(const k3attn_dims& d, int format) {
-  return format == K3ATTN_E4M3 && d.head_dim > 192 ? 1 : dec_nt(d);
+  return format != K3ATTN_BF16 && d.head_dim > 192 ? 1 : dec_nt(d);
 }
 
 // Whether calls for more than 8 query heads a key head take them 8 at a time all the same: twice
@@ -238,11 +260,11 @@ bool dec_narrow(const DecodeParams& p, int grid) {
   using C = DecCfg<FMT, DP, 1>;
   constexpr int UNIT = C::TW * C::WARPS;
   int64_t longest = (int64_t)p.table_width * p.c.page_size;
-  if (p.window > 0 && p.window < longest) longest = p.window;
+  if (p.window > 0 && (int64_t)p.window + p.sinks < longest) longest = (int64_t)p.window + p.sinks;
   const int64_t parts = (int64_t)p.B * p.Hkv * ((p.G + 7) / 8), units = parts * ((longest + UNIT - 1) / UNIT);
   const int most = FMT == CF_BF16 && DP > 192 ? 32
                    : 5 * parts <= grid        ? 16
-                   : FMT == CF_E4M3 && parts <= grid ? 4 : 1;
+                   : FMT != CF_BF16 && parts <= grid ? 4 : 1;
   return units <= (int64_t)most * grid;
 }
 
@@ -267,7 +289,7 @@ cudaError_t launch_decode(const DecodeParams& p, int dp, int nt, int dev, int sm
     case 385: return launch_decode_t<FMT, 192, 2>(p, dev, sms, s);
     case 512: return launch_decode_t<FMT, 256, 1>(p, dev, sms, s);
     case 513:
-      if constexpr (FMT != CF_E4M3) return launch_decode_t<FMT, 256, 2>(p, dev, sms, s);
+      if constexpr (FMT == CF_BF16) return launch_decode_t<FMT, 256, 2>(p, dev, sms, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -337,7 +359,7 @@ k3moe_status k3attn_kv_write(const k3attn_dims* dims, int32_t T, const uint16_t*
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, true>(p, sms, s) : launch_rows<CF_BF16, true>(p, sms, s)));
+  K3A_TRY(with_format(cache->format, [&](auto f) { return launch_rows<decltype(f)::value, true>(p, sms, s); }));
   return K3MOE_OK;
 }
 
@@ -371,7 +393,7 @@ k3moe_status k3attn_kv_append(const k3attn_dims* dims, int32_t T, const uint16_t
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY(cache->format == K3ATTN_E4M3 ? launch_norm<CF_E4M3>(p, sms, s) : launch_norm<CF_BF16>(p, sms, s));
+  K3A_TRY(with_format(cache->format, [&](auto f) { return launch_norm<decltype(f)::value>(p, sms, s); }));
   return K3MOE_OK;
 }
 
@@ -393,7 +415,7 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
   p.c = view_of(*cache);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_rows<CF_E4M3, false>(p, sms, s) : launch_rows<CF_BF16, false>(p, sms, s)));
+  K3A_TRY(with_format(cache->format, [&](auto f) { return launch_rows<decltype(f)::value, false>(p, sms, s); }));
   return K3MOE_OK;
 }
 
@@ -401,11 +423,19 @@ k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q
                            const k3attn_cache* cache, const int32_t* page_table, int32_t table_width,
                            const int32_t* lens, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                            void* stream) {
+  return k3attn_decode_sinks(dims, 0, B, q, q_stride, cache, page_table, table_width, lens, out, lse, ws, ws_bytes,
+                             stream);
+}
+
+k3moe_status k3attn_decode_sinks(const k3attn_dims* dims, int32_t n_sinks, int32_t B, const uint16_t* q,
+                                 int64_t q_stride, const k3attn_cache* cache, const int32_t* page_table,
+                                 int32_t table_width, const int32_t* lens, uint16_t* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream) {
   k3moe_status st = check_dims(dims);
   if (st != K3MOE_OK) return st;
   const k3attn_dims& d = *dims;
   if ((st = check_cache(cache, d)) != K3MOE_OK) return st;
-  if (B < 0 || table_width < 0) return K3MOE_ERR_ARG;
+  if (B < 0 || table_width < 0 || n_sinks < 0) return K3MOE_ERR_ARG;
   if (B == 0) return K3MOE_OK;
   if (!q || (table_width > 0 && !page_table) || !lens || !out || !ws) return K3MOE_ERR_ARG;
   if (B > 65535 || (int64_t)table_width * cache->page_size > INT32_MAX) return K3MOE_ERR_SHAPE;
@@ -420,6 +450,7 @@ k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q
   p.q = q; p.q_stride = q_stride;
   p.B = B; p.Hq = d.n_heads; p.Hkv = d.n_kv_heads; p.G = d.n_heads / d.n_kv_heads; p.D = d.head_dim;
   p.window = d.window;
+  p.sinks = d.window > 0 ? n_sinks : 0;
   p.scale = d.softmax_scale * 1.4426950408889634f;
   p.c = view_of(*cache);
   p.table = page_table; p.table_width = table_width; p.lens = lens;
@@ -430,8 +461,7 @@ k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q
   p.parts = reinterpret_cast<float*>(w + kRecords);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int dp = dec_dp(d), nt = dec_nt_of(d, cache->format);
-  K3A_TRY((cache->format == K3ATTN_E4M3 ? launch_decode<CF_E4M3>(p, dp, nt, dev, sms, s)
-                                        : launch_decode<CF_BF16>(p, dp, nt, dev, sms, s)));
+  K3A_TRY(with_format(cache->format, [&](auto f) { return launch_decode<decltype(f)::value>(p, dp, nt, dev, sms, s); }));
   return K3MOE_OK;
 }
 

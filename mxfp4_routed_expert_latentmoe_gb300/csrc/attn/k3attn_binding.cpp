@@ -27,7 +27,7 @@ decltype(&k3attn_qk_norm_rope) f_norm_rope;
 decltype(&k3attn_kv_write) f_write;
 decltype(&k3attn_kv_append) f_append;
 decltype(&k3attn_kv_read) f_read;
-decltype(&k3attn_decode) f_decode;
+decltype(&k3attn_decode_sinks) f_decode;
 
 struct Refused {};  // a Python error is set
 
@@ -87,6 +87,18 @@ Rows rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_t D, De
       return {static_cast<const uint16_t*>(t.data_ptr()), T > 1 ? t.stride(0) : heads * D};
   }
   refuse(o, name, at::kBFloat16, {T, heads, D}, ", the heads of a token dense", dev);
+}
+
+// a whole number that fits int32
+int32_t whole(PyObject* o, const char* name) {
+  int over = 0;
+  const long v = PyLong_AsLongAndOverflow(o, &over);
+  if (v == -1 && PyErr_Occurred()) throw Refused{};
+  if (over || v < INT32_MIN || v > INT32_MAX) {
+    PyErr_Format(PyExc_ValueError, "%s: a number that fits 32 bits is needed", name);
+    throw Refused{};
+  }
+  return (int32_t)v;
 }
 
 // the first size of a tensor (the tokens of a call)
@@ -257,9 +269,9 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// dims, q, cache, cache shape, page_table, lens, out, lse, ws, stream
+// dims, q, cache, cache shape, page_table, lens, out, lse, ws, stream[, sinks]
 PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&] {
+  return guarded(n, n == 11 ? 11 : 10, [&] {
     const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
     Device dev;
     const int32_t B = first_size(a[1], "q");
@@ -273,12 +285,13 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* lse = a[7] == Py_None ? nullptr : dense<float>(a[7], "lse", at::kFloat, {B, d.n_heads}, dev);
     const Work w = workspace(a[8], dev);
     if (width > INT32_MAX) return K3MOE_ERR_SHAPE;
-    return f_decode(&d, B, q.p, q.stride, c, table, (int32_t)width, lens, out, lse, w.p, w.bytes,
+    const int32_t sinks = n == 11 ? whole(a[10], "sinks") : 0;
+    return f_decode(&d, sinks, B, q.p, q.stride, c, table, (int32_t)width, lens, out, lse, w.p, w.bytes,
                     Stream(a[9], dev).handle);
   });
 }
 
-// the addresses of k3attn_qk_norm_rope, _kv_write, _kv_append, _kv_read, _decode
+// the addresses of k3attn_qk_norm_rope, _kv_write, _kv_append, _kv_read, _decode_sinks
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&] {
     void* f[5];
