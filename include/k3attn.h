@@ -2,7 +2,7 @@
  * k3attn.h -- C ABI of the attention operators that stand before the routed-expert block
  * of a decoder layer when it serves tokens: norms of queries and keys for each head with
  * the position rotation, a paged key-value cache (16 bits, or quantised to 8 or 4 as it is
- * written), and the attention of one new token over its pages.
+ * written), and the attention of new tokens over its pages: one of each sequence, or many.
  *
  * With D = head_dim, R = rot_dim, per token at position p and per head row x in R^D:
  *
@@ -183,6 +183,28 @@ k3moe_status k3attn_decode_sinks(const k3attn_dims* dims, int32_t n_sinks, int32
                                  int64_t q_stride, const k3attn_cache* cache, const int32_t* page_table,
                                  int32_t table_width, const int32_t* lens, uint16_t* out, float* lse, void* ws,
                                  size_t ws_bytes, void* stream);
+
+/* Attention of the new tokens of B sequences, any number of each: prompts, chunks of them behind
+ * what is cached already, a few drafted tokens.  The new tokens' own keys and values are in the cache.
+ *   q [T] rows of Hq * D bf16, q_stride elements apart: all sequences' new tokens
+ *   q_starts [B + 1] int32, not falling, 0 .. T: sequence b's new tokens are rows q_starts[b] ..
+ *     q_starts[b + 1] - 1, in order, and are the last of its cached ones: with n of them row i of the
+ *     sequence is at position p = lens[b] - n + i, and attends to the cached tokens t <= p, with a
+ *     window to those with t > p - window or t < n_sinks
+ *   page_table [B, table_width], lens [B] int32: as in k3attn_decode, lens[b] counts the new tokens
+ *   out [T, Hq, D] bf16;  lse [T, Hq] f32 or NULL: as k3attn_decode's.  Rows of no sequence (in front of
+ *     q_starts[0], from q_starts[B] on) are left as they were
+ * B at most 65535.  q_starts and lens are read on the device (a captured call replays with new
+ * ones; T is the capture's) and must not change while the call runs.  q_starts that fall or leave
+ * 0 .. T, and a length below its new tokens' number, set K3ATTN_DEV_BAD_LENGTH; a token at a
+ * negative position attends to nothing (out 0, lse -infinity).
+ * ws: k3attn_prefill_workspace_bytes(dims) bytes (0 for invalid dims), readied by
+ * k3attn_workspace_init; such a workspace serves k3attn_decode and the other calls too. */
+size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims);
+k3moe_status k3attn_prefill(const k3attn_dims* dims, int32_t n_sinks, int32_t B, int32_t T, const uint16_t* q,
+                            int64_t q_stride, const int32_t* q_starts, const k3attn_cache* cache,
+                            const int32_t* page_table, int32_t table_width, const int32_t* lens, uint16_t* out,
+                            float* lse, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

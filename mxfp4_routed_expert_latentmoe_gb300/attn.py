@@ -71,6 +71,8 @@ def _funcs():
             "k3attn_kv_append": ([D, i32, p, i64, p, i64, p, i64, p, p, p, p, p, C, p, p, p, sz, p], ctypes.c_int),
             "k3attn_kv_read": ([D, i32, p, C, p, p, p, sz, p], ctypes.c_int),
             "k3attn_decode": ([D, i32, p, i64, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
+            "k3attn_prefill_workspace_bytes": ([D], sz),
+            "k3attn_prefill": ([D, i32, i32, i32, p, i64, p, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
             "k3attn_decode_sinks": ([D, i32, i32, p, i64, C, p, i32, p, p, p, p, sz, p], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
@@ -99,7 +101,7 @@ def _load():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.bind(*(ctypes.cast(getattr(L, "k3attn_" + n), ctypes.c_void_p).value
-                   for n in ("qk_norm_rope", "kv_write", "kv_append", "kv_read", "decode_sinks")))
+                   for n in ("qk_norm_rope", "kv_write", "kv_append", "kv_read", "decode_sinks", "prefill")))
         _native = mod
     return _native
 
@@ -113,15 +115,17 @@ def declared_functions() -> list:
 
 
 # ------------------------------------------------------------------------------ what a program keeps
-def workspace_bytes(d: Dims) -> int:
-    """Bytes of workspace that decode needs with these dims (0: unsupported); the other operators
-    take any of at least MIN_WORKSPACE."""
-    return int(_funcs().k3attn_workspace_bytes(ctypes.byref(d)))
+def workspace_bytes(d: Dims, prefill: bool = False) -> int:
+    """Bytes of workspace that decode, or with `prefill` both prefill and decode, need with these dims
+    (0: unsupported); the other operators take any of at least MIN_WORKSPACE."""
+    f = _funcs().k3attn_prefill_workspace_bytes if prefill else _funcs().k3attn_workspace_bytes
+    return int(f(ctypes.byref(d)))
 
 
-def workspace(d: Dims, device="cuda"):
-    """A workspace for calls with these dims (or smaller ones), readied for its first use."""
-    n = workspace_bytes(d)
+def workspace(d: Dims, device="cuda", prefill: bool = False):
+    """A workspace for calls with these dims (or smaller ones), with `prefill` for prefill too, readied
+    for its first use."""
+    n = workspace_bytes(d, prefill)
     if n == 0:
         raise ValueError("unsupported dims")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -261,3 +265,15 @@ def decode(d: Dims, q, cache: KVCache, page_table, lens, out, ws, lse=None, stre
                                        _handle(stream), sinks)
     if code:
         _check(code, "k3attn_decode")
+
+
+def prefill(d: Dims, q, q_starts, cache: KVCache, page_table, lens, out, ws, lse=None, stream=None, sinks=0):
+    """k3attn_prefill: q [T, Hq, D] bf16, the new tokens of all sequences, sequence b's the rows
+    q_starts[b] .. q_starts[b + 1] - 1 (q_starts [B + 1] int32) and the last of its lens[b] cached tokens
+    on the pages page_table[b]; each attends to the tokens up to its own (with d.window the last d.window
+    of them, and the first `sinks`) -> out [T, Hq, D] bf16 and, if given, lse [T, Hq] f32.  ws:
+    workspace(d, prefill=True)."""
+    code = (_native or _load()).prefill(d.addr, q, q_starts, cache.addr, cache.rows, page_table, lens, out, lse, ws,
+                                        _handle(stream), sinks)
+    if code:
+        _check(code, "k3attn_prefill")

@@ -6,6 +6,7 @@
 #include <utility>
 
 #include "k3_decode.cuh"
+#include "k3_prefill.cuh"
 #include "k3_qkv.cuh"
 
 namespace {
@@ -297,6 +298,46 @@ cudaError_t launch_decode(const DecodeParams& p, int dp, int nt, int dev, int sm
 }  // namespace
 
 extern "C" {
+
+size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims) { return k3attn_workspace_bytes(dims); }
+
+k3moe_status k3attn_prefill(const k3attn_dims* dims, int32_t n_sinks, int32_t B, int32_t T, const uint16_t* q,
+                            int64_t q_stride, const int32_t* q_starts, const k3attn_cache* cache,
+                            const int32_t* page_table, int32_t table_width, const int32_t* lens, uint16_t* out,
+                            float* lse, void* ws, size_t ws_bytes, void* stream) {
+  k3moe_status st = check_dims(dims);
+  if (st != K3MOE_OK) return st;
+  const k3attn_dims& d = *dims;
+  if ((st = check_cache(cache, d)) != K3MOE_OK) return st;
+  if (B < 0 || T < 0 || table_width < 0 || n_sinks < 0) return K3MOE_ERR_ARG;
+  if (B == 0 || T == 0) return K3MOE_OK;
+  if (!q || !q_starts || (table_width > 0 && !page_table) || !lens || !out || !ws) return K3MOE_ERR_ARG;
+  if (B > 65535 || (int64_t)table_width * cache->page_size > INT32_MAX) return K3MOE_ERR_SHAPE;
+  if ((st = check_rows(q_stride, (int64_t)d.n_heads * d.head_dim)) != K3MOE_OK) return st;
+  if (!aligned(q, 16) || !aligned(q_starts, 4) || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(ws, 16))
+    return K3MOE_ERR_ALIGN;
+  if (ws_bytes < k3attn_prefill_workspace_bytes(dims)) return K3MOE_ERR_WORKSPACE;
+  int dev, sms;
+  if ((st = check_device(&dev, &sms)) != K3MOE_OK) return st;
+  PrefillParams p{};
+  p.q = q; p.q_stride = q_stride;
+  p.B = B; p.T = T; p.Hq = d.n_heads; p.Hkv = d.n_kv_heads; p.G = d.n_heads / d.n_kv_heads; p.D = d.head_dim;
+  p.window = d.window;
+  p.sinks = d.window > 0 ? n_sinks : 0;
+  p.scale = d.softmax_scale * 1.4426950408889634f;
+  p.c = view_of(*cache);
+  p.starts = q_starts; p.table = page_table; p.table_width = table_width; p.lens = lens;
+  p.out = out; p.lse = lse;
+  p.status = static_cast<uint32_t*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  K3A_TRY(with_format(cache->format, [&](auto f) {
+    const int64_t grid = ((int64_t)T * d.n_heads + 7) / 8;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    return launch(k3_prefill_simple_kernel<decltype(f)::value>, dim3((unsigned)grid), dim3(256), 0, s, p);
+  }));
+  return K3MOE_OK;
+}
 
 size_t k3attn_workspace_bytes(const k3attn_dims* dims) {
   if (check_dims(dims) != K3MOE_OK) return 0;

@@ -28,6 +28,7 @@ decltype(&k3attn_kv_write) f_write;
 decltype(&k3attn_kv_append) f_append;
 decltype(&k3attn_kv_read) f_read;
 decltype(&k3attn_decode_sinks) f_decode;
+decltype(&k3attn_prefill) f_prefill;
 
 struct Refused {};  // a Python error is set
 
@@ -291,16 +292,44 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// the addresses of k3attn_qk_norm_rope, _kv_write, _kv_append, _kv_read, _decode_sinks
+// dims, q, q_starts, cache, cache shape, page_table, lens, out, lse, ws, stream, sinks
+PyObject* py_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const k3attn_dims& d = *struct_at<k3attn_dims>(a[0]);
+    Device dev;
+    const int32_t T = first_size(a[1], "q"), B = first_size(a[2], "q_starts") - 1;
+    if (B < 0) {
+      PyErr_SetString(PyExc_ValueError, "q_starts: one more entry than sequences is needed");
+      throw Refused{};
+    }
+    const Rows q = rows(a[1], "q", T, d.n_heads, d.head_dim, dev);
+    const int32_t* starts = dense<int32_t>(a[2], "q_starts", at::kInt, {B + 1}, dev);
+    const k3attn_cache* c = cache_at(a[3], a[4], d, dev);
+    int64_t width = -1;
+    if (THPVariable_Check(a[5]) && THPVariable_Unpack(a[5]).dim() == 2) width = THPVariable_Unpack(a[5]).size(1);
+    const int32_t* table = dense<int32_t>(a[5], "page_table", at::kInt, {B, width}, dev);
+    const int32_t* lens = dense<int32_t>(a[6], "lens", at::kInt, {B}, dev);
+    uint16_t* out = dense<uint16_t>(a[7], "out", at::kBFloat16, {T, d.n_heads, d.head_dim}, dev);
+    float* lse = a[8] == Py_None ? nullptr : dense<float>(a[8], "lse", at::kFloat, {T, d.n_heads}, dev);
+    const Work w = workspace(a[9], dev);
+    const int32_t sinks = whole(a[11], "sinks");
+    if (width > INT32_MAX) return K3MOE_ERR_SHAPE;
+    return f_prefill(&d, sinks, B, T, q.p, q.stride, starts, c, table, (int32_t)width, lens, out, lse, w.p, w.bytes,
+                     Stream(a[10], dev).handle);
+  });
+}
+
+// the addresses of k3attn_qk_norm_rope, _kv_write, _kv_append, _kv_read, _decode_sinks, _prefill
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 5, [&] {
-    void* f[5];
-    for (int i = 0; i < 5; ++i) f[i] = const_cast<void*>(struct_at<void>(a[i]));
+  return guarded(n, 6, [&] {
+    void* f[6];
+    for (int i = 0; i < 6; ++i) f[i] = const_cast<void*>(struct_at<void>(a[i]));
     f_norm_rope = reinterpret_cast<decltype(f_norm_rope)>(f[0]);
     f_write = reinterpret_cast<decltype(f_write)>(f[1]);
     f_append = reinterpret_cast<decltype(f_append)>(f[2]);
     f_read = reinterpret_cast<decltype(f_read)>(f[3]);
     f_decode = reinterpret_cast<decltype(f_decode)>(f[4]);
+    f_prefill = reinterpret_cast<decltype(f_prefill)>(f[5]);
     return 0;
   });
 }
@@ -312,6 +341,7 @@ PyMethodDef methods[] = {{"bind", K3_FAST(py_bind), METH_FASTCALL, nullptr},
                          {"kv_append", K3_FAST(py_append), METH_FASTCALL, nullptr},
                          {"kv_read", K3_FAST(py_read), METH_FASTCALL, nullptr},
                          {"decode", K3_FAST(py_decode), METH_FASTCALL, nullptr},
+                         {"prefill", K3_FAST(py_prefill), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "k3attn_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
