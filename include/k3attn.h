@@ -109,6 +109,10 @@ typedef struct {
 #define K3ATTN_DEV_BAD_LENGTH 0x4u /* a length outside 0 .. table_width * page_size: taken as the
                                       nearest of these */
 
+/* In the status word too: a wait inside k3attn_prefill ran out (about two seconds); its results are
+ * invalid. */
+#define K3ATTN_TIMEOUT 0x100u
+
 /* Bytes of workspace for k3attn_decode with these dims; the other calls need the first
  * K3ATTN_MIN_WORKSPACE of them.  0 for invalid dims. */
 #define K3ATTN_MIN_WORKSPACE 256u

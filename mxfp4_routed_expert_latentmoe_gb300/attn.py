@@ -26,6 +26,7 @@ from . import device_status as _device_status
 BF16, E4M3, MXFP4 = 0, 1, 4  # K3ATTN_BF16, K3ATTN_E4M3, K3ATTN_MXFP4
 MIN_WORKSPACE = 256  # K3ATTN_MIN_WORKSPACE
 DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_BAD_LENGTH = 0x1, 0x2, 0x4
+TIMEOUT = 0x100  # K3ATTN_TIMEOUT
 _fns = None
 _native = None  # the extension module, loaded by the first operator
 

@@ -1,10 +1,24 @@
 // k3_prefill.cuh -- attention of many new tokens per sequence over the paged key-value cache.
 //
-// A warp takes one (token, query head): 32 keys at a time, a lane computes a key's logit, then the
-// lanes hold dims of the value sum.
+// One pass over the keys with a running maximum and sum, on the tensor cores: a tile is 256 rows
+// (128 for head dims past 128), the query heads of one key head times some tokens, so that a row of
+// keys is read once for all of them.  Per tile of 128 keys (64 past 128 dims) and 128 rows:
+//   S = Q K^T       128 x 128 in tensor memory
+//   P = 2^(S - m)   rounded to bf16, over S in tensor memory
+//   O += P V        128 x D in tensor memory
+// Warps: 0-3 and 4-7 the softmax of a tile's two halves, a row a thread (the tensor core works on one
+// half while the other's weights are formed); 8-13 bring keys and values, as bf16, into shared
+// memory, row by row through the page table (any page size, any strides); 14 says which tile is
+// next; 15 issues the products.
+//
+// The work, tiles times keys, stands in a line (each tile's start counts as PRE_START keys) and is
+// dealt out evenly to the blocks, whatever the lengths and masks; a tile that is cut leaves an
+// unnormalised record of each part in the workspace, and the part that arrives last joins them, in
+// order.
 #pragma once
 
 #include "k3_decode.cuh"
+#include "k3_tmem.cuh"
 
 namespace k3 {
 
@@ -12,19 +26,166 @@ struct PrefillParams {
   const uint16_t* q;
   int64_t q_stride;
   int32_t B, T, Hq, Hkv, G, D, window, sinks;
-  float scale;  // softmax_scale * log2(e): logits in powers of two
+  int32_t groups, heads, tokens;  // head groups of a key head, heads of each, tokens of a tile
+  float scale;                    // softmax_scale * log2(e): logits in powers of two
   CacheView c;
   const int32_t *starts, *table, *lens;
   int32_t table_width;
   uint16_t* out;
   float* lse;
   uint32_t* status;
+  uint32_t* arrived;  // two counters a block, zero between calls
+  float* parts;       // two records a block
 };
 
+// What a tile's start counts as, the fewest keys of a block, tiles of keys up to which a tile is not cut.
+constexpr int PRE_START = 256, PRE_LEAST = 512, PRE_WHOLE = 2;
+constexpr int PRE_MAX_BLOCKS = 192;
+constexpr int PRE_THREADS = 512, PRE_COPY_WARPS = 6;
+// Registers of the softmax warps and of the others: 256 threads each, 65536 in all, which the block
+// is launched with
+constexpr int PRE_REGS_SOFTMAX = 192, PRE_REGS_OTHERS = 64;
+
+// ---------------------------------------------------------------------------- the order of the work
+K3_HD int64_t pre_min(int64_t a, int64_t b) { return a < b ? a : b; }
+K3_HD int64_t pre_max(int64_t a, int64_t b) { return a > b ? a : b; }
+
+// A sequence's tiles (of one head group): n new tokens behind `old` ones, TT tokens a tile.  Its keys in
+// order: the sinks in front of the first token's window, then that window's and the rest.
+struct PreSeq {
+  int64_t n, old, W, S;
+  int32_t TT;
+  K3_HD int64_t tiles() const { return (n + TT - 1) / TT; }
+  K3_HD int64_t keys(int64_t m) const {
+    const int64_t p0 = old + m * TT, p1 = old + pre_min(n, (m + 1) * TT), f = W > 0 ? pre_max(0, p0 - W + 1) : 0;
+    return p1 - f + pre_min(S, f);
+  }
+  // the place of tile m's start, counted from tile 0's: the keys of full tiles in closed form (up to
+  // tile x the window's first token is no further than the sinks: all tokens are keys)
+  K3_HD int64_t place(int64_t m) const {
+    if (n <= 0) return 0;
+    const int64_t all = tiles(), full = m < all ? m : all - 1;
+    int64_t x = full;
+    if (W > 0) {
+      const int64_t t = S + W - 1 - old;
+      x = pre_min(full, t < 0 ? 0 : t / TT + 1);
+    }
+    int64_t at = x * old + TT * (x * (x + 1) / 2) + (full - x) * (TT - 1 + W + S) + full * PRE_START;
+    if (m >= all) at += keys(all - 1) + PRE_START;
+    return at;
+  }
+};
+
+// sequence b's rows of q and cached tokens, within the tensors; false: they were not
+K3_HD bool pre_bounds(const PrefillParams& p, int b, int32_t& s0, int32_t& n, int32_t& len) {
+  const int32_t a = p.starts[b], e = p.starts[b + 1], l = p.lens[b];
+  const int64_t most = (int64_t)p.table_width * p.c.page_size;
+  s0 = a < 0 ? 0 : a > p.T ? p.T : a;
+  const int32_t s1 = e < s0 ? s0 : e > p.T ? p.T : e;
+  n = s1 - s0;
+  len = l < 0 ? 0 : l > most ? (int32_t)most : l;
+  return s0 == a && s1 == e && len == l && len >= n;
+}
+K3_HD PreSeq pre_seq(const PrefillParams& p, int32_t n, int32_t len) {
+  return PreSeq{n, len > n ? len - n : 0, p.window, p.sinks, p.tokens};
+}
+
+// One part of a tile, as the block's warps get it.
+struct PreItem {
+  int32_t end;                          // no more
+  int32_t b, kvh, head0, heads;         // sequence, key head, first query head and their number
+  int32_t row0, ntok, pos0, len;        // first row of q, tokens, position of the first, cached tokens
+  int32_t f, ns, keys;                  // keys: ns sinks, then from token f on, in all
+  int32_t kt0, kt1;                     // tiles of keys
+  int32_t whole, c0, parts;             // all of them; else the tile's first block, the number of them
+};
+
+// The walk through a block's items.
+struct PreWalk {
+  int64_t x, end, chunk;  // place of the tile's first key, end of the block's range, places of a block
+  int64_t m;
+  int32_t b, h, kt, s0, n, len, bn;
+  K3_HD void seq(const PrefillParams& p) { pre_bounds(p, b, s0, n, len); }
+  // the block's first item: its range begins `off` places after sequence b's start
+  K3_HD void land(const PrefillParams& p, int64_t off) {
+    seq(p);
+    const PreSeq s = pre_seq(p, n, len);
+    const int64_t all = s.tiles(), each = s.place(all);
+    const int64_t hh = off / each, rem = off - hh * each;
+    h = (int32_t)hh;
+    int64_t lo = 0, hi = all;  // the last tile that starts at or before rem
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) / 2;
+      if (s.place(mid) <= rem)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    m = lo;
+    x = end - chunk - rem + s.place(m) + PRE_START;  // (end - chunk: the block's first place)
+    const int64_t first = end - chunk, nkt = (s.keys(m) + bn - 1) / bn;
+    kt = 0;
+    if (first > x) {
+      const int64_t k = (first - x + bn - 1) / bn;
+      if (nkt <= PRE_WHOLE || k >= nkt)
+        next(p);  // another block's to the end
+      else
+        kt = (int32_t)k;
+    }
+  }
+  K3_HD void next(const PrefillParams& p) {
+    const PreSeq s = pre_seq(p, n, len);
+    x += s.keys(m) + PRE_START;
+    kt = 0;
+    if (++m < s.tiles()) return;
+    m = 0;
+    if (++h < p.Hkv * p.groups) return;
+    h = 0;
+    do {
+      if (++b >= p.B) return;
+      if (x >= end) return;  // (past the range already, whatever it is)
+      seq(p);
+    } while (n <= 0);
+  }
+  // the item here; false: there is none
+  K3_HD bool item(const PrefillParams& p, PreItem& it) {
+    it.end = 1;
+    if (b >= p.B || (kt == 0 && x >= end)) return false;
+    const PreSeq s = pre_seq(p, n, len);
+    const int64_t keys = s.keys(m), nkt = (keys + bn - 1) / bn;
+    int64_t k1 = nkt <= PRE_WHOLE ? nkt : pre_min(nkt, (end - x + bn - 1) / bn);
+    it.end = 0;
+    it.b = b;
+    it.kvh = h / p.groups;
+    const int32_t grp = h - it.kvh * p.groups;
+    it.head0 = it.kvh * p.G + grp * p.heads;
+    it.heads = (int32_t)pre_min(p.heads, p.G - grp * p.heads);
+    it.row0 = s0 + (int32_t)(m * p.tokens);
+    it.ntok = (int32_t)pre_min(p.tokens, n - m * p.tokens);
+    it.pos0 = (int32_t)(len - n + m * p.tokens);
+    it.len = len;
+    it.f = p.window > 0 ? (int32_t)pre_max(0, (int64_t)it.pos0 - p.window + 1) : 0;
+    it.ns = (int32_t)pre_min(p.sinks, it.f);
+    it.keys = (int32_t)keys;
+    it.kt0 = kt;
+    it.kt1 = (int32_t)k1;
+    it.whole = kt == 0 && k1 == nkt;
+    it.c0 = (int32_t)(x / chunk);
+    it.parts = (int32_t)((x + (nkt - 1) * bn) / chunk) - it.c0 + 1;
+    kt = (int32_t)k1;
+    if (k1 == nkt) next(p);
+    else b = p.B;  // the rest is the next block's
+    return true;
+  }
+};
+// places of a block
+K3_HD int64_t pre_chunk(int64_t total, int64_t blocks) { return pre_max(PRE_LEAST, (total + blocks - 1) / blocks); }
+
+// ---------------------------------------------------------------------------- rows one by one
 // eight values of a cached row
 template <int FMT>
 K3_DEVI void row8(const uint8_t* row, int chunk, float scale, const uint8_t* exps, float (&x)[8]) {
-  uint4 v;
+  uint4 v = {};
   if constexpr (FMT == CF_BF16) {
     v = ldg128(row + 16 * chunk);
   } else if constexpr (FMT == CF_E4M3) {
@@ -51,68 +212,48 @@ K3_DEVI void row8(const uint8_t* row, int chunk, float scale, const uint8_t* exp
   }
 }
 
+// One row by a warp, over its visible tokens alone: a tile's products take every row of values, and
+// weight 0 times a value that is infinite or NaN is NaN, so that rows which come out without being
+// finite are formed again here.  32 keys at a time, a lane a key, then 8 dims a lane.
 template <int FMT>
-__global__ void __launch_bounds__(256) k3_prefill_simple_kernel(const PrefillParams p) {
-  __shared__ float s_q[8][256];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t item = (int64_t)blockIdx.x * 8 + warp;
-  grid_dep_wait();
-  grid_dep_launch();
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < p.B; b += 256) {
-      const int64_t most = (int64_t)p.table_width * p.c.page_size;
-      const int32_t s0 = p.starts[b], s1 = p.starts[b + 1], n = p.lens[b];
-      if (s0 < 0 || s1 < s0 || s1 > p.T || n < 0 || n > most || n < s1 - s0) flag_status(p.status, K3ATTN_DEV_BAD_LENGTH);
-    }
-  if (item >= (int64_t)p.T * p.Hq) return;
-  const int t = (int)(item / p.Hq), h = (int)(item % p.Hq), kvh = h / p.G;
-  int lo = 0, hi = p.B;  // the last sequence that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    (p.starts[mid] <= t ? lo : hi) = mid;
-  }
-  const int32_t s0 = max(p.starts[lo], 0), s1 = min(p.starts[lo + 1], p.T);
-  if (t < s0 || t >= s1) return;  // no sequence's
-  const int64_t most = min((int64_t)p.table_width * p.c.page_size, (int64_t)INT32_MAX);
-  const int32_t n = (int32_t)min(most, (int64_t)max(p.lens[lo], 0)), pos = n - s1 + t;
-  for (int d = lane; d < p.D; d += 32) s_q[warp][d] = bf16_bits_to_f32(p.q[t * p.q_stride + (int64_t)h * p.D + d]);
-  __syncwarp();
+__device__ __noinline__ void prefill_row(const PrefillParams& p, int b, int kvh, int head, int64_t row, int32_t pos, int lane) {
+  const uint16_t* const q = p.q + row * p.q_stride + (int64_t)head * p.D;
   const int32_t f = p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0, ns = min(p.sinks, f);
   const int32_t count = pos < 0 ? 0 : ns + (pos + 1 - f);
   float m = -INFINITY, l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
   for (int32_t i0 = 0; i0 < count; i0 += 32) {
     const int32_t i = i0 + lane;
-    int64_t row = -1, so = 0;
+    int64_t at = -1, so = 0;
     float s = -INFINITY;
-    if (i < count) {
-      const int32_t tok = i < ns ? i : f + (i - ns), pg = (int32_t)p.c.by_page(tok), at = tok - pg * p.c.page_size;
-      const int32_t entry = p.table[(int64_t)lo * p.table_width + pg];
+    if (i < count && i >= 0) {
+      const int32_t tok = i < ns ? i : f + (i - ns), pg = (int32_t)p.c.by_page(tok), in_page = tok - pg * p.c.page_size;
+      const int32_t entry = p.table[(int64_t)b * p.table_width + pg];
       if (entry >= 0 && entry < p.c.n_pages) {
-        row = entry * p.c.page + kvh * p.c.head + at * p.c.tok;
-        so = entry * p.c.spage + kvh * p.c.shead + at * p.c.stok;
+        at = entry * p.c.page + kvh * p.c.head + in_page * p.c.tok;
+        so = entry * p.c.spage + kvh * p.c.shead + in_page * p.c.stok;
         s = 0.f;
-        const float ks = FMT == CF_E4M3 ? p.c.ks[so] : 1.f;
+#pragma unroll 1
         for (int c = 0; c < p.D / 8; ++c) {
           float x[8];
-          row8<FMT>(p.c.k + row, c, 1.f, p.c.k_exps() + so, x);
+          row8<FMT>(p.c.k + at, c, 1.f, p.c.k_exps() + so, x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(x[e], s_q[warp][8 * c + e], s);
+          for (int e = 0; e < 8; ++e) s = fmaf(x[e], bf16_bits_to_f32(__ldg(q + 8 * c + e)), s);
         }
-        s *= ks * p.scale;
-      } else {
-        flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
+        s *= (FMT == CF_E4M3 ? p.c.ks[so] : 1.f) * p.scale;
       }
     }
     float top = s;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.f : m1, fall = exp2f(m - base), w = exp2f(s - base);
+    const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.f : m1, fall = ex2(m - base), w = ex2(s - base);
     m = m1;
     l = l * fall + w;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= fall;
+#pragma unroll 1
     for (int j = 0; j < 32; ++j) {
-      const int64_t r = __shfl_sync(0xFFFFFFFFu, row, j), o = __shfl_sync(0xFFFFFFFFu, so, j);
+      const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j), o = __shfl_sync(0xFFFFFFFFu, so, j);
       const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
       if (r < 0 || 8 * lane >= p.D) continue;
       float x[8];
@@ -124,12 +265,648 @@ __global__ void __launch_bounds__(256) k3_prefill_simple_kernel(const PrefillPar
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
   const float r = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row = (int64_t)t * p.Hq + h;
   if (8 * lane < p.D) {
-    const uint2 a = bf16x4(acc[0] * r, acc[1] * r, acc[2] * r, acc[3] * r), b = bf16x4(acc[4] * r, acc[5] * r, acc[6] * r, acc[7] * r);
-    *reinterpret_cast<uint4*>(p.out + row * p.D + 8 * lane) = make_uint4(a.x, a.y, b.x, b.y);
+    const uint2 a = bf16x4(acc[0] * r, acc[1] * r, acc[2] * r, acc[3] * r), c = bf16x4(acc[4] * r, acc[5] * r, acc[6] * r, acc[7] * r);
+    *reinterpret_cast<uint4*>(p.out + (row * p.Hq + head) * p.D + 8 * lane) = make_uint4(a.x, a.y, c.x, c.y);
   }
-  if (lane == 0 && p.lse) p.lse[row] = lse_of(m == -INFINITY ? 0.f : m, l);
+}
+
+// ---------------------------------------------------------------------------- the kernel
+template <int FMT, int DP>
+struct PreCfg {
+  static constexpr int HALVES = DP <= 128 ? 2 : 1;  // 128 rows each
+  static constexpr int ROWS = 128 * HALVES;
+  static constexpr int BN = DP <= 128 ? 128 : 64;  // keys of a tile
+  static constexpr int Q_HALF = 128 * DP * 2;
+  static constexpr int TILE = BN * DP * 2;  // bytes of a tile's keys, or values
+  static constexpr int ROOM = 227 * 1024 - 1024 - HALVES * Q_HALF - 2048 - (FMT == CF_E4M3 ? 8192 : 0);
+  static constexpr int SLOTS = ROOM / (2 * TILE) > 4 ? 4 : ROOM / (2 * TILE);  // tiles of keys, and of values, in flight
+  static constexpr int UNITS = BN / 8;  // a warp's copy: 8 rows
+  // masks and scales of 8 tiles: those of a tile are read until its weights are formed, and the copies are
+  // SLOTS tiles and one ahead of that (two with one half)
+  static constexpr int RING = 8;
+  static constexpr int SCALES = FMT == CF_E4M3 ? RING * 2 * BN * 4 : 0;
+  // barriers (512 bytes), items, masks, scales
+  static constexpr int SMEM = 1024 + HALVES * Q_HALF + 2 * SLOTS * TILE + 512 + 4 * 128 + RING * 16 + 64 + SCALES;
+  static constexpr int REC = ROWS * (DP + 2);  // floats of a record
+  // columns of tensor memory: a half's logits (with one half two buffers), its weights over them (with one
+  // half behind the sums), its sums
+  static constexpr uint32_t S_AT = BN, O_AT = DP <= 128 ? 256 : 128, P_AT = DP <= 128 ? 0 : 384, P_STEP = DP <= 128 ? BN : BN / 2;
+  static_assert(SLOTS >= 2 && SLOTS + 2 <= RING && SMEM <= 227 * 1024 && sizeof(PreItem) <= 128, "does not fit");
+};
+
+K3_DEVI float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+K3_DEVI uint32_t bf16x2_of(float2 x) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(x);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the low bits of a word: those below x
+K3_DEVI uint32_t bits_below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; }
+
+// a byte pair's E4M3 codes as bf16 (exact)
+K3_DEVI void e4m3x4_bf16(uint32_t w, uint32_t& a, uint32_t& b) {
+  uint32_t h[2];
+  e4m3x4_f16x4(w, h[0], h[1]);
+  a = bf16x2_of(__half22float2(*reinterpret_cast<const __half2*>(&h[0])));
+  b = bf16x2_of(__half22float2(*reinterpret_cast<const __half2*>(&h[1])));
+}
+K3_DEVI uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Eight E2M1 codes times 2^(b - 127) as bf16, in order: a code's sign and low bits placed at bits 15 and
+// 8..6 are the value times 2^-126 (one product puts them there), which is scaled by 2^(b - 1), in two
+// steps where that is no bf16 number.  Exact.
+K3_DEVI uint4 e2m1x8_scaled(uint32_t w, uint32_t b) {
+  const uint32_t w8 = w >> 8;
+  uint32_t o[4] = {((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, ((w & 0x00F000F0u) * 0x104u) & 0x81C081C0u,
+                   ((w8 & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, ((w8 & 0x00F000F0u) * 0x104u) & 0x81C081C0u};
+  const uint32_t e = b == 255 ? 0x7FC0u : b <= 128 ? (b + 126) << 7 : 254u << 7, s = e | e << 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], s);
+  if (b > 128 && b != 255) {
+    const uint32_t e2 = (b - 1) << 7, s2 = e2 | e2 << 16;  // 2^(b - 128)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], s2);
+  }
+  return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[0], o[1], 0x7632),
+                    __byte_perm(o[2], o[3], 0x7632));
+}
+K3_DEVI void sts128(uint32_t a, uint4 v) { *reinterpret_cast<uint4*>(__cvta_shared_to_generic(a)) = v; }
+
+template <int FMT, int DP>
+__global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const PrefillParams p) {
+  using C = PreCfg<FMT, DP>;
+  constexpr int BN = C::BN, SLOTS = C::SLOTS, HALVES = C::HALVES, ITEMS = 4, RING = C::RING;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_gave_up;
+  __shared__ int64_t s_sum[PRE_THREADS / 32], s_off;
+  __shared__ int32_t s_b, s_last[2];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, k_at = q_at + HALVES * C::Q_HALF, v_at = k_at + SLOTS * C::TILE, bars = v_at + SLOTS * C::TILE;
+  const uint32_t items_at = bars + 512, masks_at = items_at + ITEMS * 128, scales_at = (masks_at + RING * 16 + 63u) & ~63u;
+  auto k_full = [&](int s) { return bars + 8 * s; };
+  auto k_empty = [&](int s) { return bars + 8 * (4 + s); };
+  auto v_full = [&](int s) { return bars + 8 * (8 + s); };
+  auto v_empty = [&](int s) { return bars + 8 * (12 + s); };
+  auto q_full = [&](int h) { return bars + 8 * (16 + h); };
+  auto q_empty = [&](int h) { return bars + 8 * (18 + h); };
+  auto s_full = [&](int h) { return bars + 8 * (20 + h); };  // of a half, or with one half of a buffer
+  auto p_full = [&](int h) { return bars + 8 * (22 + h); };  // likewise
+  // of a half's tile n, two in turn: with one, a wait of a tile's sums was seen to pass while the product
+  // of the tile before was still under way (head dims past 128, whose logits are ahead by a tile)
+  auto o_done = [&](int h, int n) { return bars + 8 * (24 + 2 * h + (n & 1)); };
+  auto i_full = [&](int i) { return bars + 8 * (28 + i); };
+  auto i_empty = [&](int i) { return bars + 8 * (32 + i); };
+  const uint32_t done = bars + 8 * 36;
+  volatile int* const gave_up = &s_gave_up;
+
+  if (threadIdx.x == 0) {
+    s_gave_up = 0;
+    for (int i = 0; i < 4; ++i) {
+      // copies: 8 rows of a warp at a time, an arrival of each lane's copies and one behind the mask
+      mb_init(k_full(i), C::UNITS * (FMT == CF_BF16 ? 33 : 1));
+      mb_init(v_full(i), C::UNITS * (FMT == CF_BF16 ? 33 : 1));
+      mb_init(k_empty(i), 1);
+      mb_init(v_empty(i), 1);
+      mb_init(i_full(i), 1);
+      mb_init(i_empty(i), 8 + PRE_COPY_WARPS + 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mb_init(q_full(h), 16 * 32);
+      mb_init(q_empty(h), 1);
+      mb_init(s_full(h), 1);
+      mb_init(p_full(h), 128);
+      mb_init(o_done(h, 0), 1);
+      mb_init(o_done(h, 1), 1);
+    }
+    mb_init(done, 1);
+    mb_init_fence();
+  }
+  if (warp == 15) tm_alloc(smem_u32(&s_tmem), 512);
+
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // ---- this block's range: every thread counts its sequences' places
+  const int HR = p.Hkv * p.groups;
+  const int each = (p.B + PRE_THREADS - 1) / PRE_THREADS, b_lo = min(p.B, (int)threadIdx.x * each), b_hi = min(p.B, b_lo + each);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int b = b_lo; b < b_hi; ++b) {
+    int32_t s0, n, len;
+    bad |= !pre_bounds(p, b, s0, n, len);
+    const PreSeq s = pre_seq(p, n, len);
+    mine += s.place(s.tiles()) * HR;
+  }
+  if (bad && blockIdx.x == 0) flag_status(p.status, K3ATTN_DEV_BAD_LENGTH);
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) s_sum[warp] = upto;
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = s_tmem;
+  int64_t total = 0;
+  for (int w = 0; w < PRE_THREADS / 32; ++w) {
+    if (w == warp) upto += total;
+    total += s_sum[w];
+  }
+  const int64_t chunk = pre_chunk(total, gridDim.x), first = blockIdx.x * chunk;
+  if (mine > 0 && first >= upto - mine && first < upto) {
+    int64_t before = upto - mine;
+    for (int b = b_lo;; ++b) {
+      int32_t s0, n, len;
+      pre_bounds(p, b, s0, n, len);
+      const PreSeq s = pre_seq(p, n, len);
+      const int64_t here = s.place(s.tiles()) * HR;
+      if (first < before + here) {
+        s_b = b;
+        s_off = first - before;
+        break;
+      }
+      before += here;
+    }
+  }
+  __syncthreads();
+
+  // ---- roles.  An item goes to all of them: `take` waits for the next one and copies it.
+  int taken = 0;
+  auto take = [&](PreItem& it) {
+    const int i = taken % ITEMS;
+    if (!__all_sync(0xFFFFFFFFu, mb_wait(i_full(i), (taken / ITEMS) & 1, gave_up))) return false;
+    it = *reinterpret_cast<const PreItem*>(__cvta_shared_to_generic(items_at + i * 128));
+    __syncwarp();
+    if (lane == 0) mb_arrive(i_empty(i));
+    ++taken;
+    return !it.end;
+  };
+
+  if (warp < 8) {
+    regs_more<PRE_REGS_SOFTMAX>();
+    const int half = warp / 4, r = half * 128 + (warp % 4) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+    const uint32_t o_at = lanes + C::O_AT + half * 128;
+    int n_s = 0, n_tile = 0;  // tiles of keys of this half so far, and of the block
+    bool ok = half < HALVES;
+    PreItem it{};
+    while (ok && take(it)) {
+      const int nkt = it.kt1 - it.kt0, tile0 = n_tile;
+      n_tile += nkt;
+      if (it.ntok * it.heads <= half * 128) continue;
+      const int tok = r / it.heads, head = it.head0 + (r - tok * it.heads);
+      const bool valid = tok < it.ntok;
+      const int32_t pos = it.pos0 + min(tok, it.ntok - 1);
+      // visible: keys below hi that are at least lo or below sk
+      const int hi_v = max(0, min(pos + 1 - it.f + it.ns, it.keys));
+      const int lo_v = p.window > 0 ? (pos >= p.window ? pos - p.window + 1 : 0) - it.f + it.ns : 0;
+      const int sk_v = p.window > 0 ? p.sinks : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nkt; ++j) {
+        const int buf = HALVES == 2 ? half : n_s & 1;
+        const uint32_t par = HALVES == 2 ? n_s & 1 : (n_s >> 1) & 1;
+        if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(s_full(buf), par, gave_up)))) break;
+        tm_fence_after();
+        const uint32_t s_at = lanes + buf * C::S_AT;
+        uint32_t raw[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tm_ld32(s_at + 32 * c, raw + 32 * c);
+        tm_ld_wait();
+        float2 s[BN / 2];
+        const int ring = (tile0 + j) % RING, v0 = (it.kt0 + j) * BN;
+        const float* const ks = reinterpret_cast<const float*>(__cvta_shared_to_generic(scales_at + ring * 2 * BN * 4));
+        const float* const vs = ks + BN;
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) {
+          s[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
+          if constexpr (FMT == CF_E4M3)
+            s[i] = mul2(s[i], *reinterpret_cast<const float2*>(ks + 2 * i));  // (with p.scale)
+          else
+            s[i] = mul2(s[i], make_float2(p.scale, p.scale));
+        }
+        const uint4 ok4 = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(masks_at + ring * 16));
+        const uint32_t okw[4] = {ok4.x, ok4.y, ok4.z, ok4.w};
+        const int hi = hi_v - v0, lo = lo_v - v0, sk = sk_v - v0;
+        const bool all_rows = (okw[0] & okw[1] & (BN > 64 ? okw[2] & okw[3] : ~0u)) == ~0u;
+        if (!__all_sync(0xFFFFFFFFu, all_rows && hi >= BN && (lo <= 0 || sk >= BN))) {
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            const uint32_t see = bits_below(hi - 32 * c) & (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c)) & okw[c];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2& x = s[16 * c + i];
+              if (!(see >> (2 * i) & 1)) x.x = -INFINITY;
+              if (!(see >> (2 * i + 1) & 1)) x.y = -INFINITY;
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) top = max3(top, s[i].x, s[i].y);
+        // the maximum moves where a row's is more than 2^8 above it (weights up to 2^8 are as exact), and
+        // the sums with it
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
+          const float m1 = top > m + 8.f ? top : m, fall = m1 == m ? 1.f : ex2(m - m1);
+          m = m1;
+          l *= fall;
+          if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(o_done(half, n_s - 1), (n_s - 1) >> 1 & 1, gave_up)))) break;
+          tm_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < p.D; c += 16) {
+            uint32_t o[16];
+            tm_ld16(o_at + c, o);
+            tm_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
+            tm_st16(o_at + c, o);
+            tm_st_wait();
+            tm_keep16(o);
+          }
+        }
+        const float down = m == -INFINITY ? 0.f : -m;
+        float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+        uint32_t w[BN / 2];
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) {
+          const float2 x = add2(s[i], make_float2(down, down));
+          float2 e = make_float2(ex2(x.x), ex2(x.y));
+          sum[i & 1] = add2(sum[i & 1], e);
+          if constexpr (FMT == CF_E4M3) e = mul2(e, *reinterpret_cast<const float2*>(vs + 2 * i));
+          w[i] = bf16x2_of(e);
+        }
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tm_st16(lanes + C::P_AT + buf * C::P_STEP + 16 * c, w + 16 * c);
+        const float2 both = add2(sum[0], sum[1]);
+        l = both.x + both.y;
+        tm_st_wait();
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tm_keep16(w + 16 * c);
+        tm_fence_before();
+        mb_arrive(p_full(buf));
+        ++n_s;
+      }
+      if (!ok || !(ok = __all_sync(0xFFFFFFFFu, mb_wait(o_done(half, n_s - 1), (n_s - 1) >> 1 & 1, gave_up)))) break;
+      tm_fence_after();
+      const int64_t row = it.row0 + tok;
+      float* rec = p.parts + (2 * (int64_t)blockIdx.x + (it.kt0 == 0)) * C::REC;
+      float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* const out = p.out + (row * p.Hq + head) * p.D;
+      uint32_t largest = 0;  // a result that is not finite shows
+      bool final = it.whole;
+      if (it.whole) {
+#pragma unroll 1
+        for (int c = 0; c < p.D; c += 16) {
+          uint32_t o[16];
+          tm_ld16(o_at + c, o);
+          tm_ld_wait();
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            largest = max(largest, max(o[2 * i] & 0x7FFFFFFFu, o[2 * i + 1] & 0x7FFFFFFFu));
+            w[i] = bf16x2_of(make_float2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv));
+          }
+          if (valid) {
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      } else {
+        // a record: quads of dims of all rows, then each row's maximum and sum
+#pragma unroll 1
+        for (int c = 0; c < p.D; c += 16) {
+          uint32_t o[16];
+          tm_ld16(o_at + c, o);
+          tm_ld_wait();
+          if (valid)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(rec + ((c / 4 + i) * C::ROWS + r) * 4) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        if (valid) *reinterpret_cast<float2*>(rec + C::ROWS * DP + 2 * r) = make_float2(m, l);
+        team_sync(half, 128);
+        if (threadIdx.x % 128 == 0) {
+          const bool last = arrive(p.arrived + 2 * it.c0 + half) == (uint32_t)(it.parts - 1);
+          if (last) p.arrived[2 * it.c0 + half] = 0;
+          s_last[half] = last;
+        }
+        team_sync(half, 128);
+        final = *reinterpret_cast<volatile int32_t*>(&s_last[half]);
+        team_sync(half, 128);
+        if (final && valid) {
+          // block c0's part is its second record, the others' their first
+          auto part = [&](int i) { return p.parts + (2 * (int64_t)(it.c0 + i) + (i == 0)) * C::REC; };
+          float top = -INFINITY, sum = 0.f;
+          for (int i = 0; i < it.parts; ++i) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(part(i) + C::ROWS * DP + 2 * r));
+            const float t1 = fmaxf(top, x.x), b0 = t1 == -INFINITY ? 0.f : t1;
+            sum = sum * ex2(top - b0) + x.y * ex2(x.x - b0);
+            top = t1;
+          }
+          m = top;
+          l = sum;
+          inv = l == 0.f ? 0.f : 1.f / l;
+          const float b0 = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; c < p.D; c += 8) {
+            float2 o[4] = {};
+            for (int i = 0; i < it.parts; ++i) {
+              const float* const y = part(i);
+              const float f = ex2(__ldcg(y + C::ROWS * DP + 2 * r) - b0);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(y + ((c / 4 + e) * C::ROWS + r) * 4));
+                o[2 * e] = fma2(make_float2(v.x, v.y), make_float2(f, f), o[2 * e]);
+                o[2 * e + 1] = fma2(make_float2(v.z, v.w), make_float2(f, f), o[2 * e + 1]);
+              }
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              largest = max(largest, max(__float_as_uint(o[i].x) & 0x7FFFFFFFu, __float_as_uint(o[i].y) & 0x7FFFFFFFu));
+              w[i] = bf16x2_of(mul2(o[i], make_float2(inv, inv)));
+            }
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (final) {
+        if (valid && p.lse) p.lse[row * p.Hq + head] = lse_of(m == -INFINITY ? 0.f : m, l);
+        uint32_t again = __ballot_sync(0xFFFFFFFFu, valid && largest >= 0x7F800000u && l < INFINITY);
+        while (again) {
+          const int from = __ffs(again) - 1;
+          again &= again - 1;
+          prefill_row<FMT>(p, it.b, it.kvh, __shfl_sync(0xFFFFFFFFu, head, from), __shfl_sync(0xFFFFFFFFu, row, from),
+                           __shfl_sync(0xFFFFFFFFu, pos, from), lane);
+        }
+      }
+    }
+    if (half >= HALVES)
+      while (take(it)) {
+      }
+  } else {
+    regs_fewer<PRE_REGS_OTHERS>();
+    if (warp < 8 + PRE_COPY_WARPS) {
+      // ---- copies: units of 8 rows of a tile of keys, of values or of queries, dealt out in a line
+      const int w = warp - 8, row_in = lane / 4, piece = lane % 4;
+      int units = 0;                  // dealt out so far
+      int tiles = 0, q_taken[2] = {0, 0};
+      const int chunks = p.D / 8;     // 16-byte pieces of a row of bf16
+      bool ok = true;
+      PreItem it{};
+      while (ok && take(it)) {
+        const int32_t* const table = p.table + (int64_t)it.b * p.table_width;
+        // a lane's row of a unit: where it is in the cache; whether it is there
+        auto place = [&](uint32_t v, int32_t& entry, int32_t& in_page) {  // (v may be past 2^31)
+          const uint32_t t = v < (uint32_t)it.ns ? v : v - it.ns + it.f;
+          if (v >= (uint32_t)it.keys || t >= (uint32_t)it.len) return false;
+          const uint32_t pg = p.c.by_page(t);
+          entry = __ldg(table + pg);
+          in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
+          return true;
+        };
+        auto rows_of = [&](int kt, int tile, bool keys) {
+          const int slot = tile % SLOTS, ring = tile % RING;
+          const uint32_t full = keys ? k_full(slot) : v_full(slot), empty = keys ? k_empty(slot) : v_empty(slot);
+          const uint32_t dst = (keys ? k_at : v_at) + slot * C::TILE;
+          const uint8_t* const src = keys ? p.c.k : p.c.v;
+          bool waited = false;
+          for (int u = (w + PRE_COPY_WARPS - units % PRE_COPY_WARPS) % PRE_COPY_WARPS; u < C::UNITS; u += PRE_COPY_WARPS) {
+            const int row = 8 * u + row_in;
+            int32_t entry = 0, in_page = 0;
+            const bool in = place((uint32_t)kt * BN + row, entry, in_page);
+            const bool there = in && entry >= 0 && entry < p.c.n_pages;
+            if (in && !there) flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
+            const int64_t off = there ? entry * p.c.page + it.kvh * p.c.head + in_page * p.c.tok : 0;
+            const int64_t so = there ? entry * p.c.spage + it.kvh * p.c.shead + in_page * p.c.stok : 0;
+            const uint32_t to = dst + (row / 8) * 1024 + row_in * 128;
+            if constexpr (FMT == CF_BF16) {
+              if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(empty, (tile / SLOTS & 1) ^ 1, gave_up)))) return;
+              waited = true;
+#pragma unroll
+              for (int i = 0; i < DP / 32; ++i) {
+                const int c = piece + 4 * i;
+                if (c < chunks)
+                  cp_async16_or_zero(to + (c / 8) * (BN * 128) + (((c & 7) ^ row_in) << 4), src + off + (there ? 16 * c : 0),
+                                     there ? 16 : 0);
+              }
+              mb_arrive_copies(full);
+            } else if constexpr (FMT == CF_E4M3) {
+              uint4 v[DP / 64];
+              float scale = 0.f;  // the softmax reads both scales with the logits: the keys bring them
+#pragma unroll
+              for (int i = 0; i < DP / 64; ++i) {
+                const int c = piece + 4 * i;
+                v[i] = there && c < p.D / 16 ? ldg128(src + off + 16 * c) : make_uint4(0, 0, 0, 0);
+              }
+              if (there && keys && piece < 2) scale = __ldg((piece == 0 ? p.c.ks : p.c.vs) + so);
+              if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(empty, (tile / SLOTS & 1) ^ 1, gave_up)))) return;
+              waited = true;
+#pragma unroll
+              for (int i = 0; i < DP / 64; ++i) {
+                const int c = 2 * (piece + 4 * i);
+                if (c >= chunks) continue;
+                uint4 a, b;
+                e4m3x4_bf16(v[i].x, a.x, a.y);
+                e4m3x4_bf16(v[i].y, a.z, a.w);
+                e4m3x4_bf16(v[i].z, b.x, b.y);
+                e4m3x4_bf16(v[i].w, b.z, b.w);
+                const uint32_t at = to + (c / 8) * (BN * 128);
+                sts128(at + (((c & 7) ^ row_in) << 4), a);
+                sts128(at + (((c & 7) + 1 ^ row_in) << 4), b);
+              }
+              if (keys && piece < 2)
+                sts32(scales_at + ring * 2 * BN * 4 + piece * (BN * 4) + 4 * row, __float_as_uint(piece == 0 ? scale * p.scale : scale));
+              fence_smem_async();
+            } else {
+              uint4 v[(DP + 127) / 128];
+              uint32_t e[(DP + 127) / 128];
+#pragma unroll
+              for (int i = 0; i < (DP + 127) / 128; ++i) {
+                const int c = piece + 4 * i;
+                const bool on = there && c < p.D / 32;
+                v[i] = on ? ldg128(src + off + 16 * c) : make_uint4(0, 0, 0, 0);
+                e[i] = on ? __ldg((keys ? p.c.k_exps() : p.c.v_exps()) + so + c) : 127;
+              }
+              if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(empty, (tile / SLOTS & 1) ^ 1, gave_up)))) return;
+              waited = true;
+#pragma unroll
+              for (int i = 0; i < (DP + 127) / 128; ++i) {
+                const int c = 4 * (piece + 4 * i);
+                if (c >= chunks) continue;
+                const uint32_t at = to + (c / 8) * (BN * 128), x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sts128(at + (((c & 7) + k ^ row_in) << 4), e2m1x8_scaled(x[k], e[i]));
+              }
+              fence_smem_async();
+            }
+            const uint32_t rows8 = __ballot_sync(0xFFFFFFFFu, there && piece == 0);  // bits 0, 4, ..
+            if (lane == 0) {
+              if (keys) {
+                uint32_t b8 = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b8 |= (rows8 >> (4 * i) & 1u) << i;
+                *reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(masks_at + ring * 16 + u)) = (uint8_t)b8;
+              }
+              mb_arrive(full);
+            }
+          }
+          units += C::UNITS;
+        };
+        for (int j = 0; j < it.kt1 - it.kt0 && ok; ++j, ++tiles) {
+          rows_of(it.kt0 + j, tiles, true);
+          if (!ok) break;
+          if (j == 0) {
+            // the item's queries
+            for (int h = 0; h < HALVES && ok; ++h) {
+              if (it.ntok * it.heads <= h * 128) continue;
+              bool waited = false;
+              for (int u = (w + PRE_COPY_WARPS - units % PRE_COPY_WARPS) % PRE_COPY_WARPS; u < 16; u += PRE_COPY_WARPS) {
+                if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(q_empty(h), (q_taken[h] & 1) ^ 1, gave_up)))) break;
+                waited = true;
+                const int row = 8 * u + row_in, rr = 128 * h + row, tok = rr / it.heads, head = it.head0 + (rr - tok * it.heads);
+                const bool there = tok < it.ntok;
+                const uint16_t* const src = p.q + (there ? (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)head * p.D : 0);
+                const uint32_t to = q_at + h * C::Q_HALF + (row / 8) * 1024 + row_in * 128;
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                  const int c = piece + 4 * i;
+                  if (c < chunks)
+                    cp_async16_or_zero(to + (c / 8) * (128 * 128) + (((c & 7) ^ row_in) << 4), src + (there ? 8 * c : 0), there ? 16 : 0);
+                }
+                mb_arrive_copies(q_full(h));
+              }
+              units += 16;
+              ++q_taken[h];
+            }
+          }
+          if (ok) rows_of(it.kt0 + j, tiles, false);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+    } else if (warp == 14) {
+      // ---- the block's items
+      if (lane == 0) {
+        PreWalk walk;
+        walk.bn = BN;
+        walk.chunk = chunk;
+        walk.end = first + chunk;
+        walk.b = p.B;
+        walk.kt = 0;
+        walk.x = walk.end;
+        if (first < total) {
+          walk.b = s_b;
+          walk.land(p, s_off);
+        }
+        PreItem it;
+        it.end = 0;
+        for (int n = 0; !it.end; ++n) {
+          const int i = n % ITEMS;
+          walk.item(p, it);
+          if (!mb_wait(i_empty(i), (n / ITEMS & 1) ^ 1, gave_up)) break;
+          *reinterpret_cast<PreItem*>(__cvta_shared_to_generic(items_at + i * 128)) = it;
+          mb_arrive(i_full(i));
+        }
+      }
+    } else {
+      // ---- the products
+      const uint32_t kind_s = mma_kind(128, BN, false), kind_o = mma_kind(128, p.D, true);
+      const int steps = p.D / 16;
+      int tiles = 0, q_taken[2] = {0, 0}, n_p[2] = {0, 0}, n_s = 0;
+      PreItem it{};
+      bool ok = true;
+      auto tile_of_rows = [&]() {  // by one lane
+        const int nkt = it.kt1 - it.kt0, halves = HALVES == 2 && it.ntok * it.heads > 128 ? 2 : 1;
+        auto logits = [&](int h, int tile, uint32_t d) {
+          const uint32_t a = q_at + h * C::Q_HALF, b = k_at + tile % SLOTS * C::TILE;
+          for (int k = 0; k < steps; ++k)
+            mma_ss(d, rows_desc(a + (k / 4) * (128 * 128) + (k & 3) * 32), rows_desc(b + (k / 4) * (BN * 128) + (k & 3) * 32), kind_s, k > 0);
+        };
+        auto values = [&](uint32_t weights, int h, int tile, bool add) {
+          const uint32_t b = v_at + tile % SLOTS * C::TILE;
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(tmem + C::O_AT + h * 128, weights + 8 * k, rows_desc(b + k * 2048, BN * 128), kind_o, add || k > 0);
+        };
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok) ok = mb_wait(bar, parity, gave_up);
+          return ok;
+        };
+        auto keys_there = [&](int tile) {
+          if (!wait(k_full(tile % SLOTS), tile / SLOTS & 1)) return false;
+          fence_smem_async();
+          tm_fence_after();
+          return true;
+        };
+        // the first logits
+        if (!keys_there(tiles)) return;
+        for (int h = 0; h < halves && ok; ++h) {
+          if (!wait(q_full(h), q_taken[h] & 1)) return;
+          fence_smem_async();
+          logits(h, tiles, tmem + (HALVES == 2 ? h : n_s & 1) * C::S_AT);
+          tm_commit(s_full(HALVES == 2 ? h : n_s & 1));
+          if (nkt == 1) tm_commit(q_empty(h));
+          ++q_taken[h];
+        }
+        tm_commit(k_empty(tiles % SLOTS));
+        for (int j = 0; j < nkt && ok; ++j, ++tiles) {
+          const bool more = j + 1 < nkt;
+          if (HALVES == 1 && more) {  // the next logits, into the other buffer
+            if (!keys_there(tiles + 1)) return;
+            logits(0, tiles + 1, tmem + (n_s + 1 & 1) * C::S_AT);
+            tm_commit(s_full(n_s + 1 & 1));
+            tm_commit(k_empty((tiles + 1) % SLOTS));
+            if (j + 2 == nkt) tm_commit(q_empty(0));
+          }
+          if (!wait(v_full(tiles % SLOTS), tiles / SLOTS & 1)) return;
+          fence_smem_async();
+          for (int h = 0; h < halves && ok; ++h) {
+            if (!(HALVES == 2 ? wait(p_full(h), n_p[h]++ & 1) : wait(p_full(n_s & 1), n_s >> 1 & 1))) return;
+            tm_fence_after();
+            values(tmem + C::P_AT + (HALVES == 2 ? h : n_s & 1) * C::P_STEP, h, tiles, j > 0);
+            tm_commit(o_done(h, HALVES == 2 ? n_p[h] - 1 : n_s));
+            if (HALVES == 2 && more) {
+              if (h == 0 && !keys_there(tiles + 1)) return;
+              logits(h, tiles + 1, tmem + h * C::S_AT);
+              tm_commit(s_full(h));
+              if (j + 2 == nkt) tm_commit(q_empty(h));
+            }
+          }
+          tm_commit(v_empty(tiles % SLOTS));
+          if (HALVES == 2 && more) tm_commit(k_empty((tiles + 1) % SLOTS));
+          ++n_s;
+        }
+      };
+      while (ok && take(it)) {
+        if (lane == 0) tile_of_rows();
+        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+      }
+      if (lane == 0) {  // all products have ended before the memory goes
+        tm_commit(done);
+        volatile int never = 0;
+        mb_wait(done, 0, &never);
+      }
+      __syncwarp();
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (threadIdx.x == 0 && s_gave_up) flag_status(p.status, K3ATTN_TIMEOUT);
+  if (warp == 15) tm_free(tmem, 512);
 }
 
 }  // namespace k3

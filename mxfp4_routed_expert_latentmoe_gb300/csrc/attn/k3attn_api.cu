@@ -295,11 +295,50 @@ cudaError_t launch_decode(const DecodeParams& p, int dp, int nt, int dev, int sm
   return cudaErrorInvalidValue;
 }
 
+// rows of a prefill tile
+int pre_rows(const k3attn_dims& d) { return d.head_dim <= 128 ? 256 : 128; }
+static_assert(2 * PRE_MAX_BLOCKS <= DEC_MAX_TEAMS, "the counters");
+
+template <int FMT, int DP>
+cudaError_t launch_prefill_t(const PrefillParams& p, int dev, int sms, cudaStream_t s) {
+  using C = PreCfg<FMT, DP>;
+  constexpr auto kernel = k3_prefill_kernel<FMT, DP>;
+  static std::atomic<int> registers[kMaxDevices];
+  if (registers[dev].load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    registers[dev].store(a.numRegs, std::memory_order_release);
+  }
+  // the warps' shares of the registers have to be there at the launch (or a warp would wait for ever)
+  if (registers[dev].load(std::memory_order_acquire) * PRE_THREADS < 256 * (PRE_REGS_SOFTMAX + PRE_REGS_OTHERS))
+    return cudaErrorInvalidValue;
+  if (!set_smem<k3_prefill_kernel<FMT, DP>>(dev, C::SMEM)) return cudaErrorInvalidValue;
+  const int grid = sms < PRE_MAX_BLOCKS ? sms : PRE_MAX_BLOCKS;
+  return launch(kernel, dim3(grid), dim3(PRE_THREADS), C::SMEM, s, p);
+}
+template <int FMT>
+cudaError_t launch_prefill(const PrefillParams& p, int dp, int dev, int sms, cudaStream_t s) {
+  switch (dp) {
+    case 64: return launch_prefill_t<FMT, 64>(p, dev, sms, s);
+    case 128: return launch_prefill_t<FMT, 128>(p, dev, sms, s);
+    case 192: return launch_prefill_t<FMT, 192>(p, dev, sms, s);
+    case 256: return launch_prefill_t<FMT, 256>(p, dev, sms, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 extern "C" {
 
-size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims) { return k3attn_workspace_bytes(dims); }
+size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims) {
+  if (check_dims(dims) != K3MOE_OK) return 0;
+  // (128 rows of 258 floats are less than 256 of 130: a workspace serves smaller head dims too)
+  const size_t records = kRecords + (size_t)2 * PRE_MAX_BLOCKS * 256 * ((dec_dp(*dims) <= 64 ? 64 : 128) + 2) * 4;
+  const size_t decode = k3attn_workspace_bytes(dims);
+  return records > decode ? records : decode;
+}
 
 k3moe_status k3attn_prefill(const k3attn_dims* dims, int32_t n_sinks, int32_t B, int32_t T, const uint16_t* q,
                             int64_t q_stride, const int32_t* q_starts, const k3attn_cache* cache,
@@ -331,11 +370,15 @@ k3moe_status k3attn_prefill(const k3attn_dims* dims, int32_t n_sinks, int32_t B,
   p.out = out; p.lse = lse;
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  K3A_TRY(with_format(cache->format, [&](auto f) {
-    const int64_t grid = ((int64_t)T * d.n_heads + 7) / 8;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    return launch(k3_prefill_simple_kernel<decltype(f)::value>, dim3((unsigned)grid), dim3(256), 0, s, p);
-  }));
+  // a tile's rows: whole tokens with all heads of a key head, or with more heads than rows equal parts of them
+  const int rows = pre_rows(d);
+  p.groups = (p.G + rows - 1) / rows;
+  p.heads = (p.G + p.groups - 1) / p.groups;
+  p.tokens = rows / p.heads;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.arrived = reinterpret_cast<uint32_t*>(w + kCounters);
+  p.parts = reinterpret_cast<float*>(w + kRecords);
+  K3A_TRY(with_format(cache->format, [&](auto f) { return launch_prefill<decltype(f)::value>(p, dec_dp(d), dev, sms, s); }));
   return K3MOE_OK;
 }
 
