@@ -41,10 +41,10 @@ struct PrefillParams {
 // What a tile's start counts as, the fewest keys of a block, tiles of keys up to which a tile is not cut.
 constexpr int PRE_START = 256, PRE_LEAST = 512, PRE_WHOLE = 2;
 constexpr int PRE_MAX_BLOCKS = 192;
-constexpr int PRE_THREADS = 512, PRE_COPY_WARPS = 6;
-// Registers of the softmax warps and of the others: 256 threads each, 65536 in all, which the block
-// is launched with
-constexpr int PRE_REGS_SOFTMAX = 192, PRE_REGS_OTHERS = 64;
+constexpr int PRE_COPY_WARPS = 6, PRE_THREADS = 256 + 32 * PRE_COPY_WARPS + 64;
+// Registers of a thread: at the launch, then of the 256 of the softmax and of the others
+constexpr int PRE_REGS = 128, PRE_REGS_SOFTMAX = 192, PRE_REGS_OTHERS = 64;
+static_assert(256 * PRE_REGS_SOFTMAX + (PRE_THREADS - 256) * PRE_REGS_OTHERS <= PRE_THREADS * PRE_REGS, "a warp would wait for ever");
 
 // ---------------------------------------------------------------------------- the order of the work
 K3_HD int64_t pre_min(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -279,20 +279,29 @@ struct PreCfg {
   static constexpr int BN = DP <= 128 ? 128 : 64;  // keys of a tile
   static constexpr int Q_HALF = 128 * DP * 2;
   static constexpr int TILE = BN * DP * 2;  // bytes of a tile's keys, or values
-  static constexpr int ROOM = 227 * 1024 - 1024 - HALVES * Q_HALF - 2048 - (FMT == CF_E4M3 ? 8192 : 0);
-  static constexpr int SLOTS = ROOM / (2 * TILE) > 4 ? 4 : ROOM / (2 * TILE);  // tiles of keys, and of values, in flight
-  static constexpr int UNITS = BN / 8;  // a warp's copy: 8 rows
-  // masks and scales of 8 tiles: those of a tile are read until its weights are formed, and the copies are
+  // A copying warp has its rows of each tile, 8 at a time (a lane a quarter of the 16-byte pieces of one):
+  // up to EIGHTS times.  Rows in codes come through a ring of each warp's own: what a lane copies it turns
+  // into bf16 itself, RAWS tiles of keys or values later.  There: pieces and words of scales, by lanes.
+  static constexpr int EIGHTS = (BN / 8 + PRE_COPY_WARPS - 1) / PRE_COPY_WARPS;
+  static constexpr int PIECES = FMT == CF_BF16 ? 0 : FMT == CF_E4M3 ? DP / 64 : (DP + 127) / 128;
+  static constexpr int RAW8 = FMT == CF_BF16 ? 0 : PIECES * 512 + (FMT == CF_E4M3 ? 128 : PIECES * 128), RAW = EIGHTS * RAW8;
+  // masks and scales of RING tiles: those of a tile are read until its weights are formed, and the copies are
   // SLOTS tiles and one ahead of that (two with one half)
-  static constexpr int RING = 8;
+  static constexpr int RING = FMT == CF_BF16 || DP <= 64 ? 8 : 4;
   static constexpr int SCALES = FMT == CF_E4M3 ? RING * 2 * BN * 4 : 0;
-  // barriers (512 bytes), items, masks, scales
-  static constexpr int SMEM = 1024 + HALVES * Q_HALF + 2 * SLOTS * TILE + 512 + 4 * 128 + RING * 16 + 64 + SCALES;
+  static constexpr int OTHERS = 1024 + HALVES * Q_HALF + 512 + 4 * 128 + RING * 16 + 64 + SCALES;  // barriers, items, masks
+  static constexpr int ROOM = 227 * 1024 - OTHERS;
+  // tiles of keys, and of values, as bf16 (codes: no more than leaves each warp's ring two and more)
+  static constexpr int SLOTS = FMT == CF_BF16 ? (ROOM / (2 * TILE) > 4 ? 4 : ROOM / (2 * TILE)) : DP <= 64 ? 3 : 2;
+  static constexpr int V_SLOTS = FMT == CF_E4M3 && (DP == 128 || DP == 256) ? 1 : SLOTS;
+  static constexpr int RAWS_FIT = FMT == CF_BF16 ? 0 : (ROOM - (SLOTS + V_SLOTS) * TILE) / (PRE_COPY_WARPS * (RAW + 8));
+  static constexpr int RAWS = RAWS_FIT > 6 ? 6 : RAWS_FIT;
+  static constexpr int SMEM = OTHERS + (SLOTS + V_SLOTS) * TILE + PRE_COPY_WARPS * RAWS * (RAW + 8);
   static constexpr int REC = ROWS * (DP + 2);  // floats of a record
   // columns of tensor memory: a half's logits (with one half two buffers), its weights over them (with one
   // half behind the sums), its sums
   static constexpr uint32_t S_AT = BN, O_AT = DP <= 128 ? 256 : 128, P_AT = DP <= 128 ? 0 : 384, P_STEP = DP <= 128 ? BN : BN / 2;
-  static_assert(SLOTS >= 2 && SLOTS + 2 <= RING && SMEM <= 227 * 1024 && sizeof(PreItem) <= 128, "does not fit");
+  static_assert(SLOTS >= 2 && SLOTS + 2 <= RING && (FMT == CF_BF16 || RAWS >= 2) && SMEM <= 227 * 1024 && sizeof(PreItem) <= 128, "does not fit");
 };
 
 K3_DEVI float max3(float a, float b, float c) {
@@ -342,7 +351,7 @@ K3_DEVI void sts128(uint32_t a, uint4 v) { *reinterpret_cast<uint4*>(__cvta_shar
 template <int FMT, int DP>
 __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const PrefillParams p) {
   using C = PreCfg<FMT, DP>;
-  constexpr int BN = C::BN, SLOTS = C::SLOTS, HALVES = C::HALVES, ITEMS = 4, RING = C::RING;
+  constexpr int BN = C::BN, SLOTS = C::SLOTS, V_SLOTS = C::V_SLOTS, HALVES = C::HALVES, ITEMS = 4, RING = C::RING;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
@@ -350,8 +359,9 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
   __shared__ int32_t s_b, s_last[2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_at = base, k_at = q_at + HALVES * C::Q_HALF, v_at = k_at + SLOTS * C::TILE, bars = v_at + SLOTS * C::TILE;
-  const uint32_t items_at = bars + 512, masks_at = items_at + ITEMS * 128, scales_at = (masks_at + RING * 16 + 63u) & ~63u;
+  const uint32_t q_at = base, k_at = q_at + HALVES * C::Q_HALF, v_at = k_at + SLOTS * C::TILE, bars = v_at + V_SLOTS * C::TILE;
+  const uint32_t items_at = bars + 512, masks_at = items_at + ITEMS * 128, scales_at = (masks_at + RING * 16 + 63u) & ~63u,
+                 raw_at = scales_at + C::SCALES;
   auto k_full = [&](int s) { return bars + 8 * s; };
   auto k_empty = [&](int s) { return bars + 8 * (4 + s); };
   auto v_full = [&](int s) { return bars + 8 * (8 + s); };
@@ -360,37 +370,37 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
   auto q_empty = [&](int h) { return bars + 8 * (18 + h); };
   auto s_full = [&](int h) { return bars + 8 * (20 + h); };  // of a half, or with one half of a buffer
   auto p_full = [&](int h) { return bars + 8 * (22 + h); };  // likewise
-  // of a half's tile n, two in turn: with one, a wait of a tile's sums was seen to pass while the product
-  // of the tile before was still under way (head dims past 128, whose logits are ahead by a tile)
+  // of a half's tile n, two in turn: a wait that earlier tiles have left out cannot take one phase for another
   auto o_done = [&](int h, int n) { return bars + 8 * (24 + 2 * h + (n & 1)); };
   auto i_full = [&](int i) { return bars + 8 * (28 + i); };
   auto i_empty = [&](int i) { return bars + 8 * (32 + i); };
-  const uint32_t done = bars + 8 * 36;
+  auto p_rest = [&](int h) { return bars + 8 * (36 + h); };  // the second half of a tile's weights
+  const uint32_t done = bars + 8 * 38;
   volatile int* const gave_up = &s_gave_up;
 
   if (threadIdx.x == 0) {
     s_gave_up = 0;
     for (int i = 0; i < 4; ++i) {
-      // copies: 8 rows of a warp at a time, an arrival of each lane's copies and one behind the mask
-      mb_init(k_full(i), C::UNITS * (FMT == CF_BF16 ? 33 : 1));
-      mb_init(v_full(i), C::UNITS * (FMT == CF_BF16 ? 33 : 1));
+      mb_init(k_full(i), PRE_COPY_WARPS);
+      mb_init(v_full(i), PRE_COPY_WARPS);
       mb_init(k_empty(i), 1);
       mb_init(v_empty(i), 1);
       mb_init(i_full(i), 1);
       mb_init(i_empty(i), 8 + PRE_COPY_WARPS + 1);
     }
     for (int h = 0; h < 2; ++h) {
-      mb_init(q_full(h), 16 * 32);
+      mb_init(q_full(h), PRE_COPY_WARPS);
       mb_init(q_empty(h), 1);
       mb_init(s_full(h), 1);
       mb_init(p_full(h), 128);
+      mb_init(p_rest(h), 128);
       mb_init(o_done(h, 0), 1);
       mb_init(o_done(h, 1), 1);
     }
     mb_init(done, 1);
     mb_init_fence();
   }
-  if (warp == 15) tm_alloc(smem_u32(&s_tmem), 512);
+  if (warp == PRE_THREADS / 32 - 1) tm_alloc(smem_u32(&s_tmem), 512);
 
   grid_dep_wait();
   grid_dep_launch();
@@ -459,6 +469,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
     const uint32_t o_at = lanes + C::O_AT + half * 128;
     int n_s = 0, n_tile = 0;  // tiles of keys of this half so far, and of the block
+    const float unit = FMT == CF_E4M3 ? 1.f : p.scale;  // (E4M3: in the keys' scales)
     bool ok = half < HALVES;
     PreItem it{};
     while (ok && take(it)) {
@@ -472,6 +483,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
       const int hi_v = max(0, min(pos + 1 - it.f + it.ns, it.keys));
       const int lo_v = p.window > 0 ? (pos >= p.window ? pos - p.window + 1 : 0) - it.f + it.ns : 0;
       const int sk_v = p.window > 0 ? p.sinks : 0;
+      // the maximum, in units of 2^unit; the sum of weights
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nkt; ++j) {
         const int buf = HALVES == 2 ? half : n_s & 1;
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
         uint32_t raw[BN];
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) tm_ld32(s_at + 32 * c, raw + 32 * c);
-        tm_ld_wait();
+        tm_ld_wait<BN>(raw);
         float2 s[BN / 2];
         const int ring = (tile0 + j) % RING, v0 = (it.kt0 + j) * BN;
         const float* const ks = reinterpret_cast<const float*>(__cvta_shared_to_generic(scales_at + ring * 2 * BN * 4));
@@ -490,10 +502,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
 #pragma unroll
         for (int i = 0; i < BN / 2; ++i) {
           s[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
-          if constexpr (FMT == CF_E4M3)
-            s[i] = mul2(s[i], *reinterpret_cast<const float2*>(ks + 2 * i));  // (with p.scale)
-          else
-            s[i] = mul2(s[i], make_float2(p.scale, p.scale));
+          if constexpr (FMT == CF_E4M3) s[i] = mul2(s[i], *reinterpret_cast<const float2*>(ks + 2 * i));  // (with p.scale)
         }
         const uint4 ok4 = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(masks_at + ring * 16));
         const uint32_t okw[4] = {ok4.x, ok4.y, ok4.z, ok4.w};
@@ -511,15 +520,16 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
             }
           }
         }
-        float top = -INFINITY;
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < BN / 2; ++i) top = max3(top, s[i].x, s[i].y);
+        for (int i = 0; i < BN / 2; ++i) tops[i & 3] = max3(tops[i & 3], s[i].x, s[i].y);
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         // the maximum moves where a row's is more than 2^8 above it (weights up to 2^8 are as exact), and
         // the sums with it
         if (j == 0) {
           m = top;
-        } else if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
-          const float m1 = top > m + 8.f ? top : m, fall = m1 == m ? 1.f : ex2(m - m1);
+        } else if (__any_sync(0xFFFFFFFFu, (top - m) * unit > 8.f)) {
+          const float m1 = (top - m) * unit > 8.f ? top : m, fall = m1 == m ? 1.f : ex2((m - m1) * unit);
           m = m1;
           l *= fall;
           if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(o_done(half, n_s - 1), (n_s - 1) >> 1 & 1, gave_up)))) break;
@@ -528,7 +538,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
           for (int c = 0; c < p.D; c += 16) {
             uint32_t o[16];
             tm_ld16(o_at + c, o);
-            tm_ld_wait();
+            tm_ld_wait<16>(o);
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
             tm_st16(o_at + c, o);
@@ -537,32 +547,42 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
           }
         }
         const float down = m == -INFINITY ? 0.f : -m;
-        float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
-        uint32_t w[BN / 2];
+        float2 sum[4] = {};
+        const uint32_t p_at = lanes + C::P_AT + buf * C::P_STEP;
 #pragma unroll
-        for (int i = 0; i < BN / 2; ++i) {
-          const float2 x = add2(s[i], make_float2(down, down));
-          float2 e = make_float2(ex2(x.x), ex2(x.y));
-          sum[i & 1] = add2(sum[i & 1], e);
-          if constexpr (FMT == CF_E4M3) e = mul2(e, *reinterpret_cast<const float2*>(vs + 2 * i));
-          w[i] = bf16x2_of(e);
+        for (int part = 0; part < 2; ++part) {  // the product begins with the first half's weights
+          uint32_t w[BN / 4];
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int i = part * (BN / 4) + 16 * c + k;
+              // (the difference first: with the products first, sums and products become one, which does not round
+              // the product, and beside a large maximum nothing is left of a weight)
+              float2 x = add2(s[i], make_float2(down, down));
+              if (FMT != CF_E4M3) x = mul2(x, make_float2(unit, unit));
+              float2 e = make_float2(ex2(x.x), ex2(x.y));
+              sum[k & 3] = add2(sum[k & 3], e);
+              if constexpr (FMT == CF_E4M3) e = mul2(e, *reinterpret_cast<const float2*>(vs + 2 * i));
+              w[16 * c + k] = bf16x2_of(e);
+            }
+            tm_st16(p_at + part * (BN / 4) + 16 * c, w + 16 * c);
+          }
+          tm_st_wait();
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) tm_keep16(w + 16 * c);
+          tm_fence_before();
+          mb_arrive(part ? p_rest(buf) : p_full(buf));
         }
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tm_st16(lanes + C::P_AT + buf * C::P_STEP + 16 * c, w + 16 * c);
-        const float2 both = add2(sum[0], sum[1]);
-        l = both.x + both.y;
-        tm_st_wait();
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tm_keep16(w + 16 * c);
-        tm_fence_before();
-        mb_arrive(p_full(buf));
+        const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += both.x + both.y;
         ++n_s;
       }
       if (!ok || !(ok = __all_sync(0xFFFFFFFFu, mb_wait(o_done(half, n_s - 1), (n_s - 1) >> 1 & 1, gave_up)))) break;
       tm_fence_after();
       const int64_t row = it.row0 + tok;
       float* rec = p.parts + (2 * (int64_t)blockIdx.x + (it.kt0 == 0)) * C::REC;
-      float inv = l == 0.f ? 0.f : 1.f / l;
+      float inv = l == 0.f ? 0.f : 1.f / l, base = m == -INFINITY ? 0.f : m * unit;
       uint16_t* const out = p.out + (row * p.Hq + head) * p.D;
       uint32_t largest = 0;  // a result that is not finite shows
       bool final = it.whole;
@@ -571,7 +591,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
         for (int c = 0; c < p.D; c += 16) {
           uint32_t o[16];
           tm_ld16(o_at + c, o);
-          tm_ld_wait();
+          tm_ld_wait<16>(o);
           uint32_t w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -589,13 +609,13 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
         for (int c = 0; c < p.D; c += 16) {
           uint32_t o[16];
           tm_ld16(o_at + c, o);
-          tm_ld_wait();
+          tm_ld_wait<16>(o);
           if (valid)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(rec + ((c / 4 + i) * C::ROWS + r) * 4) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
-        if (valid) *reinterpret_cast<float2*>(rec + C::ROWS * DP + 2 * r) = make_float2(m, l);
+        if (valid) *reinterpret_cast<float2*>(rec + C::ROWS * DP + 2 * r) = make_float2(m * unit, l);
         team_sync(half, 128);
         if (threadIdx.x % 128 == 0) {
           const bool last = arrive(p.arrived + 2 * it.c0 + half) == (uint32_t)(it.parts - 1);
@@ -615,16 +635,15 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
             sum = sum * ex2(top - b0) + x.y * ex2(x.x - b0);
             top = t1;
           }
-          m = top;
           l = sum;
           inv = l == 0.f ? 0.f : 1.f / l;
-          const float b0 = m == -INFINITY ? 0.f : m;
+          base = top == -INFINITY ? 0.f : top;
 #pragma unroll 1
           for (int c = 0; c < p.D; c += 8) {
             float2 o[4] = {};
             for (int i = 0; i < it.parts; ++i) {
               const float* const y = part(i);
-              const float f = ex2(__ldcg(y + C::ROWS * DP + 2 * r) - b0);
+              const float f = ex2(__ldcg(y + C::ROWS * DP + 2 * r) - base);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(y + ((c / 4 + e) * C::ROWS + r) * 4));
@@ -643,7 +662,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
         }
       }
       if (final) {
-        if (valid && p.lse) p.lse[row * p.Hq + head] = lse_of(m == -INFINITY ? 0.f : m, l);
+        if (valid && p.lse) p.lse[row * p.Hq + head] = lse_of(base, l);
         uint32_t again = __ballot_sync(0xFFFFFFFFu, valid && largest >= 0x7F800000u && l < INFINITY);
         while (again) {
           const int from = __ffs(again) - 1;
@@ -659,145 +678,259 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
   } else {
     regs_fewer<PRE_REGS_OTHERS>();
     if (warp < 8 + PRE_COPY_WARPS) {
-      // ---- copies: units of 8 rows of a tile of keys, of values or of queries, dealt out in a line
+      // ---- copies
       const int w = warp - 8, row_in = lane / 4, piece = lane % 4;
-      int units = 0;                  // dealt out so far
+      const int chunks = p.D / 8;  // 16-byte pieces of a row of bf16
       int tiles = 0, q_taken[2] = {0, 0};
-      const int chunks = p.D / 8;     // 16-byte pieces of a row of bf16
       bool ok = true;
       PreItem it{};
-      while (ok && take(it)) {
-        const int32_t* const table = p.table + (int64_t)it.b * p.table_width;
-        // a lane's row of a unit: where it is in the cache; whether it is there
-        auto place = [&](uint32_t v, int32_t& entry, int32_t& in_page) {  // (v may be past 2^31)
-          const uint32_t t = v < (uint32_t)it.ns ? v : v - it.ns + it.f;
-          if (v >= (uint32_t)it.keys || t >= (uint32_t)it.len) return false;
-          const uint32_t pg = p.c.by_page(t);
-          entry = __ldg(table + pg);
-          in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
-          return true;
-        };
-        auto rows_of = [&](int kt, int tile, bool keys) {
-          const int slot = tile % SLOTS, ring = tile % RING;
-          const uint32_t full = keys ? k_full(slot) : v_full(slot), empty = keys ? k_empty(slot) : v_empty(slot);
-          const uint32_t dst = (keys ? k_at : v_at) + slot * C::TILE;
-          const uint8_t* const src = keys ? p.c.k : p.c.v;
-          bool waited = false;
-          for (int u = (w + PRE_COPY_WARPS - units % PRE_COPY_WARPS) % PRE_COPY_WARPS; u < C::UNITS; u += PRE_COPY_WARPS) {
-            const int row = 8 * u + row_in;
-            int32_t entry = 0, in_page = 0;
-            const bool in = place((uint32_t)kt * BN + row, entry, in_page);
-            const bool there = in && entry >= 0 && entry < p.c.n_pages;
-            if (in && !there) flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
-            const int64_t off = there ? entry * p.c.page + it.kvh * p.c.head + in_page * p.c.tok : 0;
-            const int64_t so = there ? entry * p.c.spage + it.kvh * p.c.shead + in_page * p.c.stok : 0;
-            const uint32_t to = dst + (row / 8) * 1024 + row_in * 128;
-            if constexpr (FMT == CF_BF16) {
-              if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(empty, (tile / SLOTS & 1) ^ 1, gave_up)))) return;
-              waited = true;
-#pragma unroll
-              for (int i = 0; i < DP / 32; ++i) {
-                const int c = piece + 4 * i;
-                if (c < chunks)
-                  cp_async16_or_zero(to + (c / 8) * (BN * 128) + (((c & 7) ^ row_in) << 4), src + off + (there ? 16 * c : 0),
-                                     there ? 16 : 0);
-              }
-              mb_arrive_copies(full);
-            } else if constexpr (FMT == CF_E4M3) {
-              uint4 v[DP / 64];
-              float scale = 0.f;  // the softmax reads both scales with the logits: the keys bring them
-#pragma unroll
-              for (int i = 0; i < DP / 64; ++i) {
-                const int c = piece + 4 * i;
-                v[i] = there && c < p.D / 16 ? ldg128(src + off + 16 * c) : make_uint4(0, 0, 0, 0);
-              }
-              if (there && keys && piece < 2) scale = __ldg((piece == 0 ? p.c.ks : p.c.vs) + so);
-              if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(empty, (tile / SLOTS & 1) ^ 1, gave_up)))) return;
-              waited = true;
-#pragma unroll
-              for (int i = 0; i < DP / 64; ++i) {
-                const int c = 2 * (piece + 4 * i);
-                if (c >= chunks) continue;
-                uint4 a, b;
-                e4m3x4_bf16(v[i].x, a.x, a.y);
-                e4m3x4_bf16(v[i].y, a.z, a.w);
-                e4m3x4_bf16(v[i].z, b.x, b.y);
-                e4m3x4_bf16(v[i].w, b.z, b.w);
-                const uint32_t at = to + (c / 8) * (BN * 128);
-                sts128(at + (((c & 7) ^ row_in) << 4), a);
-                sts128(at + (((c & 7) + 1 ^ row_in) << 4), b);
-              }
-              if (keys && piece < 2)
-                sts32(scales_at + ring * 2 * BN * 4 + piece * (BN * 4) + 4 * row, __float_as_uint(piece == 0 ? scale * p.scale : scale));
-              fence_smem_async();
-            } else {
-              uint4 v[(DP + 127) / 128];
-              uint32_t e[(DP + 127) / 128];
-#pragma unroll
-              for (int i = 0; i < (DP + 127) / 128; ++i) {
-                const int c = piece + 4 * i;
-                const bool on = there && c < p.D / 32;
-                v[i] = on ? ldg128(src + off + 16 * c) : make_uint4(0, 0, 0, 0);
-                e[i] = on ? __ldg((keys ? p.c.k_exps() : p.c.v_exps()) + so + c) : 127;
-              }
-              if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(empty, (tile / SLOTS & 1) ^ 1, gave_up)))) return;
-              waited = true;
-#pragma unroll
-              for (int i = 0; i < (DP + 127) / 128; ++i) {
-                const int c = 4 * (piece + 4 * i);
-                if (c >= chunks) continue;
-                const uint32_t at = to + (c / 8) * (BN * 128), x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sts128(at + (((c & 7) + k ^ row_in) << 4), e2m1x8_scaled(x[k], e[i]));
-              }
-              fence_smem_async();
-            }
-            const uint32_t rows8 = __ballot_sync(0xFFFFFFFFu, there && piece == 0);  // bits 0, 4, ..
-            if (lane == 0) {
-              if (keys) {
-                uint32_t b8 = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) b8 |= (rows8 >> (4 * i) & 1u) << i;
-                *reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(masks_at + ring * 16 + u)) = (uint8_t)b8;
-              }
-              mb_arrive(full);
-            }
-          }
-          units += C::UNITS;
-        };
-        for (int j = 0; j < it.kt1 - it.kt0 && ok; ++j, ++tiles) {
-          rows_of(it.kt0 + j, tiles, true);
-          if (!ok) break;
-          if (j == 0) {
-            // the item's queries
-            for (int h = 0; h < HALVES && ok; ++h) {
-              if (it.ntok * it.heads <= h * 128) continue;
-              bool waited = false;
-              for (int u = (w + PRE_COPY_WARPS - units % PRE_COPY_WARPS) % PRE_COPY_WARPS; u < 16; u += PRE_COPY_WARPS) {
-                if (!waited && !(ok = __all_sync(0xFFFFFFFFu, mb_wait(q_empty(h), (q_taken[h] & 1) ^ 1, gave_up)))) break;
-                waited = true;
-                const int row = 8 * u + row_in, rr = 128 * h + row, tok = rr / it.heads, head = it.head0 + (rr - tok * it.heads);
-                const bool there = tok < it.ntok;
-                const uint16_t* const src = p.q + (there ? (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)head * p.D : 0);
-                const uint32_t to = q_at + h * C::Q_HALF + (row / 8) * 1024 + row_in * 128;
-#pragma unroll
-                for (int i = 0; i < DP / 32; ++i) {
-                  const int c = piece + 4 * i;
-                  if (c < chunks)
-                    cp_async16_or_zero(to + (c / 8) * (128 * 128) + (((c & 7) ^ row_in) << 4), src + (there ? 8 * c : 0), there ? 16 : 0);
-                }
-                mb_arrive_copies(q_full(h));
-              }
-              units += 16;
-              ++q_taken[h];
-            }
-          }
-          if (ok) rows_of(it.kt0 + j, tiles, false);
+      // Copies on the way, oldest first: the barriers that wait for them.  A copy is announced when it has
+      // landed and a fence of the thread that made it has made it visible to the tensor core, at the latest
+      // before the warp waits for anything.
+      uint32_t late[4] = {0, 0, 0, 0};
+      int n_late = 0;
+      auto landed = [&]() {
+        if (n_late == 1)
+          cp_async_wait<0>();
+        else if (n_late == 2)
+          cp_async_wait<1>();
+        else if (n_late == 3)
+          cp_async_wait<2>();
+        else
+          cp_async_wait<3>();
+        fence_smem_async();
+        __syncwarp();
+        if (lane == 0) mb_arrive(late[0]);
+        late[0] = late[1];
+        late[1] = late[2];
+        late[2] = late[3];
+        --n_late;
+      };
+      auto on_the_way = [&](uint32_t bar) {
+        cp_async_commit();
+        if (n_late == 0) late[0] = bar;
+        if (n_late == 1) late[1] = bar;
+        if (n_late == 2) late[2] = bar;
+        if (n_late == 3) late[3] = bar;
+        ++n_late;
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (n_late > 0) {
+          if (n_late < 4 && __all_sync(0xFFFFFFFFu, mb_try(bar, parity))) return true;
+          while (n_late > 0) landed();
         }
+        return (bool)__all_sync(0xFFFFFFFFu, mb_wait(bar, parity, gave_up));
+      };
+      // a piece's place in eight rows of a tile
+      auto piece_at = [&](int c, int block) { return row_in * 128 + (c / 8) * block + (((c & 7) ^ row_in) << 4); };
+      // a row of a tile or of the queries, bf16, its pieces 4 lanes apart
+      auto copy = [&](const uint8_t* from, bool there, uint32_t to, int block) {
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+          const int c = piece + 4 * i;
+          if (c < chunks) cp_async16_or_zero(to + piece_at(c, block), from + (there ? 16 * c : 0), there ? 16 : 0);
+        }
+      };
+      // A warp's eights of `all`: the first `more` warps have one more than the others; of the values the
+      // last ones (so that tiles whose eights the warps do not divide are even over keys and values).
+      auto first_of = [&](int all, bool values) {
+        const int least = all / PRE_COPY_WARPS, more = all - least * PRE_COPY_WARPS;
+        return least * w + (values ? max(0, w - (PRE_COPY_WARPS - more)) : min(w, more));
+      };
+      auto count_of = [&](int all, bool values) {
+        const int least = all / PRE_COPY_WARPS, more = all - least * PRE_COPY_WARPS;
+        return least + ((values ? w >= PRE_COPY_WARPS - more : w < more) ? 1 : 0);
+      };
+      const int k_first = first_of(BN / 8, false), k_count = count_of(BN / 8, false);
+      const int v_first = first_of(BN / 8, true), v_count = count_of(BN / 8, true);
+      // the warp's rows of the queries of half h
+      auto queries = [&](const PreItem& x, int h, int taken_before) {
+        if (!wait(q_empty(h), (taken_before & 1) ^ 1)) return false;
+        const int q_first = first_of(16, false), q_count = count_of(16, false);
+#pragma unroll 1
+        for (int g = q_first; g < q_first + q_count; ++g) {
+          const int rr = 128 * h + 8 * g + row_in, tok = rr / x.heads, head = x.head0 + (rr - tok * x.heads);
+          const bool there = tok < x.ntok;
+          const uint16_t* const src = p.q + (there ? (int64_t)(x.row0 + tok) * p.q_stride + (int64_t)head * p.D : 0);
+          copy(reinterpret_cast<const uint8_t*>(src), there, q_at + h * C::Q_HALF + g * 1024, 128 * 128);
+        }
+        on_the_way(q_full(h));
+        return true;
+      };
+      // the warp's rows of the keys or values of tile kt, one a lane: page (-1: there is no such row) and place
+      // in it
+      int32_t entry, in_page;
+      uint32_t rows;  // those that are there
+      auto look_up = [&](int kt, bool values) {
+        entry = -1;
+        in_page = 0;
+        // (v may be past 2^31)
+        const uint32_t v = (uint32_t)kt * BN + 8 * (values ? v_first : k_first) + lane, t = v < (uint32_t)it.ns ? v : v - it.ns + it.f;
+        if (lane < 8 * (values ? v_count : k_count) && v < (uint32_t)it.keys && t < (uint32_t)it.len) {
+          const uint32_t pg = p.c.by_page(t);
+          in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
+          entry = __ldg(p.table + (int64_t)it.b * p.table_width + pg);
+          if (entry < 0 || entry >= p.c.n_pages) {
+            flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
+            entry = -1;
+          }
+        }
+        rows = __ballot_sync(0xFFFFFFFFu, entry >= 0);
+      };
+      auto set_mask = [&](int tile, uint32_t x) {  // (for all lanes to see after __syncwarp)
+        if (lane < k_count)
+          *reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(masks_at + tile % RING * 16 + k_first + lane)) = (uint8_t)(x >> (8 * lane));
+      };
+      if constexpr (FMT == CF_BF16) {
+        auto rows_to = [&](const uint8_t* from, uint32_t tile_at, int first, int count) {
+#pragma unroll
+          for (int g = 0; g < C::EIGHTS; ++g) {
+            if (g >= count) break;
+            const int32_t e = __shfl_sync(0xFFFFFFFFu, entry, 8 * g + row_in), at = __shfl_sync(0xFFFFFFFFu, in_page, 8 * g + row_in);
+            const bool there = e >= 0;
+            copy(from + (there ? it.kvh * p.c.head + e * p.c.page + at * p.c.tok : 0), there, tile_at + (first + g) * 1024, BN * 128);
+          }
+        };
+        while (ok) {
+          if (n_late > 0 && !__all_sync(0xFFFFFFFFu, mb_try(i_full(taken % ITEMS), (taken / ITEMS) & 1)))
+            while (n_late > 0) landed();
+          if (!take(it)) break;
+#pragma unroll 1
+          for (int j = it.kt0; j < it.kt1; ++j, ++tiles) {
+            look_up(j, false);
+            const int ks = tiles % SLOTS, vs = tiles % V_SLOTS;
+            if (!(ok = wait(k_empty(ks), (tiles / SLOTS & 1) ^ 1))) break;
+            rows_to(p.c.k, k_at + ks * C::TILE, k_first, k_count);
+            set_mask(tiles, rows);
+            on_the_way(k_full(ks));
+            look_up(j, true);
+            if (j == it.kt0)
+#pragma unroll 1
+              for (int h = 0; h < HALVES && ok && it.ntok * it.heads > h * 128; ++h) ok = queries(it, h, q_taken[h]++);
+            if (!ok || !(ok = wait(v_empty(vs), (tiles / V_SLOTS & 1) ^ 1))) break;
+            rows_to(p.c.v, v_at + vs * C::TILE, v_first, v_count);
+            on_the_way(v_full(vs));
+          }
+        }
+        while (n_late > 0) landed();
+      } else {
+        // Rows in codes: begun (their copies are on the way into the ring) and finished (in place as bf16), in
+        // the order of the products: an item's first keys, its queries, their values, the next keys ..
+        static_assert(C::RAW % 16 == 0, "copies of 16 bytes");
+        constexpr int RAWS = C::RAWS;
+        const uint32_t raws = raw_at + w * (RAWS * C::RAW), notes = raw_at + PRE_COPY_WARPS * RAWS * C::RAW + w * (RAWS * 8);
+        const uint32_t own16 = raws + lane * 16, own4 = raws + C::PIECES * 512 + lane * 4;  // a lane's pieces and words
+        constexpr int KEYS = 0, QUERIES = 1, VALUES = 2, NEW_ITEM = 3, NO_MORE = 4;
+        int state = NEW_ITEM, j = 0, front = 0, back = 0, slot_front = 0, slot_back = 0;
+#pragma unroll 1
+        while (ok) {
+          if (front - back == RAWS || (state == NO_MORE && front != back) || state == QUERIES) {
+            // ---- finish the oldest; before an item's queries all of it that was begun
+            if (state == QUERIES && front == back) {
+              for (int h = 0; h < HALVES && ok && it.ntok * it.heads > h * 128; ++h) ok = queries(it, h, q_taken[h]++);
+              while (n_late > 0) landed();
+              state = VALUES;
+              continue;
+            }
+            if (state == QUERIES || state == NO_MORE)
+              cp_async_wait<0>();
+            else
+              cp_async_wait<RAWS - 1>();
+            const uint2 note = lds64(notes + 8 * (back % RAWS));
+            const int at = slot_back, tile = (int)note.x;
+            ++back;
+            slot_back = slot_back + C::RAW == RAWS * C::RAW ? 0 : slot_back + C::RAW;
+            const bool keys = !(note.y >> 31);
+            const int slot = keys ? tile % SLOTS : tile % V_SLOTS;
+            const uint32_t full = keys ? k_full(slot) : v_full(slot);
+            if (!(ok = wait(keys ? k_empty(slot) : v_empty(slot), ((keys ? tile / SLOTS : tile / V_SLOTS) & 1) ^ 1))) break;
+            const int first = keys ? k_first : v_first, count = keys ? k_count : v_count;
+            const uint32_t to0 = (keys ? k_at : v_at) + slot * C::TILE + first * 1024;
+#pragma unroll
+            for (int g = 0; g < C::EIGHTS; ++g) {
+              if (g >= count) break;
+              const uint32_t to = to0 + g * 1024, from16 = own16 + at + g * C::RAW8, from4 = own4 + at + g * C::RAW8;
+#pragma unroll
+              for (int k = 0; k < C::PIECES; ++k) {
+                const uint4 v = lds128(from16 + k * 512);
+                if constexpr (FMT == CF_E4M3) {
+                  const int c = 2 * (piece + 4 * k);
+                  if (c >= chunks) continue;
+                  uint4 a, b;
+                  e4m3x4_bf16(v.x, a.x, a.y);
+                  e4m3x4_bf16(v.y, a.z, a.w);
+                  e4m3x4_bf16(v.z, b.x, b.y);
+                  e4m3x4_bf16(v.w, b.z, b.w);
+                  sts128(to + piece_at(c, BN * 128), a);
+                  sts128(to + piece_at(c + 1, BN * 128), b);
+                } else {
+                  const int c = 4 * (piece + 4 * k);
+                  if (c >= chunks) continue;
+                  const uint32_t e = lds32(from4 + k * 128) >> (8 * piece) & 255, x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) sts128(to + piece_at(c + q, BN * 128), e2m1x8_scaled(x[q], e));
+                }
+              }
+              if (FMT == CF_E4M3 && keys && piece < 2) {
+                // (the softmax reads both scales with the logits)
+                const float scale = lds_f32(from4);
+                sts32(scales_at + tile % RING * 2 * BN * 4 + piece * (BN * 4) + 4 * (8 * (first + g) + row_in),
+                      __float_as_uint(piece == 0 ? scale * p.scale : scale));
+              }
+            }
+            if (keys) set_mask(tile, note.y);
+            fence_smem_async();
+            __syncwarp();
+            if (lane == 0) mb_arrive(full);
+            continue;
+          }
+          if (state == NO_MORE) break;
+          if (state == NEW_ITEM) {
+            if (!take(it)) {
+              ok = !*gave_up;
+              state = NO_MORE;
+              continue;
+            }
+            j = it.kt0;
+            state = KEYS;
+          }
+          // ---- begin a tile's keys or values
+          const bool keys = state == KEYS;
+          look_up(j, !keys);
+          const uint8_t *const from = keys ? p.c.k : p.c.v, *const exps = keys ? p.c.k_exps() : p.c.v_exps();
+#pragma unroll
+          for (int g = 0; g < C::EIGHTS; ++g) {
+            if (g >= (keys ? k_count : v_count)) break;
+            const int32_t e = __shfl_sync(0xFFFFFFFFu, entry, 8 * g + row_in), at = __shfl_sync(0xFFFFFFFFu, in_page, 8 * g + row_in);
+            const bool there = e >= 0;
+            const uint8_t* const src = from + (there ? it.kvh * p.c.head + e * p.c.page + at * p.c.tok : 0);
+            const int64_t so = there ? it.kvh * p.c.shead + e * p.c.spage + at * p.c.stok : 0;
+            const int to = slot_front + g * C::RAW8;
+#pragma unroll
+            for (int k = 0; k < C::PIECES; ++k) {
+              const int c = piece + 4 * k;
+              const uint32_t bytes = there && c < p.D / (FMT == CF_E4M3 ? 16 : 32) ? 16 : 0;
+              cp_async16_or_zero(own16 + to + k * 512, src + (bytes ? 16 * c : 0), bytes);
+              if (FMT == CF_MXFP4) cp_async4_or_zero(own4 + to + k * 128, exps + (bytes ? so + 4 * k : 0), bytes / 4);
+            }
+            if (FMT == CF_E4M3 && keys && piece < 2) cp_async4_or_zero(own4 + to, (piece == 0 ? p.c.ks : p.c.vs) + so, there ? 4 : 0);
+          }
+          if (lane == 0) sts64(notes + 8 * (front % RAWS), (uint32_t)tiles, keys ? rows : 0x80000000u);
+          __syncwarp();
+          cp_async_commit();
+          ++front;
+          slot_front = slot_front + C::RAW == RAWS * C::RAW ? 0 : slot_front + C::RAW;
+          if (keys) {
+            state = j == it.kt0 ? QUERIES : VALUES;
+          } else {
+            ++tiles;
+            state = ++j < it.kt1 ? KEYS : NEW_ITEM;
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
       }
-      cp_async_commit();
-      cp_async_wait<0>();
-    } else if (warp == 14) {
+    } else if (warp == 8 + PRE_COPY_WARPS) {
       // ---- the block's items
       if (lane == 0) {
         PreWalk walk;
@@ -822,83 +955,95 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
         }
       }
     } else {
-      // ---- the products
+      // ---- the products.  All lanes go through this together, so that descriptors and addresses are the
+      // warp's; one of them issues (lane 0 alone going through all of it issued wrong ones when the compiler
+      // kept them in the warp's registers).
       const uint32_t kind_s = mma_kind(128, BN, false), kind_o = mma_kind(128, p.D, true);
       const int steps = p.D / 16;
+      const bool issues = elect_one();
       int tiles = 0, q_taken[2] = {0, 0}, n_p[2] = {0, 0}, n_s = 0;
       PreItem it{};
       bool ok = true;
-      auto tile_of_rows = [&]() {  // by one lane
-        const int nkt = it.kt1 - it.kt0, halves = HALVES == 2 && it.ntok * it.heads > 128 ? 2 : 1;
-        auto logits = [&](int h, int tile, uint32_t d) {
-          const uint32_t a = q_at + h * C::Q_HALF, b = k_at + tile % SLOTS * C::TILE;
-          for (int k = 0; k < steps; ++k)
-            mma_ss(d, rows_desc(a + (k / 4) * (128 * 128) + (k & 3) * 32), rows_desc(b + (k / 4) * (BN * 128) + (k & 3) * 32), kind_s, k > 0);
-        };
-        auto values = [&](uint32_t weights, int h, int tile, bool add) {
-          const uint32_t b = v_at + tile % SLOTS * C::TILE;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xFFFFFFFFu, mb_wait(bar, parity, gave_up));
+        return ok;
+      };
+      auto logits = [&](int h, int tile, int buf) {
+        const uint64_t a = rows_desc(q_at + h * C::Q_HALF), b = rows_desc(k_at + tile % SLOTS * C::TILE);
+        const uint32_t d = tmem + buf * C::S_AT;
+        if (issues) {
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_ts(tmem + C::O_AT + h * 128, weights + 8 * k, rows_desc(b + k * 2048, BN * 128), kind_o, add || k > 0);
-        };
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (ok) ok = mb_wait(bar, parity, gave_up);
-          return ok;
-        };
-        auto keys_there = [&](int tile) {
-          if (!wait(k_full(tile % SLOTS), tile / SLOTS & 1)) return false;
-          fence_smem_async();
-          tm_fence_after();
-          return true;
-        };
+          for (int k = 0; k < DP / 16; ++k)
+            if (k < steps) mma_ss(d, a + ((k / 4) * 1024 + (k & 3) * 2), b + ((k / 4) * (BN * 8) + (k & 3) * 2), kind_s, k > 0);
+          tm_commit(s_full(buf));
+        }
+      };
+      // the product of half of a tile's weights
+      auto values = [&](int buf, int h, int tile, bool add, int part) {
+        const uint64_t b = rows_desc(v_at + tile % V_SLOTS * C::TILE, BN * 128);
+        const uint32_t d = tmem + C::O_AT + h * 128, a = tmem + C::P_AT + buf * C::P_STEP;
+        if (issues)
+#pragma unroll
+          for (int i = 0; i < BN / 32; ++i) {
+            const int k = part * (BN / 32) + i;
+            mma_ts(d, a + 8 * k, b + k * 128, kind_o, add || k > 0);
+          }
+      };
+      auto commit = [&](uint32_t bar) {
+        if (issues) tm_commit(bar);
+      };
+      auto keys_there = [&](int tile) {
+        if (!wait(k_full(tile % SLOTS), tile / SLOTS & 1)) return false;
+        tm_fence_after();
+        return true;
+      };
+      auto rows_of_item = [&]() {
+        const int nkt = it.kt1 - it.kt0, halves = HALVES == 2 && it.ntok * it.heads > 128 ? 2 : 1;
         // the first logits
         if (!keys_there(tiles)) return;
-        for (int h = 0; h < halves && ok; ++h) {
+        for (int h = 0; h < halves; ++h) {
           if (!wait(q_full(h), q_taken[h] & 1)) return;
-          fence_smem_async();
-          logits(h, tiles, tmem + (HALVES == 2 ? h : n_s & 1) * C::S_AT);
-          tm_commit(s_full(HALVES == 2 ? h : n_s & 1));
-          if (nkt == 1) tm_commit(q_empty(h));
+          tm_fence_after();
+          logits(h, tiles, HALVES == 2 ? h : n_s & 1);
+          if (nkt == 1) commit(q_empty(h));
           ++q_taken[h];
         }
-        tm_commit(k_empty(tiles % SLOTS));
-        for (int j = 0; j < nkt && ok; ++j, ++tiles) {
+        commit(k_empty(tiles % SLOTS));
+        for (int j = 0; j < nkt; ++j, ++tiles) {
           const bool more = j + 1 < nkt;
           if (HALVES == 1 && more) {  // the next logits, into the other buffer
             if (!keys_there(tiles + 1)) return;
-            logits(0, tiles + 1, tmem + (n_s + 1 & 1) * C::S_AT);
-            tm_commit(s_full(n_s + 1 & 1));
-            tm_commit(k_empty((tiles + 1) % SLOTS));
-            if (j + 2 == nkt) tm_commit(q_empty(0));
+            logits(0, tiles + 1, (n_s + 1) & 1);
+            commit(k_empty((tiles + 1) % SLOTS));
+            if (j + 2 == nkt) commit(q_empty(0));
           }
-          if (!wait(v_full(tiles % SLOTS), tiles / SLOTS & 1)) return;
-          fence_smem_async();
-          for (int h = 0; h < halves && ok; ++h) {
-            if (!(HALVES == 2 ? wait(p_full(h), n_p[h]++ & 1) : wait(p_full(n_s & 1), n_s >> 1 & 1))) return;
+          if (!wait(v_full(tiles % V_SLOTS), tiles / V_SLOTS & 1)) return;
+          for (int h = 0; h < halves; ++h) {
+            const int buf = HALVES == 2 ? h : n_s & 1;
+            const uint32_t parity = HALVES == 2 ? n_p[h] & 1 : n_s >> 1 & 1;
+            if (!wait(p_full(buf), parity)) return;
             tm_fence_after();
-            values(tmem + C::P_AT + (HALVES == 2 ? h : n_s & 1) * C::P_STEP, h, tiles, j > 0);
-            tm_commit(o_done(h, HALVES == 2 ? n_p[h] - 1 : n_s));
+            values(buf, h, tiles, j > 0, 0);
+            if (!wait(p_rest(buf), parity)) return;
+            tm_fence_after();
+            values(buf, h, tiles, j > 0, 1);
+            commit(o_done(h, HALVES == 2 ? n_p[h] : n_s));
+            ++n_p[h];
             if (HALVES == 2 && more) {
               if (h == 0 && !keys_there(tiles + 1)) return;
-              logits(h, tiles + 1, tmem + h * C::S_AT);
-              tm_commit(s_full(h));
-              if (j + 2 == nkt) tm_commit(q_empty(h));
+              logits(h, tiles + 1, h);
+              if (j + 2 == nkt) commit(q_empty(h));
             }
           }
-          tm_commit(v_empty(tiles % SLOTS));
-          if (HALVES == 2 && more) tm_commit(k_empty((tiles + 1) % SLOTS));
+          commit(v_empty(tiles % V_SLOTS));
+          if (HALVES == 2 && more) commit(k_empty((tiles + 1) % SLOTS));
           ++n_s;
         }
       };
-      while (ok && take(it)) {
-        if (lane == 0) tile_of_rows();
-        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
-      }
-      if (lane == 0) {  // all products have ended before the memory goes
-        tm_commit(done);
-        volatile int never = 0;
-        mb_wait(done, 0, &never);
-      }
+      while (ok && take(it)) rows_of_item();
+      commit(done);  // all products have ended before the memory goes
+      volatile int never = 0;
+      mb_wait(done, 0, &never);
       __syncwarp();
     }
   }
@@ -906,7 +1051,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
   __syncthreads();
   tm_fence_after();
   if (threadIdx.x == 0 && s_gave_up) flag_status(p.status, K3ATTN_TIMEOUT);
-  if (warp == 15) tm_free(tmem, 512);
+  if (warp == PRE_THREADS / 32 - 1) tm_free(tmem, 512);
 }
 
 }  // namespace k3

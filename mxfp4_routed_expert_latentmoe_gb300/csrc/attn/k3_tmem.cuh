@@ -13,10 +13,6 @@ K3_DEVI void mb_init_fence() { asm volatile("fence.mbarrier_init.release.cluster
 K3_DEVI void mb_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// an arrival once all of this thread's cp.async copies so far have landed (counted from the start)
-K3_DEVI void mb_arrive_copies(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
-}
 K3_DEVI bool mb_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -54,6 +50,12 @@ K3_DEVI void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync
 K3_DEVI void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 // shared-memory writes of the generic proxy before reads of the tensor core
 K3_DEVI void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+// one lane of a warp whose lanes are all here
+K3_DEVI bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(is));
+  return is != 0;
+}
 K3_DEVI void tm_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
@@ -83,6 +85,7 @@ K3_DEVI uint64_t rows_desc(uint32_t addr, uint32_t block = 16) {
          (uint64_t)2 << 61;
 }
 #define K3_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define K3_U4(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
 #define K3_W4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
 // a lane's 32 or 16 columns of its row
 K3_DEVI void tm_ld32(uint32_t a, uint32_t* r) {
@@ -101,7 +104,15 @@ K3_DEVI void tm_ld16(uint32_t a, uint32_t* r) {
       : "r"(a)
       : "memory");
 }
-K3_DEVI void tm_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// waits for the loads before it; N registers that they fill (nothing of theirs may be used in front of
+// the wait, which the compiler sees by the registers alone)
+template <int N>
+K3_DEVI void tm_ld_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile("" : K3_U4(r, i), K3_U4(r, i + 4), K3_U4(r, i + 8), K3_U4(r, i + 12));
+}
 K3_DEVI void tm_st16(uint32_t a, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -115,6 +126,7 @@ K3_DEVI void tm_keep16(const uint32_t* r) {
   asm volatile("" ::K3_W4(r, 0), K3_W4(r, 4), K3_W4(r, 8), K3_W4(r, 12));
 }
 #undef K3_R4
+#undef K3_U4
 #undef K3_W4
 
 template <int N>

@@ -311,7 +311,7 @@ cudaError_t launch_prefill_t(const PrefillParams& p, int dev, int sms, cudaStrea
     registers[dev].store(a.numRegs, std::memory_order_release);
   }
   // the warps' shares of the registers have to be there at the launch (or a warp would wait for ever)
-  if (registers[dev].load(std::memory_order_acquire) * PRE_THREADS < 256 * (PRE_REGS_SOFTMAX + PRE_REGS_OTHERS))
+  if (registers[dev].load(std::memory_order_acquire) < PRE_REGS)
     return cudaErrorInvalidValue;
   if (!set_smem<k3_prefill_kernel<FMT, DP>>(dev, C::SMEM)) return cudaErrorInvalidValue;
   const int grid = sms < PRE_MAX_BLOCKS ? sms : PRE_MAX_BLOCKS;
