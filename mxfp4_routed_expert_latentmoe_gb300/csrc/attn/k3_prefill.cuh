@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
       mb_init(q_full(h), PRE_COPY_WARPS);
       mb_init(q_empty(h), 1);
       mb_init(s_full(h), 1);
-      mb_init(p_full(h), 128);
-      mb_init(p_rest(h), 128);
+      mb_init(p_full(h), 4);
+      mb_init(p_rest(h), 4);
       mb_init(o_done(h, 0), 1);
       mb_init(o_done(h, 1), 1);
     }
@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
 #pragma unroll
           for (int c = 0; c < BN / 64; ++c) tm_keep16(w + 16 * c);
           tm_fence_before();
-          mb_arrive(part ? p_rest(buf) : p_full(buf));
+          __syncwarp();
+          if (lane == 0) mb_arrive(part ? p_rest(buf) : p_full(buf));
         }
         const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += both.x + both.y;
@@ -757,23 +758,27 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
         on_the_way(q_full(h));
         return true;
       };
-      // the warp's rows of the keys or values of tile kt, one a lane: page (-1: there is no such row) and place
-      // in it
-      int32_t entry, in_page;
-      uint32_t rows;  // those that are there
-      auto look_up = [&](int kt, bool values) {
-        entry = -1;
-        in_page = 0;
+      // The warp's rows of the keys or values of a tile, one a lane: page and place in it (-1: there is no such
+      // row).  The page table is read a step ahead of the rows' use.
+      int32_t entry = -1, in_page = 0, entry_next = -1, in_page_next = 0;
+      uint32_t rows = 0;  // those that are there
+      auto look_up = [&](int kt, bool values) {  // the next ones
+        entry_next = -1;
+        in_page_next = -1;
         // (v may be past 2^31)
         const uint32_t v = (uint32_t)kt * BN + 8 * (values ? v_first : k_first) + lane, t = v < (uint32_t)it.ns ? v : v - it.ns + it.f;
         if (lane < 8 * (values ? v_count : k_count) && v < (uint32_t)it.keys && t < (uint32_t)it.len) {
           const uint32_t pg = p.c.by_page(t);
-          in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
-          entry = __ldg(p.table + (int64_t)it.b * p.table_width + pg);
-          if (entry < 0 || entry >= p.c.n_pages) {
-            flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
-            entry = -1;
-          }
+          in_page_next = (int32_t)(t - pg * (uint32_t)p.c.page_size);
+          entry_next = __ldg(p.table + (int64_t)it.b * p.table_width + pg);
+        }
+      };
+      auto use_next = [&]() {
+        entry = entry_next;
+        in_page = in_page_next;
+        if (in_page >= 0 && (entry < 0 || entry >= p.c.n_pages)) {
+          flag_status(p.status, K3ATTN_DEV_BAD_PAGE);
+          entry = -1;
         }
         rows = __ballot_sync(0xFFFFFFFFu, entry >= 0);
       };
@@ -795,18 +800,21 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
           if (n_late > 0 && !__all_sync(0xFFFFFFFFu, mb_try(i_full(taken % ITEMS), (taken / ITEMS) & 1)))
             while (n_late > 0) landed();
           if (!take(it)) break;
+          look_up(it.kt0, false);
 #pragma unroll 1
           for (int j = it.kt0; j < it.kt1; ++j, ++tiles) {
-            look_up(j, false);
+            use_next();
+            look_up(j, true);
             const int ks = tiles % SLOTS, vs = tiles % V_SLOTS;
             if (!(ok = wait(k_empty(ks), (tiles / SLOTS & 1) ^ 1))) break;
             rows_to(p.c.k, k_at + ks * C::TILE, k_first, k_count);
             set_mask(tiles, rows);
             on_the_way(k_full(ks));
-            look_up(j, true);
             if (j == it.kt0)
 #pragma unroll 1
               for (int h = 0; h < HALVES && ok && it.ntok * it.heads > h * 128; ++h) ok = queries(it, h, q_taken[h]++);
+            use_next();
+            if (j + 1 < it.kt1) look_up(j + 1, false);
             if (!ok || !(ok = wait(v_empty(vs), (tiles / V_SLOTS & 1) ^ 1))) break;
             rows_to(p.c.v, v_at + vs * C::TILE, v_first, v_count);
             on_the_way(v_full(vs));
@@ -893,10 +901,12 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) k3_prefill_kernel(const Prefil
             }
             j = it.kt0;
             state = KEYS;
+            look_up(j, false);
           }
           // ---- begin a tile's keys or values
           const bool keys = state == KEYS;
-          look_up(j, !keys);
+          use_next();
+          if (keys || j + 1 < it.kt1) look_up(keys ? j : j + 1, keys);
           const uint8_t *const from = keys ? p.c.k : p.c.v, *const exps = keys ? p.c.k_exps() : p.c.v_exps();
 #pragma unroll
           for (int g = 0; g < C::EIGHTS; ++g) {
