@@ -299,8 +299,40 @@ cudaError_t launch_decode(const DecodeParams& p, int dp, int nt, int dev, int sm
 int pre_rows(const k3attn_dims& d) { return d.head_dim <= 128 ? 256 : 128; }
 static_assert(2 * PRE_MAX_BLOCKS <= DEC_MAX_TEAMS, "the counters");
 
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link)
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static std::atomic<EncodeTiled> fn{nullptr};
+  EncodeTiled f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* x = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &x, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
+    f = reinterpret_cast<EncodeTiled>(x);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+// Boxes of 64 dims of 8 tokens of a page of a bf16 cache.  false: they cannot be described (or are not worth
+// it: fewer than 64 dims, pages of less than 8 tokens), and rows are copied one by one.
+bool map_rows(CUtensorMap* m, void* rows, const CacheView& c, int Hkv, int D) {
+  const EncodeTiled f = encode_tiled();
+  if (!f || D < 64 || c.page_size < 8) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)Hkv, (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.tok, (cuuint64_t)c.head, (cuuint64_t)c.page};
+  const cuuint32_t box[4] = {64, 8, 1, 1}, each[4] = {1, 1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, rows, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int FMT, int DP>
-cudaError_t launch_prefill_t(const PrefillParams& p, int dev, int sms, cudaStream_t s) {
+cudaError_t launch_prefill_t(const PrefillParams& p, const PrefillMaps& maps, int dev, int sms, cudaStream_t s) {
   using C = PreCfg<FMT, DP>;
   constexpr auto kernel = k3_prefill_kernel<FMT, DP>;
   static std::atomic<int> registers[kMaxDevices];
@@ -315,15 +347,17 @@ cudaError_t launch_prefill_t(const PrefillParams& p, int dev, int sms, cudaStrea
     return cudaErrorInvalidValue;
   if (!set_smem<k3_prefill_kernel<FMT, DP>>(dev, C::SMEM)) return cudaErrorInvalidValue;
   const int grid = sms < PRE_MAX_BLOCKS ? sms : PRE_MAX_BLOCKS;
-  return launch(kernel, dim3(grid), dim3(PRE_THREADS), C::SMEM, s, p);
+  return launch(kernel, dim3(grid), dim3(PRE_THREADS), C::SMEM, s, maps, p);
 }
 template <int FMT>
-cudaError_t launch_prefill(const PrefillParams& p, int dp, int dev, int sms, cudaStream_t s) {
+cudaError_t launch_prefill(PrefillParams p, int dp, int dev, int sms, cudaStream_t s) {
+  PrefillMaps maps{};
+  if (FMT == CF_BF16) p.boxes = map_rows(&maps.k, p.c.k, p.c, p.Hkv, p.D) && map_rows(&maps.v, p.c.v, p.c, p.Hkv, p.D);
   switch (dp) {
-    case 64: return launch_prefill_t<FMT, 64>(p, dev, sms, s);
-    case 128: return launch_prefill_t<FMT, 128>(p, dev, sms, s);
-    case 192: return launch_prefill_t<FMT, 192>(p, dev, sms, s);
-    case 256: return launch_prefill_t<FMT, 256>(p, dev, sms, s);
+    case 64: return launch_prefill_t<FMT, 64>(p, maps, dev, sms, s);
+    case 128: return launch_prefill_t<FMT, 128>(p, maps, dev, sms, s);
+    case 192: return launch_prefill_t<FMT, 192>(p, maps, dev, sms, s);
+    case 256: return launch_prefill_t<FMT, 256>(p, maps, dev, sms, s);
   }
   return cudaErrorInvalidValue;
 }
