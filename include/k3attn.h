@@ -109,7 +109,7 @@ typedef struct {
 #define K3ATTN_DEV_BAD_LENGTH 0x4u /* a length outside 0 .. table_width * page_size: taken as the
                                       nearest of these */
 
-/* In the status word too: a wait inside k3attn_prefill ran out (about two seconds); its results are
+/* In the status word too: a wait inside k3attn_prefill ran out (a second and more); its results are
  * invalid. */
 #define K3ATTN_TIMEOUT 0x100u
 

@@ -46,9 +46,6 @@ struct PrefillMaps {
 constexpr int PRE_START = 256, PRE_LEAST = 512, PRE_WHOLE = 2;
 constexpr int PRE_MAX_BLOCKS = 192;
 constexpr int PRE_COPY_WARPS = 6, PRE_THREADS = 256 + 32 * PRE_COPY_WARPS + 64;
-// Registers of a thread: at the launch, then of the 256 of the softmax and of the others
-constexpr int PRE_REGS = 128, PRE_REGS_SOFTMAX = 192, PRE_REGS_OTHERS = 64;
-static_assert(256 * PRE_REGS_SOFTMAX + (PRE_THREADS - 256) * PRE_REGS_OTHERS <= PRE_THREADS * PRE_REGS, "a warp would wait for ever");
 
 // ---------------------------------------------------------------------------- the order of the work
 K3_HD int64_t pre_min(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -472,7 +469,6 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   };
 
   if (warp < 8) {
-    regs_more<PRE_REGS_SOFTMAX>();
     const int half = warp / 4, r = half * 128 + (warp % 4) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
     const uint32_t o_at = lanes + C::O_AT + half * 128;
@@ -493,44 +489,49 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       const int sk_v = p.window > 0 ? p.sinks : 0;
       // the maximum, in units of 2^unit; the sum of weights
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < nkt; ++j) {
         const int buf = HALVES == 2 ? half : n_s & 1;
         const uint32_t par = HALVES == 2 ? n_s & 1 : (n_s >> 1) & 1;
         if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(s_full(buf), par, gave_up)))) break;
         tm_fence_after();
         const uint32_t s_at = lanes + buf * C::S_AT;
-        uint32_t raw[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tm_ld32(s_at + 32 * c, raw + 32 * c);
-        tm_ld_wait<BN>(raw);
-        float2 s[BN / 2];
         const int ring = (tile0 + j) % RING, v0 = (it.kt0 + j) * BN;
         const float* const ks = reinterpret_cast<const float*>(__cvta_shared_to_generic(scales_at + ring * 2 * BN * 4));
         const float* const vs = ks + BN;
-#pragma unroll
-        for (int i = 0; i < BN / 2; ++i) {
-          s[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
-          if constexpr (FMT == CF_E4M3) s[i] = mul2(s[i], *reinterpret_cast<const float2*>(ks + 2 * i));  // (with p.scale)
-        }
         const uint4 ok4 = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(masks_at + ring * 16));
-        const uint32_t okw[4] = {ok4.x, ok4.y, ok4.z, ok4.w};
         const int hi = hi_v - v0, lo = lo_v - v0, sk = sk_v - v0;
-        const bool all_rows = (okw[0] & okw[1] & (BN > 64 ? okw[2] & okw[3] : ~0u)) == ~0u;
-        if (!__all_sync(0xFFFFFFFFu, all_rows && hi >= BN && (lo <= 0 || sk >= BN))) {
+        const bool all_rows = (ok4.x & ok4.y & (BN > 64 ? ok4.z & ok4.w : ~0u)) == ~0u;
+        const bool masked = !__all_sync(0xFFFFFFFFu, all_rows && hi >= BN && (lo <= 0 || sk >= BN));
+        // 32 logits of a row, twice (for the maximum and for the weights): tensor memory is as near as
+        // registers are, and code that holds all of a row at once does not fit the instruction cache
+        auto logits_of = [&](int c, float2 (&s)[16]) {
+          uint32_t raw[32];
+          tm_ld32(s_at + 32 * c, raw);
+          tm_ld_wait<32>(raw);
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            const uint32_t see = bits_below(hi - 32 * c) & (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c)) & okw[c];
+          for (int i = 0; i < 16; ++i) {
+            s[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
+            if constexpr (FMT == CF_E4M3) s[i] = mul2(s[i], *reinterpret_cast<const float2*>(ks + 32 * c + 2 * i));  // (with p.scale)
+          }
+          if (masked) {
+            const uint32_t there = c < 2 ? (c == 0 ? ok4.x : ok4.y) : (c == 2 ? ok4.z : ok4.w);
+            const uint32_t see = bits_below(hi - 32 * c) & (~bits_below(lo - 32 * c) | bits_below(sk - 32 * c)) & there;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float2& x = s[16 * c + i];
-              if (!(see >> (2 * i) & 1)) x.x = -INFINITY;
-              if (!(see >> (2 * i + 1) & 1)) x.y = -INFINITY;
+              if (!(see >> (2 * i) & 1)) s[i].x = -INFINITY;
+              if (!(see >> (2 * i + 1) & 1)) s[i].y = -INFINITY;
             }
           }
-        }
+        };
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          float2 s[16];
+          logits_of(c, s);
 #pragma unroll
-        for (int i = 0; i < BN / 2; ++i) tops[i & 3] = max3(tops[i & 3], s[i].x, s[i].y);
+          for (int i = 0; i < 16; ++i) tops[i & 3] = max3(tops[i & 3], s[i].x, s[i].y);
+        }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         // the maximum moves where a row's is more than 2^8 above it (weights up to 2^8 are as exact), and
         // the sums with it
@@ -557,31 +558,30 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         const float down = m == -INFINITY ? 0.f : -m;
         float2 sum[4] = {};
         const uint32_t p_at = lanes + C::P_AT + buf * C::P_STEP;
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          float2 s[16];
+          logits_of(c, s);
+          uint32_t w[16];
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {  // the product begins with the first half's weights
-          uint32_t w[BN / 4];
-#pragma unroll
-          for (int c = 0; c < BN / 64; ++c) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int i = part * (BN / 4) + 16 * c + k;
-              // (the difference first: with the products first, sums and products become one, which does not round
-              // the product, and beside a large maximum nothing is left of a weight)
-              float2 x = add2(s[i], make_float2(down, down));
-              if (FMT != CF_E4M3) x = mul2(x, make_float2(unit, unit));
-              float2 e = make_float2(ex2(x.x), ex2(x.y));
-              sum[k & 3] = add2(sum[k & 3], e);
-              if constexpr (FMT == CF_E4M3) e = mul2(e, *reinterpret_cast<const float2*>(vs + 2 * i));
-              w[16 * c + k] = bf16x2_of(e);
-            }
-            tm_st16(p_at + part * (BN / 4) + 16 * c, w + 16 * c);
+          for (int i = 0; i < 16; ++i) {
+            // (the difference first: with the products first, sums and products become one, which does not round
+            // the product, and beside a large maximum nothing is left of a weight)
+            float2 x = add2(s[i], make_float2(down, down));
+            if (FMT != CF_E4M3) x = mul2(x, make_float2(unit, unit));
+            float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[i & 3] = add2(sum[i & 3], e);
+            if constexpr (FMT == CF_E4M3) e = mul2(e, *reinterpret_cast<const float2*>(vs + 32 * c + 2 * i));
+            w[i] = bf16x2_of(e);
           }
+          tm_st16(p_at + 16 * c, w);  // (over logits that are read)
           tm_st_wait();
-#pragma unroll
-          for (int c = 0; c < BN / 64; ++c) tm_keep16(w + 16 * c);
-          tm_fence_before();
-          __syncwarp();
-          if (lane == 0) mb_arrive(part ? p_rest(buf) : p_full(buf));
+          tm_keep16(w);
+          if (c == BN / 64 - 1 || c == BN / 32 - 1) {  // the product begins with the first half's weights
+            tm_fence_before();
+            __syncwarp();
+            if (lane == 0) mb_arrive(c == BN / 32 - 1 ? p_rest(buf) : p_full(buf));
+          }
         }
         const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += both.x + both.y;
@@ -685,7 +685,6 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       while (take(it)) {
       }
   } else {
-    regs_fewer<PRE_REGS_OTHERS>();
     if (warp < 8 + PRE_COPY_WARPS) {
       // ---- copies
       const int w = warp - 8, row_in = lane / 4, piece = lane % 4;
@@ -1049,6 +1048,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         const int nkt = it.kt1 - it.kt0, halves = HALVES == 2 && it.ntok * it.heads > 128 ? 2 : 1;
         // the first logits
         if (!keys_there(tiles)) return;
+#pragma unroll 1
         for (int h = 0; h < halves; ++h) {
           if (!wait(q_full(h), q_taken[h] & 1)) return;
           tm_fence_after();
@@ -1057,6 +1057,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
           ++q_taken[h];
         }
         commit(k_empty(tiles % SLOTS));
+#pragma unroll 1
         for (int j = 0; j < nkt; ++j, ++tiles) {
           const bool more = j + 1 < nkt;
           if (HALVES == 1 && more) {  // the next logits, into the other buffer
@@ -1066,6 +1067,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
             if (j + 2 == nkt) commit(q_empty(0));
           }
           if (!wait(v_full(tiles % V_SLOTS), tiles / V_SLOTS & 1)) return;
+#pragma unroll 1
           for (int h = 0; h < halves; ++h) {
             const int buf = HALVES == 2 ? h : n_s & 1;
             const uint32_t parity = HALVES == 2 ? n_p[h] & 1 : n_s >> 1 & 1;

@@ -44,21 +44,16 @@ K3_DEVI bool mb_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of the given parity; false if the block has given up, or after about two seconds
-// (then it has).
+// Waits for the phase of the given parity; false if the block has given up, or after 2^24 looks (a
+// second and more; then it has).
 K3_DEVI bool mb_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (mb_try(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mb_try(bar, parity)) return true;
-    if (*gave_up) return false;
-    if (clock64() - t0 > (1ll << 32)) {
-      *gave_up = 1;
-      return false;
-    }
+  for (uint32_t n = 1; n < (1u << 24); ++n) {
+    if (mb_try(bar, parity)) return true;
+    if ((n & 255) == 0 && *gave_up) return false;
   }
+  *gave_up = 1;
+  return false;
 }
 
 K3_DEVI void tm_alloc(uint32_t dst, uint32_t columns) {
@@ -150,14 +145,5 @@ K3_DEVI void tm_keep16(const uint32_t* r) {
 #undef K3_R4
 #undef K3_U4
 #undef K3_W4
-
-template <int N>
-K3_DEVI void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-K3_DEVI void regs_fewer() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
 
 }  // namespace k3
