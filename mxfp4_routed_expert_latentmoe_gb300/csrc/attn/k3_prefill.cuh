@@ -296,9 +296,9 @@ struct PreCfg {
   // tiles of keys, and of values, as bf16 (codes: no more than leaves each warp's ring two and more)
   static constexpr int SLOTS = FMT == CF_BF16 ? (ROOM / (2 * TILE) > 4 ? 4 : ROOM / (2 * TILE)) : DP <= 64 ? 3 : 2;
   static constexpr int V_SLOTS = FMT == CF_E4M3 && (DP == 128 || DP == 256) ? 1 : SLOTS;
-  static constexpr int RAWS_FIT = FMT == CF_BF16 ? 0 : (ROOM - (SLOTS + V_SLOTS) * TILE) / (PRE_COPY_WARPS * (RAW + 16));
+  static constexpr int RAWS_FIT = FMT == CF_BF16 ? 0 : (ROOM - (SLOTS + V_SLOTS) * TILE) / (PRE_COPY_WARPS * (RAW + 8));
   static constexpr int RAWS = RAWS_FIT > 6 ? 6 : RAWS_FIT;
-  static constexpr int SMEM = OTHERS + (SLOTS + V_SLOTS) * TILE + PRE_COPY_WARPS * RAWS * (RAW + 16);
+  static constexpr int SMEM = OTHERS + (SLOTS + V_SLOTS) * TILE + PRE_COPY_WARPS * RAWS * (RAW + 8);
   static constexpr int REC = ROWS * (DP + 2);  // floats of a record
   // columns of tensor memory: a half's logits (with one half two buffers), its weights over them (with one
   // half behind the sums), its sums
@@ -364,8 +364,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, k_at = q_at + HALVES * C::Q_HALF, v_at = k_at + SLOTS * C::TILE, bars = v_at + V_SLOTS * C::TILE;
   const uint32_t items_at = bars + 512, masks_at = items_at + ITEMS * 128, scales_at = (masks_at + RING * 16 + 63u) & ~63u,
-                 raw_at = scales_at + C::SCALES,
-                 raw_notes = raw_at + PRE_COPY_WARPS * C::RAWS * C::RAW, raw_bars = raw_notes + PRE_COPY_WARPS * C::RAWS * 8;
+                 raw_at = scales_at + C::SCALES, raw_notes = raw_at + PRE_COPY_WARPS * C::RAWS * C::RAW;
   auto k_full = [&](int s) { return bars + 8 * s; };
   auto k_empty = [&](int s) { return bars + 8 * (4 + s); };
   auto v_full = [&](int s) { return bars + 8 * (8 + s); };
@@ -402,7 +401,6 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       mb_init(o_done(h, 1), 1);
     }
     mb_init(done, 1);
-    for (int i = 0; i < PRE_COPY_WARPS * C::RAWS; ++i) mb_init(raw_bars + 8 * i, 1);
     mb_init_fence();
   }
   if (warp == PRE_THREADS / 32 - 1) tm_alloc(smem_u32(&s_tmem), 512);
@@ -503,12 +501,9 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         const int hi = hi_v - v0, lo = lo_v - v0, sk = sk_v - v0;
         const bool all_rows = (ok4.x & ok4.y & (BN > 64 ? ok4.z & ok4.w : ~0u)) == ~0u;
         const bool masked = !__all_sync(0xFFFFFFFFu, all_rows && hi >= BN && (lo <= 0 || sk >= BN));
-        // 32 logits of a row, twice (for the maximum and for the weights): tensor memory is as near as
-        // registers are, and code that holds all of a row at once does not fit the instruction cache
-        auto logits_of = [&](int c, float2 (&s)[16]) {
-          uint32_t raw[32];
-          tm_ld32(s_at + 32 * c, raw);
-          tm_ld_wait<32>(raw);
+        // Logits are read twice, for the maximum and for the weights: tensor memory is as near as registers,
+        // and a row of 128 does not leave the other warps registers enough.  raw: 32 of them, from 32 c on
+        auto logits_of = [&](int c, const uint32_t* raw, float2 (&s)[16]) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             s[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
@@ -526,11 +521,18 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         };
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          float2 s[16];
-          logits_of(c, s);
+        for (int part = 0; part < BN / 64; ++part) {
+          uint32_t raw[64];
+          tm_ld32(s_at + 64 * part, raw);
+          tm_ld32(s_at + 64 * part + 32, raw + 32);
+          tm_ld_wait<64>(raw);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) tops[i & 3] = max3(tops[i & 3], s[i].x, s[i].y);
+          for (int c = 0; c < 2; ++c) {
+            float2 s[16];
+            logits_of(2 * part + c, raw + 32 * c, s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) tops[i & 3] = max3(tops[i & 3], s[i].x, s[i].y);
+          }
         }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         // the maximum moves where a row's is more than 2^8 above it (weights up to 2^8 are as exact), and
@@ -558,11 +560,9 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         const float down = m == -INFINITY ? 0.f : -m;
         float2 sum[4] = {};
         const uint32_t p_at = lanes + C::P_AT + buf * C::P_STEP;
-#pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
+        auto weights_of = [&](int c, const uint32_t* raw, uint32_t (&w)[16]) {
           float2 s[16];
-          logits_of(c, s);
-          uint32_t w[16];
+          logits_of(c, raw, s);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             // (the difference first: with the products first, sums and products become one, which does not round
@@ -575,13 +575,26 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
             w[i] = bf16x2_of(e);
           }
           tm_st16(p_at + 16 * c, w);  // (over logits that are read)
+        };
+        // (of BN 64 a part is 32 logits, of 128 two times 32, the second ones read while the first are at work)
+        constexpr int IN_PART = BN / 64;
+        uint32_t raw[2][32];
+        tm_ld32(s_at, raw[0]);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {  // the product begins with the first part's weights
+          uint32_t w[IN_PART][16];
+          tm_ld_wait<32>(raw[0]);
+          if (IN_PART == 2) tm_ld32(s_at + 64 * part + 32, raw[1]);
+          weights_of(IN_PART * part, raw[0], w[0]);
+          if (IN_PART == 2) tm_ld_wait<32>(raw[1]);
+          if (part == 0) tm_ld32(s_at + 32 * IN_PART, raw[0]);
+          if (IN_PART == 2) weights_of(2 * part + 1, raw[1], w[IN_PART - 1]);
           tm_st_wait();
-          tm_keep16(w);
-          if (c == BN / 64 - 1 || c == BN / 32 - 1) {  // the product begins with the first half's weights
-            tm_fence_before();
-            __syncwarp();
-            if (lane == 0) mb_arrive(c == BN / 32 - 1 ? p_rest(buf) : p_full(buf));
-          }
+#pragma unroll
+          for (int c = 0; c < IN_PART; ++c) tm_keep16(w[c]);
+          tm_fence_before();
+          __syncwarp();
+          if (lane == 0) mb_arrive(part ? p_rest(buf) : p_full(buf));
         }
         const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += both.x + both.y;
@@ -850,7 +863,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         // the order of the products: an item's first keys, its queries, their values, the next keys ..
         static_assert(C::RAW % 16 == 0, "copies of 16 bytes");
         constexpr int RAWS = C::RAWS;
-        const uint32_t raws = raw_at + w * (RAWS * C::RAW), notes = raw_notes + w * (RAWS * 8), landed_bars = raw_bars + w * (RAWS * 8);
+        const uint32_t raws = raw_at + w * (RAWS * C::RAW), notes = raw_notes + w * (RAWS * 8);
         const uint32_t row_bytes = FMT == CF_E4M3 ? p.D : p.D / 2;
         constexpr int KEYS = 0, QUERIES = 1, VALUES = 2, NEW_ITEM = 3, NO_MORE = 4;
         int state = NEW_ITEM, j = 0, front = 0, back = 0, slot_front = 0, slot_back = 0;
@@ -869,7 +882,6 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
             else
               cp_async_wait<RAWS - 1>();
             __syncwarp();
-            if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(landed_bars + 8 * (back % RAWS), back / RAWS & 1, gave_up)))) break;
             const uint2 note = lds64(notes + 8 * (back % RAWS));
             const int tile = (int)note.x;
             const uint32_t raw = raws + slot_back;
@@ -940,16 +952,19 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
           {
             const uint8_t *const from = keys ? p.c.k : p.c.v, *const exps = keys ? p.c.k_exps() : p.c.v_exps();
             const bool mine = lane < 8 * (keys ? k_count : v_count), there = entry >= 0;
-            const uint32_t to = raws + slot_front + lane * C::RAW_ROW, word = raws + slot_front + C::OWN * C::RAW_ROW + 4 * lane;
-            const uint32_t bar = landed_bars + 8 * (front % RAWS);
+            const uint32_t word = raws + slot_front + C::OWN * C::RAW_ROW + 4 * lane;
             const int64_t so = there ? it.kvh * p.c.shead + entry * p.c.spage + in_page * p.c.stok : 0;
-            if (lane == 0) mb_arrive_expect(bar, __popc(rows) * row_bytes);
-            __syncwarp();
+            const uint64_t row = (uint64_t)(uintptr_t)(from + (there ? it.kvh * p.c.head + entry * p.c.page + in_page * p.c.tok : 0));
+            constexpr int IN_ROW = C::RAW_ROW / 16;  // pieces of a row: consecutive lanes
+#pragma unroll
+            for (int i = 0; i < (C::OWN * IN_ROW + 31) / 32; ++i) {
+              const int r = (32 * i + lane) / IN_ROW, c = (32 * i + lane) % IN_ROW;
+              const uint64_t src = __shfl_sync(0xFFFFFFFFu, row, r & 31);
+              const uint32_t n = rows >> r & 1 && 16 * c < row_bytes ? 16 : 0;
+              if (r < C::OWN)
+                cp_async16_or_zero(raws + slot_front + 16 * (32 * i + lane), reinterpret_cast<const uint8_t*>(src) + (n ? 16 * c : 0), n);
+            }
             if (mine) {
-              if (there)
-                bulk_copy(to, from + it.kvh * p.c.head + entry * p.c.page + in_page * p.c.tok, row_bytes, bar);
-              else
-                for (int i = 0; i < C::RAW_ROW; i += 16) sts128(to + i, make_uint4(0, 0, 0, 0));
               if constexpr (FMT == CF_MXFP4) {
 #pragma unroll
                 for (int k = 0; k < C::WORDS; ++k) {
