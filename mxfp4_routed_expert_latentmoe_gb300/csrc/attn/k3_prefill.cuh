@@ -43,9 +43,12 @@ struct PrefillMaps {
 };
 
 // What a tile's start counts as, the fewest keys of a block, tiles of keys up to which a tile is not cut.
-constexpr int PRE_START = 256, PRE_LEAST = 512, PRE_WHOLE = 2;
+constexpr int PRE_START = 768, PRE_LEAST = 512, PRE_WHOLE = 2;
 constexpr int PRE_MAX_BLOCKS = 192;
 constexpr int PRE_COPY_WARPS = 6, PRE_THREADS = 256 + 32 * PRE_COPY_WARPS + 64;
+// Registers of a thread: at the launch, then of the 256 of the softmax and of the others
+constexpr int PRE_REGS = 128, PRE_REGS_SOFTMAX = 160, PRE_REGS_OTHERS = 96;
+static_assert(PRE_THREADS == 512 && PRE_REGS_SOFTMAX + PRE_REGS_OTHERS <= 2 * PRE_REGS, "a warp would wait for ever");
 
 // ---------------------------------------------------------------------------- the order of the work
 K3_HD int64_t pre_min(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -467,6 +470,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   };
 
   if (warp < 8) {
+    regs_more<PRE_REGS_SOFTMAX>();
     const int half = warp / 4, r = half * 128 + (warp % 4) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
     const uint32_t o_at = lanes + C::O_AT + half * 128;
@@ -507,7 +511,14 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             s[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
-            if constexpr (FMT == CF_E4M3) s[i] = mul2(s[i], *reinterpret_cast<const float2*>(ks + 32 * c + 2 * i));  // (with p.scale)
+          }
+          if constexpr (FMT == CF_E4M3) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {  // (with p.scale)
+              const float4 x = *reinterpret_cast<const float4*>(ks + 32 * c + 2 * i);
+              s[i] = mul2(s[i], make_float2(x.x, x.y));
+              s[i + 1] = mul2(s[i + 1], make_float2(x.z, x.w));
+            }
           }
           if (masked) {
             const uint32_t there = c < 2 ? (c == 0 ? ok4.x : ok4.y) : (c == 2 ? ok4.z : ok4.w);
@@ -698,6 +709,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       while (take(it)) {
       }
   } else {
+    regs_fewer<PRE_REGS_OTHERS>();
     if (warp < 8 + PRE_COPY_WARPS) {
       // ---- copies
       const int w = warp - 8, row_in = lane / 4, piece = lane % 4;

@@ -138,4 +138,13 @@ K3_DEVI void tm_keep16(const uint32_t* r) {
 #undef K3_U4
 #undef K3_W4
 
+template <int N>
+K3_DEVI void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+K3_DEVI void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 }  // namespace k3

@@ -335,6 +335,15 @@ template <int FMT, int DP>
 cudaError_t launch_prefill_t(const PrefillParams& p, const PrefillMaps& maps, int dev, int sms, cudaStream_t s) {
   using C = PreCfg<FMT, DP>;
   constexpr auto kernel = k3_prefill_kernel<FMT, DP>;
+  static std::atomic<int> registers[kMaxDevices];
+  if (registers[dev].load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    registers[dev].store(a.numRegs, std::memory_order_release);
+  }
+  // the warps' shares of the registers have to be there at the launch (or a warp would wait for ever)
+  if (registers[dev].load(std::memory_order_acquire) < PRE_REGS) return cudaErrorInvalidValue;
   if (!set_smem<k3_prefill_kernel<FMT, DP>>(dev, C::SMEM)) return cudaErrorInvalidValue;
   const int grid = sms < PRE_MAX_BLOCKS ? sms : PRE_MAX_BLOCKS;
   return launch(kernel, dim3(grid), dim3(PRE_THREADS), C::SMEM, s, maps, p);
