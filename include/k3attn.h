@@ -110,7 +110,7 @@ typedef struct {
                                       nearest of these */
 
 /* In the status word too: a wait inside k3attn_prefill ran out (a second and more); its results are
- * invalid. */
+ * invalid, and the workspace has to be readied again. */
 #define K3ATTN_TIMEOUT 0x100u
 
 /* Bytes of workspace for k3attn_decode with these dims; the other calls need the first
@@ -202,6 +202,12 @@ k3moe_status k3attn_decode_sinks(const k3attn_dims* dims, int32_t n_sinks, int32
  * ones; T is the capture's) and must not change while the call runs.  q_starts that fall or leave
  * 0 .. T, and a length below its new tokens' number, set K3ATTN_DEV_BAD_LENGTH; a token at a
  * negative position attends to nothing (out 0, lse -infinity).
+ * Logits, softmax statistics and sums are held in fp32, powers of two to 2^-22; a weight (times its
+ * row's scale, K3ATTN_E4M3) is rounded to bf16 before its product (off by 2^-8 of itself at most), the
+ * sum of weights is of the unrounded ones, the result is rounded to bf16 once.  A weight below 2^-126
+ * of the largest is lost.  K3ATTN_E4M3: a key's scale multiplies its logit behind the product with its
+ * codes, so that queries of more than about 1e33 leave fp32 there.  A value that is infinite or NaN has
+ * a part in no token that does not attend to it, but costs the tokens of its tile a slower pass.
  * ws: k3attn_prefill_workspace_bytes(dims) bytes (0 for invalid dims), readied by
  * k3attn_workspace_init; such a workspace serves k3attn_decode and the other calls too. */
 size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims);

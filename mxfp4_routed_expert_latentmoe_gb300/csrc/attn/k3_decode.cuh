@@ -14,12 +14,19 @@
 // tokens, bf16: 168 us, 88% (the copies alone reach 95%; the rest is the join at the 3 or 4
 // sequence ends of a block).  Up to 16 query heads: twice the matrix instructions and weights a
 // tile with the registers of 8 warps an SM used up, so that a warp's own instruction latency
-// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 64 us, 43%.  Few
+// bounds it: 201 sequences in a window of 1000, 12 heads on E4M3 rows of 192: 64 us, 43%.  MXFP4 rows are
+// half as many bytes and as many values: instructions bound them (some 900 a warp for 32 tokens of 128
+// dims; issue slots 45%, two warps a scheduler waiting for their own results): 2 x 262143 tokens 145 us,
+// 40% of the copy rate, 64 up to 8192 107 us, 37%.  Few
 // short sequences: the chain of dependent reads (lengths, page table, rows, joined records),
 // 4.7 us for one token, 7.9 us for one sequence of 347.
 // mma.sync rather than tcgen05: the products are 2 G flops a cached byte (under 100 TFLOP/s at
 // the copy rate with 8 heads), E4M3 rows have to pass through registers on their way to fp16
 // anyway, and the softmax stays in the registers that the products leave it in.
+//
+// MXFP4: codes become fp16 operands exactly, a group's two steps of a key have sums of their own, which
+// the group's scale multiplies in fp32; a value's largest scale goes into its weight's exponent like an
+// E4M3 row's, and each group's weights are the row's times the power of two that is left (prepare_scales).
 //
 // E4M3 rows become fp16 operands exactly; a key's scale multiplies its logit, a value's scale
 // goes into its weight's exponent, with a maximum of its own, so that weights of values of any

@@ -15,6 +15,24 @@
 // dealt out evenly to the blocks, whatever the lengths and masks; a tile that is cut leaves an
 // unnormalised record of each part in the workspace, and the part that arrives last joins them, in
 // order.
+//
+// Codes become bf16 on their way: E2M1 times its power of two is a bf16 number, E4M3 codes are, and a
+// row's E4M3 scale multiplies its column of logits, or of weights (in fp32, before they are rounded).
+// Rounded to fewer bits: a weight to bf16, whose range takes values of any size (fp16 would need a
+// maximum of its own for them); both operands of a product have one type, and the result is rounded
+// to bf16 anyway (8192-token prompt: results off by 2.2e-3 in the mean square, 1.65e-3 with fp32 weights).
+//
+// What bounds it (GB300, clocks a tile of 128 keys and 256 rows of 128 dims, measured with clock reads in
+// a copy).  bf16, 8192-token prompt, 64 query and 8 key heads: 1.10 ms, 1000 TFLOP/s, 53% of the burst
+// rate; the products take 2048 clocks of 4900, the rest is the chain of a half: from logits to the first
+// weights 1500, to the last 2500 (maximum 700, then 32 logits at a time; the two halves' warps share the
+// issue slots, neither pipe is full), then its turn at the tensor core; and a tile's start, 20000 clocks
+// (queries once the last products are through, the sums' way out), for which PRE_START stands: 768
+// keys, 1396 us at 256, 1202 at 512, 1118 at 1024.  Codes: the copying warps (a chunk of 1500 behind
+// 30001 tokens, MXFP4: 1.94 ms, 41% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses and
+// copies; E4M3 in a window of 1000: 0.57 ms), and for few rows (drafts: 200 us) the chain of one half.
+// Ten copying warps of 64 registers instead of six of 96 were 6 to 20% slower, rows of codes as bulk
+// copies of a row each (some 85 clocks to issue one) 35%.
 #pragma once
 
 #include "k3_decode.cuh"
@@ -42,7 +60,8 @@ struct PrefillMaps {
   CUtensorMap k, v;  // dims, tokens of a page, heads, pages
 };
 
-// What a tile's start counts as, the fewest keys of a block, tiles of keys up to which a tile is not cut.
+// What a tile's start counts as (see above), the fewest keys of a block, tiles of keys up to which a tile is
+// not cut (its join would take longer).
 constexpr int PRE_START = 768, PRE_LEAST = 512, PRE_WHOLE = 2;
 constexpr int PRE_MAX_BLOCKS = 192;
 constexpr int PRE_COPY_WARPS = 6, PRE_THREADS = 256 + 32 * PRE_COPY_WARPS + 64;

@@ -9,6 +9,8 @@
 // that form the angles, twice a token in an append: 65536 tokens of 4 query heads and 1 key head of
 // 128 take 118 us into an E4M3 cache (23%; fp64 units 68% busy), norms alone 63 us (39%).
 //
+// MXFP4 rows: the largest of 32 neighbours by two shuffles, of a rotated key's pieces through shared memory.
+//
 // A row (a head of a token) is taken by 8, 16 or 32 lanes, eight elements a lane, and a thread
 // has the loads of up to QKV_ROWS rows in flight before it waits for any.
 #pragma once
