@@ -1,6 +1,6 @@
 """The attention operators that stand before the routed-expert block when it serves tokens:
 norms of queries and keys per head with the position rotation, the paged key-value cache
-(bf16, E4M3 with a scale per row, or MXFP4), and the attention of one new token over its pages.
+(bf16, E4M3 with a scale per row, or MXFP4), and the attention of new tokens over its pages.
 
 Thin binding over the C ABI declared in ``include/k3attn.h``, which has the formulas.  Every
 function checks its tensors (ValueError), which all have to be on one device, passes pointers and
@@ -10,9 +10,10 @@ a decode step's kernels take no longer than they would in Python.
 
     d = attn.dims(n_heads=64, n_kv_heads=8, head_dim=128, rot_dim=128)
     cache = attn.KVCache.empty(d, n_pages=4096, page_size=64, fmt="e4m3")
-    ws = attn.workspace(d)
+    ws = attn.workspace(d, prefill=True)
     attn.kv_append(d, q, k, v, positions, slots, inv_freq, q_w, k_w, cache, q_out, ws)
-    attn.decode(d, q_out, cache, page_table, lens, out, ws)
+    attn.prefill(d, q_out, q_starts, cache, page_table, lens, out, ws)  # any number of tokens each
+    attn.decode(d, q_out, cache, page_table, lens, out, ws)             # one new token each
 """
 from __future__ import annotations
 
