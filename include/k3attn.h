@@ -109,7 +109,7 @@ typedef struct {
 #define K3ATTN_DEV_BAD_LENGTH 0x4u /* a length outside 0 .. table_width * page_size: taken as the
                                       nearest of these */
 
-/* In the status word too: a wait inside k3attn_prefill ran out (a second and more); its results are
+/* In the status word too: a wait inside k3attn_prefill ran out (after about a minute); its results are
  * invalid, and the workspace has to be readied again. */
 #define K3ATTN_TIMEOUT 0x100u
 
@@ -207,7 +207,8 @@ k3moe_status k3attn_decode_sinks(const k3attn_dims* dims, int32_t n_sinks, int32
  * sum of weights is of the unrounded ones, the result is rounded to bf16 once.  A weight below 2^-126
  * of the largest is lost.  K3ATTN_E4M3: a key's scale multiplies its logit behind the product with its
  * codes, so that queries of more than about 1e33 leave fp32 there.  A value that is infinite or NaN has
- * a part in no token that does not attend to it, but costs the tokens of its tile a slower pass.
+ * a part in no token that does not attend to it, but costs the tokens of its tile a slower pass (with
+ * some 2^23 tokens and more it may outlast the other warps' waits: K3ATTN_TIMEOUT).
  * ws: k3attn_prefill_workspace_bytes(dims) bytes (0 for invalid dims), readied by
  * k3attn_workspace_init; such a workspace serves k3attn_decode and the other calls too. */
 size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims);

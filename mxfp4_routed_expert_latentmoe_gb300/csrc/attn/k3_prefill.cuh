@@ -245,8 +245,8 @@ __device__ __noinline__ void prefill_row(const PrefillParams& p, int b, int kvh,
   const int32_t count = pos < 0 ? 0 : ns + (pos + 1 - f);
   float m = -INFINITY, l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-  for (int32_t i0 = 0; i0 < count; i0 += 32) {
-    const int32_t i = i0 + lane;
+  for (int64_t i0 = 0; i0 < count; i0 += 32) {  // (past 2^31 with the last of the longest sequences)
+    const int32_t i = (int32_t)(i0 + lane);
     int64_t at = -1, so = 0;
     float s = -INFINITY;
     if (i < count && i >= 0) {

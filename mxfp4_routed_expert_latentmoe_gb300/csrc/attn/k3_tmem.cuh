@@ -36,8 +36,9 @@ K3_DEVI bool mb_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of the given parity; false if the block has given up, or after 2^24 looks (a
-// second and more; then it has).
+// Waits for the phase of the given parity; false if the block has given up, or after 2^24 looks of
+// some 7800 clocks each, about a minute (then it has).  Half a million tokens with an infinite value among
+// them take the rows that are formed again 4 s a tile, for which the other warps wait.
 K3_DEVI bool mb_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
 #pragma unroll 1
   for (uint32_t n = 1; n < (1u << 24); ++n) {
