@@ -29,7 +29,7 @@
 // issue slots, neither pipe is full), then its turn at the tensor core; and a tile's start, 20000 clocks
 // (queries once the last products are through, the sums' way out), for which PRE_START stands: 768
 // keys, 1396 us at 256, 1202 at 512, 1118 at 1024.  Codes: the copying warps (a chunk of 1500 behind
-// 30001 tokens, MXFP4: 1.94 ms, 41% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses and
+// 30001 tokens, MXFP4: 1.93 ms, 41% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses and
 // copies; E4M3 in a window of 1000: 0.57 ms), and for few rows (drafts: 200 us) the chain of one half.
 // Ten copying warps of 64 registers instead of six of 96 were 6 to 20% slower, rows of codes as bulk
 // copies of a row each (some 85 clocks to issue one) 35%.
@@ -428,7 +428,6 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   if (warp == PRE_THREADS / 32 - 1) tm_alloc(smem_u32(&s_tmem), 512);
 
   grid_dep_wait();
-  grid_dep_launch();
 
   // ---- this block's range: every thread counts its sequences' places
   const int HR = p.Hkv * p.groups;
@@ -452,6 +451,8 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
+  // (not before the block has its tensor memory: the next kernel's could take it and wait for this one)
+  grid_dep_launch();
   const uint32_t tmem = s_tmem;
   int64_t total = 0;
   for (int w = 0; w < PRE_THREADS / 32; ++w) {
