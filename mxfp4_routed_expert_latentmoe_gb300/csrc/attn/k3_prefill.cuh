@@ -401,6 +401,9 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   auto i_empty = [&](int i) { return bars + 8 * (32 + i); };
   auto p_rest = [&](int h) { return bars + 8 * (36 + h); };  // the second half of a tile's weights
   const uint32_t done = bars + 8 * 38;
+  // of a half's cut tile: the four warps' rows of the record are there; s_last says whether it is the last one
+  auto r_there = [&](int h) { return bars + 8 * (39 + h); };
+  auto r_last = [&](int h) { return bars + 8 * (41 + h); };
   volatile int* const gave_up = &s_gave_up;
 
   if (threadIdx.x == 0) {
@@ -421,6 +424,8 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       mb_init(p_rest(h), 4);
       mb_init(o_done(h, 0), 1);
       mb_init(o_done(h, 1), 1);
+      mb_init(r_there(h), 4);
+      mb_init(r_last(h), 1);
     }
     mb_init(done, 1);
     mb_init_fence();
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
     const int half = warp / 4, r = half * 128 + (warp % 4) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
     const uint32_t o_at = lanes + C::O_AT + half * 128;
-    int n_s = 0, n_tile = 0;  // tiles of keys of this half so far, and of the block
+    int n_s = 0, n_tile = 0, n_cut = 0;  // tiles of keys of this half so far, and of the block; cut tiles of rows
     const float unit = FMT == CF_E4M3 ? 1.f : p.scale;  // (E4M3: in the keys' scales)
     bool ok = half < HALVES;
     PreItem it{};
@@ -669,15 +674,22 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
               *reinterpret_cast<uint4*>(rec + ((c / 4 + i) * C::ROWS + r) * 4) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
         if (valid) *reinterpret_cast<float2*>(rec + C::ROWS * DP + 2 * r) = make_float2(m * unit, l);
-        team_sync(half, 128);
-        if (threadIdx.x % 128 == 0) {
-          const bool last = arrive(p.arrived + 2 * it.c0 + half) == (uint32_t)(it.parts - 1);
-          if (last) p.arrived[2 * it.c0 + half] = 0;
-          s_last[half] = last;
+        // (waits that end, no barrier of the half's warps: one of them may have given up, or not have
+        // come this far)
+        __syncwarp();
+        if (lane == 0) mb_arrive(r_there(half));
+        if (warp % 4 == 0) {
+          if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(r_there(half), n_cut & 1, gave_up)))) break;
+          if (lane == 0) {
+            const bool last = arrive(p.arrived + 2 * it.c0 + half) == (uint32_t)(it.parts - 1);
+            if (last) p.arrived[2 * it.c0 + half] = 0;
+            s_last[half] = last;  // (read by all warps before they arrive at r_there again)
+            mb_arrive(r_last(half));
+          }
         }
-        team_sync(half, 128);
+        if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(r_last(half), n_cut & 1, gave_up)))) break;
+        ++n_cut;
         final = *reinterpret_cast<volatile int32_t*>(&s_last[half]);
-        team_sync(half, 128);
         if (final && valid) {
           // block c0's part is its second record, the others' their first
           auto part = [&](int i) { return p.parts + (2 * (int64_t)(it.c0 + i) + (i == 0)) * C::REC; };
@@ -1140,7 +1152,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       while (ok && take(it)) rows_of_item();
       commit(done);  // all products have ended before the memory goes
       volatile int never = 0;
-      mb_wait(done, 0, &never);
+      mb_wait(done, 0, &never, MB_LOOKS);
       __syncwarp();
     }
   }

@@ -36,12 +36,16 @@ K3_DEVI bool mb_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of the given parity; false if the block has given up, or after 2^24 looks of
+// Waits for the phase of the given parity; false if the block has given up, or after MB_LOOKS looks of
 // some 7800 clocks each, about a minute (then it has).  Half a million tokens with an infinite value among
 // them take the rows that are formed again 4 s a tile, for which the other warps wait.
-K3_DEVI bool mb_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+constexpr uint32_t MB_LOOKS = 1u << 24;
+#ifndef K3_MB_LOOKS  // (a test lets chosen waits run out at once)
+#define K3_MB_LOOKS MB_LOOKS
+#endif
+K3_DEVI bool mb_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, uint32_t looks = K3_MB_LOOKS) {
 #pragma unroll 1
-  for (uint32_t n = 1; n < (1u << 24); ++n) {
+  for (uint32_t n = 1; n < looks; ++n) {
     if (mb_try(bar, parity)) return true;
     if ((n & 255) == 0 && *gave_up) return false;
   }
