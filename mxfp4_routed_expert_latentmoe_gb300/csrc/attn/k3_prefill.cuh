@@ -401,9 +401,10 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   auto i_empty = [&](int i) { return bars + 8 * (32 + i); };
   auto p_rest = [&](int h) { return bars + 8 * (36 + h); };  // the second half of a tile's weights
   const uint32_t done = bars + 8 * 38;
-  // of a half's cut tile: the four warps' rows of the record are there; s_last says whether it is the last one
-  auto r_there = [&](int h) { return bars + 8 * (39 + h); };
-  auto r_last = [&](int h) { return bars + 8 * (41 + h); };
+  // of a half's cut tile, one that goes on from the block before (0) or on behind (1), of which a block has one
+  // each: the four warps' rows of the record are there; s_last says whether it is the last one
+  auto r_there = [&](int h, int which) { return bars + 8 * (39 + 2 * h + which); };
+  auto r_last = [&](int h, int which) { return bars + 8 * (43 + 2 * h + which); };
   volatile int* const gave_up = &s_gave_up;
 
   if (threadIdx.x == 0) {
@@ -424,8 +425,10 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       mb_init(p_rest(h), 4);
       mb_init(o_done(h, 0), 1);
       mb_init(o_done(h, 1), 1);
-      mb_init(r_there(h), 4);
-      mb_init(r_last(h), 1);
+      for (int i = 0; i < 2; ++i) {
+        mb_init(r_there(h, i), 4);
+        mb_init(r_last(h, i), 1);
+      }
     }
     mb_init(done, 1);
     mb_init_fence();
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
     const int half = warp / 4, r = half * 128 + (warp % 4) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
     const uint32_t o_at = lanes + C::O_AT + half * 128;
-    int n_s = 0, n_tile = 0, n_cut = 0;  // tiles of keys of this half so far, and of the block; cut tiles of rows
+    int n_s = 0, n_tile = 0;  // tiles of keys of this half so far, and of the block
     const float unit = FMT == CF_E4M3 ? 1.f : p.scale;  // (E4M3: in the keys' scales)
     bool ok = half < HALVES;
     PreItem it{};
@@ -677,18 +680,17 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         // (waits that end, no barrier of the half's warps: one of them may have given up, or not have
         // come this far)
         __syncwarp();
-        if (lane == 0) mb_arrive(r_there(half));
+        if (lane == 0) mb_arrive(r_there(half, it.kt0 == 0));
         if (warp % 4 == 0) {
-          if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(r_there(half), n_cut & 1, gave_up)))) break;
+          if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(r_there(half, it.kt0 == 0), 0, gave_up)))) break;
           if (lane == 0) {
             const bool last = arrive(p.arrived + 2 * it.c0 + half) == (uint32_t)(it.parts - 1);
             if (last) p.arrived[2 * it.c0 + half] = 0;
-            s_last[half] = last;  // (read by all warps before they arrive at r_there again)
-            mb_arrive(r_last(half));
+            s_last[half] = last;  // (read by all warps before they arrive at the next r_there)
+            mb_arrive(r_last(half, it.kt0 == 0));
           }
         }
-        if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(r_last(half), n_cut & 1, gave_up)))) break;
-        ++n_cut;
+        if (!(ok = __all_sync(0xFFFFFFFFu, mb_wait(r_last(half, it.kt0 == 0), 0, gave_up)))) break;
         final = *reinterpret_cast<volatile int32_t*>(&s_last[half]);
         if (final && valid) {
           // block c0's part is its second record, the others' their first
