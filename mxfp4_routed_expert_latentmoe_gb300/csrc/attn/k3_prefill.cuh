@@ -201,6 +201,14 @@ struct PreWalk {
     return true;
   }
 };
+// The keys of a tile that a token at position pos attends to: those below hi that are at least lo or below sk.
+struct PreSeen {
+  int32_t hi, lo, sk;
+  K3_DEVI PreSeen(const PrefillParams& p, int32_t pos, int32_t f, int32_t ns, int32_t keys)
+      : hi(max(0, min(pos + 1 - f + ns, keys))),
+        lo(p.window > 0 ? (pos >= p.window ? pos - p.window + 1 : 0) - f + ns : 0),
+        sk(p.window > 0 ? p.sinks : 0) {}
+};
 // places of a block
 K3_HD int64_t pre_chunk(int64_t total, int64_t blocks) { return pre_max(PRE_LEAST, (total + blocks - 1) / blocks); }
 
@@ -235,62 +243,245 @@ K3_DEVI void row8(const uint8_t* row, int chunk, float scale, const uint8_t* exp
   }
 }
 
-// One row by a warp, over its visible tokens alone: a tile's products take every row of values, and
-// weight 0 times a value that is infinite or NaN is NaN, so that rows which come out without being
-// finite are formed again here.  32 keys at a time, a lane a key, then 8 dims a lane.
+// the low bits of a word: those below x
+K3_DEVI uint32_t bits_below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; }
+
+// A tile's products take every row of values, and weight 0 times a value that is infinite or NaN is NaN.  A
+// row of the result that is not finite has
+//   seen such a value itself, in each of its dims that are not finite: then it is right;
+//   or not seen one that a tile of its keys holds, behind its position or in front of its window;
+//   or sums of finite values have left fp32's range on the way, with weights of up to 2^8.
+// prefill_again tells them apart and forms the latter two again, over their visible keys alone.
+struct PreKeys {
+  int32_t b, kvh, f, ns, keys, len;  // as PreItem's
+};
+struct PreRow {  // a lane's: its visible keys, its place
+  PreSeen seen;
+  int32_t head;
+  int64_t row;
+};
+K3_HD constexpr int key_lanes(int dp) { return dp <= 64 ? 8 : dp <= 128 ? 16 : 32; }  // lanes a key, eight dims each
+
+// where key v's row begins (-1: there is none), and its scales
+K3_DEVI void key_at(const PrefillParams& p, const PreKeys& k, uint32_t v, int64_t& at, int64_t& so) {
+  at = -1;
+  so = 0;
+  const uint32_t t = v < (uint32_t)k.ns ? v : v - k.ns + k.f;
+  if (v >= (uint32_t)k.keys || t >= (uint32_t)k.len) return;
+  const uint32_t pg = p.c.by_page(t), in_page = t - pg * (uint32_t)p.c.page_size;
+  const int32_t entry = __ldg(p.table + (int64_t)k.b * p.table_width + pg);
+  if (entry < 0 || entry >= p.c.n_pages) return;
+  at = entry * p.c.page + k.kvh * p.c.head + in_page * p.c.tok;
+  so = entry * p.c.spage + k.kvh * p.c.shead + in_page * p.c.stok;
+}
+// which of eight values of a row are not finite
 template <int FMT>
-__device__ __noinline__ void prefill_row(const PrefillParams& p, int b, int kvh, int head, int64_t row, int32_t pos, int lane) {
-  const uint16_t* const q = p.q + row * p.q_stride + (int64_t)head * p.D;
-  const int32_t f = p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0, ns = min(p.sinks, f);
-  const int32_t count = pos < 0 ? 0 : ns + (pos + 1 - f);
-  float m = -INFINITY, l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int64_t i0 = 0; i0 < count; i0 += 32) {  // (past 2^31 with the last of the longest sequences)
-    const int32_t i = (int32_t)(i0 + lane);
-    int64_t at = -1, so = 0;
-    float s = -INFINITY;
-    if (i < count && i >= 0) {
-      const int32_t tok = i < ns ? i : f + (i - ns), pg = (int32_t)p.c.by_page(tok), in_page = tok - pg * p.c.page_size;
-      const int32_t entry = p.table[(int64_t)b * p.table_width + pg];
-      if (entry >= 0 && entry < p.c.n_pages) {
-        at = entry * p.c.page + kvh * p.c.head + in_page * p.c.tok;
-        so = entry * p.c.spage + kvh * p.c.shead + in_page * p.c.stok;
-        s = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < p.D / 8; ++c) {
-          float x[8];
-          row8<FMT>(p.c.k + at, c, 1.f, p.c.k_exps() + so, x);
+K3_DEVI uint32_t not_finite8(const PrefillParams& p, int64_t at, int64_t so, int chunk) {
+  float x[8];
+  row8<FMT>(p.c.v + at, chunk, FMT == CF_E4M3 ? p.c.vs[so] : 1.f, p.c.v_exps() + so, x);
+  uint32_t bits = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(x[e], bf16_bits_to_f32(__ldg(q + 8 * c + e)), s);
-        }
-        s *= (FMT == CF_E4M3 ? p.c.ks[so] : 1.f) * p.scale;
+  for (int e = 0; e < 8; ++e) bits |= (uint32_t)((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) << e;
+  return bits;
+}
+// which of the keys v0 .. v0 + 31 have a value that is not finite
+template <int FMT, int DP>
+K3_DEVI uint32_t not_finite32(const PrefillParams& p, const PreKeys& k, uint32_t v0, int lane) {
+  constexpr int L = key_lanes(DP), N = 32 / L;
+  int64_t at, so;
+  key_at(p, k, v0 + lane, at, so);
+  uint32_t keys = 0;
+#pragma unroll 4
+  for (int j = 0; j < 32; j += N) {
+    const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j + lane / L), o = __shfl_sync(0xFFFFFFFFu, so, j + lane / L);
+    const bool on = r >= 0 && 8 * (lane % L) < p.D;  // (else any row's: loads without a branch)
+    const uint32_t bits = not_finite8<FMT>(p, on ? r : 0, on ? o : 0, on ? lane % L : 0);
+    const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, on && bits);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (lanes >> (n * L) & (0xFFFFFFFFu >> (32 - L))) keys |= 1u << (j + n);
+  }
+  return keys;
+}
+
+// The first four (or fewer) of the rows `which` by a warp, which share the loads: 32 keys at a time, `L` lanes
+// a key, then a lane a key for the weights.
+template <int FMT, int DP>
+K3_DEVI void prefill_rows(const PrefillParams& p, const PreKeys& k, const PreRow& x, uint32_t which, int lane) {
+  constexpr int L = key_lanes(DP), N = 32 / L, ROWS = 2;
+  const int c = lane % L;
+  const bool on = 8 * c < p.D;
+  int from[ROWS], hi[ROWS], lo[ROWS], most = 0;
+  float q[ROWS][8], acc[ROWS][8], m[ROWS], l[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    from[i] = __ffs(which) - 1;
+    if (which & (which - 1)) which &= which - 1;  // (else the last one again)
+    hi[i] = __shfl_sync(0xFFFFFFFFu, x.seen.hi, from[i]);
+    lo[i] = __shfl_sync(0xFFFFFFFFu, x.seen.lo, from[i]);
+    most = max(most, hi[i]);
+    const int64_t row = __shfl_sync(0xFFFFFFFFu, x.row, from[i]);
+    const int head = __shfl_sync(0xFFFFFFFFu, x.head, from[i]);
+    float2 y[4];
+    unpack8(on ? ldg128(reinterpret_cast<const uint8_t*>(p.q + row * p.q_stride + (int64_t)head * p.D + 8 * c)) : make_uint4(0, 0, 0, 0), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      q[i][e] = e & 1 ? y[e / 2].y : y[e / 2].x;
+      acc[i][e] = 0.f;
+    }
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+#pragma unroll 1
+  for (int64_t v0 = 0; v0 < most; v0 += 32) {
+    const int64_t v = v0 + lane;  // the lane's key
+    int64_t at, so;
+    key_at(p, k, (uint32_t)v, at, so);
+    float s[ROWS] = {};
+#pragma unroll 4
+    for (int j = 0; j < 32; j += N) {
+      // (loads without a branch: where there is no key, or no dim of the lane's, of any row)
+      const int64_t r = pre_max(__shfl_sync(0xFFFFFFFFu, at, j + lane / L), 0), o = __shfl_sync(0xFFFFFFFFu, so, j + lane / L);
+      float y[8];
+      row8<FMT>(p.c.k + r, on ? c : 0, 1.f, p.c.k_exps() + o, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = on ? y[e] : 0.f;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        float d = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d = fmaf(y[e], q[i][e], d);
+#pragma unroll
+        for (int a = L / 2; a; a >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, a);
+        d = __shfl_sync(0xFFFFFFFFu, d, (lane - j) * L & 31);  // that of key lane, where it is one of these
+        if ((uint32_t)(lane - j) < (uint32_t)N) s[i] = d;
       }
     }
-    float top = s;
+    float w[ROWS];
+    const float unit = (FMT == CF_E4M3 && at >= 0 ? p.c.ks[so] : 1.f) * p.scale;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.f : m1, fall = ex2(m - base), w = ex2(s - base);
-    m = m1;
-    l = l * fall + w;
+    for (int i = 0; i < ROWS; ++i) {
+      const bool seen = at >= 0 && v < hi[i] && (v >= lo[i] || v < x.seen.sk);
+      const float z = seen ? s[i] * unit : -INFINITY;
+      float top = z;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= fall;
-#pragma unroll 1
-    for (int j = 0; j < 32; ++j) {
-      const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j), o = __shfl_sync(0xFFFFFFFFu, so, j);
-      const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
-      if (r < 0 || 8 * lane >= p.D) continue;
-      float x[8];
-      row8<FMT>(p.c.v + r, lane, FMT == CF_E4M3 ? p.c.vs[o] : 1.f, p.c.v_exps() + o, x);
+      for (int a = 16; a; a >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, a));
+      const float m1 = fmaxf(m[i], top), base = m1 == -INFINITY ? 0.f : m1, fall = ex2(m[i] - base), e1 = ex2(z - base);
+      m[i] = m1;
+      l[i] = l[i] * fall + e1;
+      w[i] = seen ? e1 : -1.f;  // (not seen: no product with its value)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(wj, x[e], acc[e]);
+      for (int e = 0; e < 8; ++e) acc[i][e] *= fall;
+    }
+#pragma unroll 4
+    for (int j = 0; j < 32; j += N) {
+      const int64_t r = pre_max(__shfl_sync(0xFFFFFFFFu, at, j + lane / L), 0), o = __shfl_sync(0xFFFFFFFFu, so, j + lane / L);
+      float y[8];
+      row8<FMT>(p.c.v + r, on ? c : 0, FMT == CF_E4M3 ? p.c.vs[o] : 1.f, p.c.v_exps() + o, y);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const float wj = __shfl_sync(0xFFFFFFFFu, w[i], j + lane / L);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float sum = fmaf(wj, y[e], acc[i][e]);
+          acc[i][e] = wj >= 0.f ? sum : acc[i][e];
+        }
+      }
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  if (8 * lane < p.D) {
-    const uint2 a = bf16x4(acc[0] * r, acc[1] * r, acc[2] * r, acc[3] * r), c = bf16x4(acc[4] * r, acc[5] * r, acc[6] * r, acc[7] * r);
-    *reinterpret_cast<uint4*>(p.out + (row * p.Hq + head) * p.D + 8 * lane) = make_uint4(a.x, a.y, c.x, c.y);
+  for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+    for (int a = 16; a; a >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], a);
+    const float r = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int a = L; a < 32; a <<= 1) acc[i][e] += __shfl_xor_sync(0xFFFFFFFFu, acc[i][e], a);
+      acc[i][e] *= r;
+    }
+    const int64_t row = __shfl_sync(0xFFFFFFFFu, x.row, from[i]);
+    const int head = __shfl_sync(0xFFFFFFFFu, x.head, from[i]);
+    if (lane < L && on) {  // (one row twice: the same numbers)
+      const uint2 a = bf16x4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]), b = bf16x4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      *reinterpret_cast<uint4*>(p.out + (row * p.Hq + head) * p.D + 8 * c) = make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+}
+
+// A warp's rows that are not finite (in `rows`, a lane a row; out holds them).
+template <int FMT, int DP>
+__device__ __noinline__ void prefill_again(const PrefillParams& p, const PreKeys k, const PreRow x, uint32_t rows, int lane) {
+  const bool mine = rows >> lane & 1;
+  auto seen = [&](int64_t v0) {  // by the lane's row
+    return bits_below((int)(x.seen.hi - v0)) & (~bits_below((int)(x.seen.lo - v0)) | bits_below((int)(x.seen.sk - v0)));
+  };
+  // ---- parts 0 and 1: the keys that not all of them see, behind the first one's last, in front of the last one's window
+  int hi0 = mine ? x.seen.hi : INT32_MAX, hi1 = mine ? x.seen.hi : 0, lo1 = mine ? x.seen.lo : 0;
+#pragma unroll
+  for (int a = 16; a; a >>= 1) {
+    hi0 = min(hi0, __shfl_xor_sync(0xFFFFFFFFu, hi0, a));
+    hi1 = max(hi1, __shfl_xor_sync(0xFFFFFFFFu, hi1, a));
+    lo1 = max(lo1, __shfl_xor_sync(0xFFFFFFFFu, lo1, a));
+  }
+  uint32_t hidden = 0, unseen = 0, open = rows, dims[8];
+  __syncwarp();  // (what other lanes have written is read, and written again)
+#pragma unroll 1
+  for (int part = 0; part < 3; ++part) {
+    if (part == 2) {
+      // ---- the rows that all of these are finite for: their dims that are not finite (a byte a row, a lane
+      // eight dims), until a visible value accounts for each
+      unseen = __ballot_sync(0xFFFFFFFFu, mine && hidden);
+      open = rows & ~unseen;
+#pragma unroll 1
+      for (int g = 0; g < 8; ++g) {
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t row = __shfl_sync(0xFFFFFFFFu, x.row, 4 * g + i);
+          const int head = __shfl_sync(0xFFFFFFFFu, x.head, 4 * g + i);
+          const bool on = (open >> (4 * g + i) & 1) && 8 * lane < p.D;
+          const uint4 v = on ? *reinterpret_cast<const uint4*>(p.out + (row * p.Hq + head) * p.D + 8 * lane) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) bytes |= (uint32_t)((w[e / 2] >> (16 * (e & 1)) & 0x7F80u) == 0x7F80u) << (8 * i + e);
+        }
+        dims[g] = bytes;
+      }
+    }
+    const int64_t begin = part == 0 ? hi0 : part == 1 ? x.seen.sk : 0, end = part == 0 ? k.keys : part == 1 ? min(lo1, k.keys) : hi1;
+#pragma unroll 1
+    for (int64_t v0 = begin & ~31; open && v0 < end; v0 += 32) {
+      uint32_t keys = not_finite32<FMT, DP>(p, k, (uint32_t)v0, lane);
+      const uint32_t mask = seen(v0);
+      if (part < 2) {
+        hidden |= keys & ~mask;
+        continue;
+      }
+#pragma unroll 1
+      for (; keys && open; keys &= keys - 1) {
+        const int j = __ffs(keys) - 1;
+        int64_t at, so;
+        key_at(p, k, (uint32_t)v0 + j, at, so);
+        const uint32_t its = 8 * lane < p.D ? not_finite8<FMT>(p, at, so, lane) : 0, sees = __ballot_sync(0xFFFFFFFFu, mask >> j & 1);
+        uint32_t left = 0;
+#pragma unroll 1
+        for (int g = 0; g < 8; ++g) {
+          // (a row's bit to each bit of its byte; a byte's any bit to a row's bit)
+          const uint32_t bytes = dims[g] & ~(its * 0x01010101u & ((sees >> (4 * g) & 15) * 0x00204081u & 0x01010101u) * 255u);
+          dims[g] = bytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) left |= (uint32_t)((bytes >> (8 * i) & 255) != 0) << (4 * g + i);
+        }
+        open &= __reduce_or_sync(0xFFFFFFFFu, left);
+      }
+    }
+  }
+#pragma unroll 1
+  for (uint32_t which = unseen | open; which;) {
+    prefill_rows<FMT, DP>(p, k, x, which, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) which &= which - 1;
   }
 }
 
@@ -337,8 +528,6 @@ K3_DEVI uint32_t bf16x2_of(float2 x) {
   const __nv_bfloat162 h = __float22bfloat162_rn(x);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// the low bits of a word: those below x
-K3_DEVI uint32_t bits_below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; }
 
 // a byte pair's E4M3 codes as bf16 (exact)
 K3_DEVI void e4m3x4_bf16(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -513,10 +702,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       const int tok = r / it.heads, head = it.head0 + (r - tok * it.heads);
       const bool valid = tok < it.ntok;
       const int32_t pos = it.pos0 + min(tok, it.ntok - 1);
-      // visible: keys below hi that are at least lo or below sk
-      const int hi_v = max(0, min(pos + 1 - it.f + it.ns, it.keys));
-      const int lo_v = p.window > 0 ? (pos >= p.window ? pos - p.window + 1 : 0) - it.f + it.ns : 0;
-      const int sk_v = p.window > 0 ? p.sinks : 0;
+      const PreSeen keys_seen(p, pos, it.f, it.ns, it.keys);
       // the maximum, in units of 2^unit; the sum of weights
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -530,7 +716,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
         const float* const ks = reinterpret_cast<const float*>(__cvta_shared_to_generic(scales_at + ring * 2 * BN * 4));
         const float* const vs = ks + BN;
         const uint4 ok4 = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(masks_at + ring * 16));
-        const int hi = hi_v - v0, lo = lo_v - v0, sk = sk_v - v0;
+        const int hi = keys_seen.hi - v0, lo = keys_seen.lo - v0, sk = keys_seen.sk - v0;
         const bool all_rows = (ok4.x & ok4.y & (BN > 64 ? ok4.z & ok4.w : ~0u)) == ~0u;
         const bool masked = !__all_sync(0xFFFFFFFFu, all_rows && hi >= BN && (lo <= 0 || sk >= BN));
         // Logits are read twice, for the maximum and for the weights: tensor memory is as near as registers,
@@ -730,13 +916,9 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       }
       if (final) {
         if (valid && p.lse) p.lse[row * p.Hq + head] = lse_of(base, l);
-        uint32_t again = __ballot_sync(0xFFFFFFFFu, valid && largest >= 0x7F800000u && l < INFINITY);
-        while (again) {
-          const int from = __ffs(again) - 1;
-          again &= again - 1;
-          prefill_row<FMT>(p, it.b, it.kvh, __shfl_sync(0xFFFFFFFFu, head, from), __shfl_sync(0xFFFFFFFFu, row, from),
-                           __shfl_sync(0xFFFFFFFFu, pos, from), lane);
-        }
+        const uint32_t again = __ballot_sync(0xFFFFFFFFu, valid && largest >= 0x7F800000u && l < INFINITY);
+        if (__builtin_expect(again != 0, 0))
+          prefill_again<FMT, DP>(p, PreKeys{it.b, it.kvh, it.f, it.ns, it.keys, it.len}, PreRow{keys_seen, head, row}, again, lane);
       }
     }
     if (half >= HALVES)
