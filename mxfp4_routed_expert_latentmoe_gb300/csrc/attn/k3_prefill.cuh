@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       };
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (n_late > 0) {
-          if (n_late < 4 && __all_sync(0xFFFFFFFFu, mb_try(bar, parity))) return true;
+          if (n_late < 4 && __all_sync(0xFFFFFFFFu, mb_test(bar, parity))) return true;
           while (n_late > 0) landed();
         }
         return (bool)__all_sync(0xFFFFFFFFu, mb_wait(bar, parity, gave_up));
@@ -1063,7 +1063,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
           on_the_way(full);
         };
         while (ok) {
-          if (n_late > 0 && !__all_sync(0xFFFFFFFFu, mb_try(i_full(taken % ITEMS), (taken / ITEMS) & 1)))
+          if (n_late > 0 && !__all_sync(0xFFFFFFFFu, mb_test(i_full(taken % ITEMS), (taken / ITEMS) & 1)))
             while (n_late > 0) landed();
           if (!take(it)) break;
           look_up(it.kt0, false);

@@ -36,6 +36,16 @@ K3_DEVI bool mb_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// whether the phase is through, without waiting
+K3_DEVI bool mb_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Waits for the phase of the given parity; false if the block has given up, or after MB_LOOKS looks of
 // some 7800 clocks each, about a minute (then it has).  The longest that a block's warps wait for one
 // another is for rows that are formed again: 1 to 5 s for a tile over half a million tokens (64 to 256 dims).
