@@ -11,7 +11,7 @@
 // memory, row by row through the page table (any page size, any strides); 14 says which tile is
 // next; 15 issues the products.
 //
-// The work, tiles times keys, stands in a line (each tile's start counts as PRE_START keys) and is
+// The work, tiles times keys, stands in a line (each tile's start counts as some keys, pre_start) and is
 // dealt out evenly to the blocks, whatever the lengths and masks; a tile that is cut leaves an
 // unnormalised record of each part in the workspace, and the part that arrives last joins them, in
 // order.
@@ -23,14 +23,13 @@
 // to bf16 anyway (8192-token prompt: results off by 2.2e-3 in the mean square, 1.65e-3 with fp32 weights).
 //
 // What bounds it (GB300, clocks a tile of 128 keys and 256 rows of 128 dims, measured with clock reads in
-// a copy).  bf16, 8192-token prompt, 64 query and 8 key heads: 1.10 ms, 1000 TFLOP/s, 53% of the burst
+// a copy).  bf16, 8192-token prompt, 64 query and 8 key heads: 1.02 ms, 1075 TFLOP/s, 57% of the burst
 // rate; the products take 2048 clocks of 4900, the rest is the chain of a half: from logits to the first
 // weights 1500, to the last 2500 (maximum 700, then 32 logits at a time; the two halves' warps share the
-// issue slots, neither pipe is full), then its turn at the tensor core; and a tile's start, 20000 clocks
-// (queries once the last products are through, the sums' way out), for which PRE_START stands: 768
-// keys, 1396 us at 256, 1202 at 512, 1118 at 1024.  Codes: the copying warps (a chunk of 1500 behind
-// 30001 tokens, MXFP4: 1.93 ms, 41% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses and
-// copies; E4M3 in a window of 1000: 0.57 ms), and for few rows (drafts: 200 us) the chain of one half.
+// issue slots, neither pipe is full), then its turn at the tensor core; and a tile's start, some 14000 clocks
+// (queries once the last products are through, the sums' way out; pre_start).  Codes: the copying warps (a chunk of
+// 1500 behind 30001 tokens, MXFP4: 1.92 ms, 41% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses
+// and copies; E4M3 in a window of 1000: 0.56 ms), and for few rows (drafts: 200 us) the chain of one half.
 // Ten copying warps of 64 registers instead of six of 96 were 6 to 20% slower, rows of codes as bulk
 // copies of a row each (some 85 clocks to issue one) 35%.
 #pragma once
@@ -39,6 +38,24 @@
 #include "k3_tmem.cuh"
 
 namespace k3 {
+
+// What a tile's start counts as, in keys.  A tile of n tiles of keys (windowed prompts, 8 query heads a key
+// head) takes, in us: bf16 of 64 dims 5.5 + 2.33 n, 128 dims 6.7 + 2.69 n, 192 dims 3.6 + 1.86 n, 256 dims 3.2 + 2.31 n;
+// E4M3 5.5 + 2.84 n, 6.5 + 3.64 n, 4.7 + 2.65 n, 4.3 + 3.13 n; MXFP4 6.5 + 3.03 n, 9.6 + 3.16 n, 4.7 + 2.97 n, 4.8 + 3.04 n:
+// 230 to 390 keys with two halves, 90 to 120 with one.  Measured best: somewhat more, as a block's
+// first tile has none of its start hidden (8192-token prompts, 64/8 heads, us: bf16 of 128 dims 1093, 1049,
+// 1025, 1027, 1045 at 256, 320, 384, 512, 768 keys, of 192 dims 2866, 2729, 2627, 2642, 2690 at 64, 128, 192, 256, 384;
+// E4M3 of 128 dims 1780, 1708, 1713, 1724, 1747 at 128, 256, 320, 384, 512; six E4M3 prompts of up to 3000,
+// 192 dims: 873, 809, 844, 859 at 64, 128, 192, 256).
+constexpr int PRE_START = 384;
+K3_HD constexpr int pre_start(bool bf16, bool two_halves) { return two_halves ? (bf16 ? PRE_START : 320) : (bf16 ? 192 : 128); }
+// The fewest keys of a block: where the work gives them less, tiles have a block each, and only what is longer is cut
+// (128: 4 tokens behind 8000, 32/8 heads of 128, bf16 87 us, 77 at 512; 1024: 8 single tokens behind 500 34 us, 28).
+// Tiles of keys up to which a tile is not cut, as its join would take longer (1: 8192 tokens and less
+// as at 2; 4: up to 30% less for tiles of 3 and 4, 700 tokens of 256 dims 62 us instead of 49).
+constexpr int PRE_LEAST = 512, PRE_WHOLE = 2;
+static_assert(PRE_LEAST >= 128, "a block without a tile of keys in the middle of a tile's");
+constexpr int PRE_MAX_BLOCKS = 192;
 
 struct PrefillParams {
   const uint16_t* q;
@@ -55,15 +72,12 @@ struct PrefillParams {
   uint32_t* arrived;  // two counters a block, zero between calls
   float* parts;       // two records a block
   int32_t boxes;      // whether rows of bf16 may come in boxes of 8 tokens of a page
+  int32_t start = PRE_START;
 };
 struct PrefillMaps {
   CUtensorMap k, v;  // dims, tokens of a page, heads, pages
 };
 
-// What a tile's start counts as (see above), the fewest keys of a block, tiles of keys up to which a tile is
-// not cut (its join would take longer).
-constexpr int PRE_START = 768, PRE_LEAST = 512, PRE_WHOLE = 2;
-constexpr int PRE_MAX_BLOCKS = 192;
 constexpr int PRE_COPY_WARPS = 6, PRE_THREADS = 256 + 32 * PRE_COPY_WARPS + 64;
 // Registers of a thread: at the launch, then of the 256 of the softmax and of the others
 constexpr int PRE_REGS = 128, PRE_REGS_SOFTMAX = 160, PRE_REGS_OTHERS = 96;
@@ -77,7 +91,7 @@ K3_HD int64_t pre_max(int64_t a, int64_t b) { return a > b ? a : b; }
 // order: the sinks in front of the first token's window, then that window's and the rest.
 struct PreSeq {
   int64_t n, old, W, S;
-  int32_t TT;
+  int32_t TT, start = PRE_START;
   K3_HD int64_t tiles() const { return (n + TT - 1) / TT; }
   K3_HD int64_t keys(int64_t m) const {
     const int64_t p0 = old + m * TT, p1 = old + pre_min(n, (m + 1) * TT), f = W > 0 ? pre_max(0, p0 - W + 1) : 0;
@@ -93,8 +107,8 @@ struct PreSeq {
       const int64_t t = S + W - 1 - old;
       x = pre_min(full, t < 0 ? 0 : t / TT + 1);
     }
-    int64_t at = x * old + TT * (x * (x + 1) / 2) + (full - x) * (TT - 1 + W + S) + full * PRE_START;
-    if (m >= all) at += keys(all - 1) + PRE_START;
+    int64_t at = x * old + TT * (x * (x + 1) / 2) + (full - x) * (TT - 1 + W + S) + full * start;
+    if (m >= all) at += keys(all - 1) + start;
     return at;
   }
 };
@@ -109,8 +123,13 @@ K3_HD bool pre_bounds(const PrefillParams& p, int b, int32_t& s0, int32_t& n, in
   len = l < 0 ? 0 : l > most ? (int32_t)most : l;
   return s0 == a && s1 == e && len == l && len >= n;
 }
-K3_HD PreSeq pre_seq(const PrefillParams& p, int32_t n, int32_t len) {
-  return PreSeq{n, len > n ? len - n : 0, p.window, p.sinks, p.tokens};
+K3_HD PreSeq pre_seq(const PrefillParams& p, int32_t n, int32_t len, int32_t start) {
+  return PreSeq{n, len > n ? len - n : 0, p.window, p.sinks, p.tokens, start};
+}
+K3_HD PreSeq pre_seq(const PrefillParams& p, int32_t n, int32_t len) { return pre_seq(p, n, len, p.start); }
+// What a start counts as in a call of `total` places with p.start: a block's least where blocks have less.
+K3_HD int32_t pre_start_in(const PrefillParams& p, int64_t total, int64_t blocks) {
+  return total < blocks * PRE_LEAST && p.start < PRE_LEAST ? PRE_LEAST : p.start;
 }
 
 // One part of a tile, as the block's warps get it.
@@ -127,12 +146,13 @@ struct PreItem {
 struct PreWalk {
   int64_t x, end, chunk;  // place of the tile's first key, end of the block's range, places of a block
   int64_t m;
-  int32_t b, h, kt, s0, n, len, bn;
+  int32_t b, h, kt, s0, n, len, bn, start = 0;  // start: 0 as p has it
+  K3_HD int32_t start_of(const PrefillParams& p) const { return start ? start : p.start; }
   K3_HD void seq(const PrefillParams& p) { pre_bounds(p, b, s0, n, len); }
   // the block's first item: its range begins `off` places after sequence b's start
   K3_HD void land(const PrefillParams& p, int64_t off) {
     seq(p);
-    const PreSeq s = pre_seq(p, n, len);
+    const PreSeq s = pre_seq(p, n, len, start_of(p));
     const int64_t all = s.tiles(), each = s.place(all);
     const int64_t hh = off / each, rem = off - hh * each;
     h = (int32_t)hh;
@@ -145,7 +165,7 @@ struct PreWalk {
         hi = mid;
     }
     m = lo;
-    x = end - chunk - rem + s.place(m) + PRE_START;  // (end - chunk: the block's first place)
+    x = end - chunk - rem + s.place(m) + start_of(p);  // (end - chunk: the block's first place)
     const int64_t first = end - chunk, nkt = (s.keys(m) + bn - 1) / bn;
     kt = 0;
     if (first > x) {
@@ -157,8 +177,8 @@ struct PreWalk {
     }
   }
   K3_HD void next(const PrefillParams& p) {
-    const PreSeq s = pre_seq(p, n, len);
-    x += s.keys(m) + PRE_START;
+    const PreSeq s = pre_seq(p, n, len, start_of(p));
+    x += s.keys(m) + start_of(p);
     kt = 0;
     if (++m < s.tiles()) return;
     m = 0;
@@ -174,7 +194,7 @@ struct PreWalk {
   K3_HD bool item(const PrefillParams& p, PreItem& it) {
     it.end = 1;
     if (b >= p.B || (kt == 0 && x >= end)) return false;
-    const PreSeq s = pre_seq(p, n, len);
+    const PreSeq s = pre_seq(p, n, len, start_of(p));
     const int64_t keys = s.keys(m), nkt = (keys + bn - 1) / bn;
     int64_t k1 = nkt <= PRE_WHOLE ? nkt : pre_min(nkt, (end - x + bn - 1) / bn);
     it.end = 0;
@@ -570,6 +590,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
   __shared__ int64_t s_sum[PRE_THREADS / 32], s_off;
+  __shared__ uint32_t s_tiles[PRE_THREADS / 32];
   __shared__ int32_t s_b, s_last[2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -630,21 +651,31 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   const int HR = p.Hkv * p.groups;
   const int each = (p.B + PRE_THREADS - 1) / PRE_THREADS, b_lo = min(p.B, (int)threadIdx.x * each), b_hi = min(p.B, b_lo + each);
   int64_t mine = 0;
+  uint32_t tiles_mine = 0;  // (used where there are few: they may wrap)
   bool bad = false;
   for (int b = b_lo; b < b_hi; ++b) {
     int32_t s0, n, len;
     bad |= !pre_bounds(p, b, s0, n, len);
     const PreSeq s = pre_seq(p, n, len);
     mine += s.place(s.tiles()) * HR;
+    tiles_mine += (uint32_t)s.tiles() * HR;
   }
   if (bad && blockIdx.x == 0) flag_status(p.status, K3ATTN_DEV_BAD_LENGTH);
   int64_t upto = mine;
+  uint32_t tiles_upto = tiles_mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-    if (lane >= o) upto += v;
+    const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, tiles_upto, o);
+    if (lane >= o) {
+      upto += v;
+      tiles_upto += n;
+    }
   }
-  if (lane == 31) s_sum[warp] = upto;
+  if (lane == 31) {
+    s_sum[warp] = upto;
+    s_tiles[warp] = tiles_upto;
+  }
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -652,9 +683,20 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
   grid_dep_launch();
   const uint32_t tmem = s_tmem;
   int64_t total = 0;
+  uint32_t tiles_total = 0;
   for (int w = 0; w < PRE_THREADS / 32; ++w) {
-    if (w == warp) upto += total;
+    if (w == warp) {
+      upto += total;
+      tiles_upto += tiles_total;
+    }
     total += s_sum[w];
+    tiles_total += s_tiles[w];
+  }
+  const int32_t start = pre_start_in(p, total, gridDim.x);
+  if (start != p.start) {
+    mine += tiles_mine * (start - p.start);
+    upto += tiles_upto * (start - p.start);
+    total += tiles_total * (start - p.start);
   }
   const int64_t chunk = pre_chunk(total, gridDim.x), first = blockIdx.x * chunk;
   if (mine > 0 && first >= upto - mine && first < upto) {
@@ -662,7 +704,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
     for (int b = b_lo;; ++b) {
       int32_t s0, n, len;
       pre_bounds(p, b, s0, n, len);
-      const PreSeq s = pre_seq(p, n, len);
+      const PreSeq s = pre_seq(p, n, len, start);
       const int64_t here = s.place(s.tiles()) * HR;
       if (first < before + here) {
         s_b = b;
@@ -1225,6 +1267,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1)
       if (lane == 0) {
         PreWalk walk;
         walk.bn = BN;
+        walk.start = start;
         walk.chunk = chunk;
         walk.end = first + chunk;
         walk.b = p.B;

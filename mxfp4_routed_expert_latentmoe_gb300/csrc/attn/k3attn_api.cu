@@ -408,6 +408,7 @@ k3moe_status k3attn_prefill(const k3attn_dims* dims, int32_t n_sinks, int32_t B,
   p.groups = (p.G + rows - 1) / rows;
   p.heads = (p.G + p.groups - 1) / p.groups;
   p.tokens = rows / p.heads;
+  p.start = pre_start(cache->format == K3ATTN_BF16, rows == 256);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.arrived = reinterpret_cast<uint32_t*>(w + kCounters);
   p.parts = reinterpret_cast<float*>(w + kRecords);
