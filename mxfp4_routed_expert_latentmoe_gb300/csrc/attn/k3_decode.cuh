@@ -522,7 +522,9 @@ __global__ void __launch_bounds__(DecCfg<FMT, DP, NT>::WARPS * 32, 1) k3_decode_
         uint32_t t = ahead.token<TW>(W, tw, lane & (TW - 1));
         r.in = t < (uint32_t)ahead.n;
         if (r.in) {
-          t = ahead.seen(p, t);
+          // (without sinks nothing to do: 201 windowed sequences, 12 heads on E4M3 rows of 192: 64.6 us, 65.9 with
+          // the arithmetic always; MXFP4 the other way round, 64 sequences up to 8192: 107.6 us always, 108.8)
+          if (FMT == CF_MXFP4 || p.sinks > 0) t = ahead.seen(p, t);
           const uint32_t pg = p.c.by_page(t);
           r.entry = __ldg(p.table + (int64_t)ahead.b * p.table_width + pg);
           r.in_page = (int32_t)(t - pg * (uint32_t)p.c.page_size);
