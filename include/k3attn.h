@@ -173,8 +173,9 @@ k3moe_status k3attn_kv_read(const k3attn_dims* dims, int32_t T, const int32_t* s
  * Logits, softmax statistics and sums are held in fp32, powers of two to 2^-22.  A token's weight
  * enters the sum of values rounded to the type of its product, bf16 for a K3ATTN_BF16 cache (off
  * by 2^-8 of itself at most), fp16 for the others (2^-11, or 2^-40 of the largest); the sum of
- * weights is of the unrounded ones.  K3ATTN_MXFP4: the 32 values of a row whose scale is 2^25 and
- * more below the largest of the row's scales count as zeros.  The result is rounded to bf16 once. */
+ * weights is of the unrounded ones.  K3ATTN_MXFP4 rounds it once more for each 32 values of a row,
+ * whose scale may be 2^d below the largest of the row's: by 2^-11 of itself again, or 2^(d - 40) of the
+ * largest; with d of 25 and more the 32 values count as zeros.  The result is rounded to bf16 once. */
 k3moe_status k3attn_decode(const k3attn_dims* dims, int32_t B, const uint16_t* q, int64_t q_stride,
                            const k3attn_cache* cache, const int32_t* page_table, int32_t table_width,
                            const int32_t* lens, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
