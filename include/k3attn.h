@@ -210,8 +210,8 @@ k3moe_status k3attn_decode_sinks(const k3attn_dims* dims, int32_t n_sinks, int32
  * codes, so that queries of more than about 1e33 leave fp32 there.  A value that is infinite or NaN has
  * a part in no token that does not attend to it.  Those next to it that do not (up to 256 tokens) are
  * formed again in a slower pass, and so are tokens whose sums of finite values leave fp32's range with
- * weights of up to 2^8 (values of 1e36 and more): 1 to 5 s over half a million tokens; from some 2^22
- * tokens on it may outlast the other warps' waits (K3ATTN_TIMEOUT).
+ * weights of up to 2^8 (values of 1e36 and more), or that see infinities of both signs: 0.5 to 3 s over
+ * half a million tokens; from some 2^23 tokens on it may outlast the other warps' waits (K3ATTN_TIMEOUT).
  * ws: k3attn_prefill_workspace_bytes(dims) bytes (0 for invalid dims), readied by
  * k3attn_workspace_init; such a workspace serves k3attn_decode and the other calls too. */
 size_t k3attn_prefill_workspace_bytes(const k3attn_dims* dims);

@@ -233,17 +233,33 @@ struct PreSeen {
 K3_HD int64_t pre_chunk(int64_t total, int64_t blocks) { return pre_max(PRE_LEAST, (total + blocks - 1) / blocks); }
 
 // ---------------------------------------------------------------------------- rows one by one
-// eight values of a cached row
+// eight values of a cached row: as they are stored, and as numbers
+struct Eight {
+  uint4 v;
+  uint32_t exp;
+};
 template <int FMT>
-K3_DEVI void row8(const uint8_t* row, int chunk, float scale, const uint8_t* exps, float (&x)[8]) {
-  uint4 v = {};
+K3_DEVI Eight load8(const uint8_t* row, int chunk, const uint8_t* exps) {
+  Eight r{};
   if constexpr (FMT == CF_BF16) {
-    v = ldg128(row + 16 * chunk);
+    r.v = ldg128(row + 16 * chunk);
   } else if constexpr (FMT == CF_E4M3) {
     const uint2 c = ldg64(row + 8 * chunk);
+    r.v.x = c.x;
+    r.v.y = c.y;
+  } else {
+    r.v.x = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * chunk));
+    r.exp = __ldg(exps + chunk / 4);
+  }
+  return r;
+}
+template <int FMT>
+K3_DEVI void values8(const Eight& r, float scale, float (&x)[8]) {
+  uint4 v = r.v;
+  if constexpr (FMT == CF_E4M3) {
     uint32_t h[4];
-    e4m3x4_f16x4(c.x, h[0], h[1]);
-    e4m3x4_f16x4(c.y, h[2], h[3]);
+    e4m3x4_f16x4(v.x, h[0], h[1]);
+    e4m3x4_f16x4(v.y, h[2], h[3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
@@ -251,9 +267,8 @@ K3_DEVI void row8(const uint8_t* row, int chunk, float scale, const uint8_t* exp
       x[2 * i + 1] = f.y * scale;
     }
     return;
-  } else {
-    v = e2m1x8_bf16(__ldg(reinterpret_cast<const uint32_t*>(row + 4 * chunk)), exps[chunk / 4]);
   }
+  if constexpr (FMT == CF_MXFP4) v = e2m1x8_bf16(v.x, r.exp);
   float2 y[4];
   unpack8(v, y);
 #pragma unroll
@@ -267,11 +282,11 @@ K3_DEVI void row8(const uint8_t* row, int chunk, float scale, const uint8_t* exp
 K3_DEVI uint32_t bits_below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; }
 
 // A tile's products take every row of values, and weight 0 times a value that is infinite or NaN is NaN.  A
-// row of the result that is not finite has
-//   seen such a value itself, in each of its dims that are not finite: then it is right;
-//   or not seen one that a tile of its keys holds, behind its position or in front of its window;
-//   or sums of finite values have left fp32's range on the way, with weights of up to 2^8.
-// prefill_again tells them apart and forms the latter two again, over their visible keys alone.
+// row of the result that is not finite is right if it has seen a NaN in each dim that is NaN and an infinity in
+// each that is infinite.  Else one of its tile's keys has such a value that it does not see, behind its position
+// or in front of its window (or infinities of both signs are there, or its weight has vanished), or sums of
+// finite values have left fp32's range on the way, with weights of up to 2^8: prefill_again forms the row again,
+// over its visible keys alone.
 struct PreKeys {
   int32_t b, kvh, f, ns, keys, len;  // as PreItem's
 };
@@ -294,15 +309,22 @@ K3_DEVI void key_at(const PrefillParams& p, const PreKeys& k, uint32_t v, int64_
   at = entry * p.c.page + k.kvh * p.c.head + in_page * p.c.tok;
   so = entry * p.c.spage + k.kvh * p.c.shead + in_page * p.c.stok;
 }
-// which of eight values of a row are not finite
+// which of eight values are NaN (bits 0 .. 7), and infinite (8 .. 15)
 template <int FMT>
-K3_DEVI uint32_t not_finite8(const PrefillParams& p, int64_t at, int64_t so, int chunk) {
+K3_DEVI uint32_t not_finite_of(const Eight& v, float scale) {
   float x[8];
-  row8<FMT>(p.c.v + at, chunk, FMT == CF_E4M3 ? p.c.vs[so] : 1.f, p.c.v_exps() + so, x);
+  values8<FMT>(v, scale, x);
   uint32_t bits = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) bits |= (uint32_t)((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) << e;
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    bits |= (uint32_t)(m > 0x7F800000u) << e | (uint32_t)(m == 0x7F800000u) << (8 + e);
+  }
   return bits;
+}
+template <int FMT>
+K3_DEVI uint32_t not_finite8(const PrefillParams& p, int64_t at, int64_t so, int chunk) {
+  return not_finite_of<FMT>(load8<FMT>(p.c.v + at, chunk, p.c.v_exps() + so), FMT == CF_E4M3 ? __ldg(p.c.vs + so) : 1.f);
 }
 // which of the keys v0 .. v0 + 31 have a value that is not finite
 template <int FMT, int DP>
@@ -311,15 +333,26 @@ K3_DEVI uint32_t not_finite32(const PrefillParams& p, const PreKeys& k, uint32_t
   int64_t at, so;
   key_at(p, k, v0 + lane, at, so);
   uint32_t keys = 0;
-#pragma unroll 4
-  for (int j = 0; j < 32; j += N) {
-    const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j + lane / L), o = __shfl_sync(0xFFFFFFFFu, so, j + lane / L);
-    const bool on = r >= 0 && 8 * (lane % L) < p.D;  // (else any row's: loads without a branch)
-    const uint32_t bits = not_finite8<FMT>(p, on ? r : 0, on ? o : 0, on ? lane % L : 0);
-    const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, on && bits);
+  constexpr int AT_ONCE = 8;  // loads on the way
+#pragma unroll 1
+  for (int j0 = 0; j0 < 32; j0 += AT_ONCE * N) {
+    Eight e[AT_ONCE];
+    float scale[AT_ONCE];
+    bool on[AT_ONCE];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (lanes >> (n * L) & (0xFFFFFFFFu >> (32 - L))) keys |= 1u << (j + n);
+    for (int a = 0; a < AT_ONCE; ++a) {
+      const int64_t r = __shfl_sync(0xFFFFFFFFu, at, j0 + a * N + lane / L), o = __shfl_sync(0xFFFFFFFFu, so, j0 + a * N + lane / L);
+      on[a] = r >= 0 && 8 * (lane % L) < p.D;  // (else any row's: loads without a branch)
+      e[a] = load8<FMT>(p.c.v + (on[a] ? r : 0), on[a] ? lane % L : 0, p.c.v_exps() + (on[a] ? o : 0));
+      scale[a] = FMT == CF_E4M3 ? __ldg(p.c.vs + (on[a] ? o : 0)) : 1.f;
+    }
+#pragma unroll
+    for (int a = 0; a < AT_ONCE; ++a) {
+      const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, on[a] && not_finite_of<FMT>(e[a], scale[a]));
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (lanes >> (n * L) & (0xFFFFFFFFu >> (32 - L))) keys |= 1u << (j0 + a * N + n);
+    }
   }
   return keys;
 }
@@ -328,7 +361,7 @@ K3_DEVI uint32_t not_finite32(const PrefillParams& p, const PreKeys& k, uint32_t
 // a key, then a lane a key for the weights.
 template <int FMT, int DP>
 K3_DEVI void prefill_rows(const PrefillParams& p, const PreKeys& k, const PreRow& x, uint32_t which, int lane) {
-  constexpr int L = key_lanes(DP), N = 32 / L, ROWS = 2;
+  constexpr int L = key_lanes(DP), N = 32 / L, ROWS = 2, AT_ONCE = 8;  // (loads of keys on the way)
   const int c = lane % L;
   const bool on = 8 * c < p.D;
   int from[ROWS], hi[ROWS], lo[ROWS], most = 0;
@@ -358,23 +391,30 @@ K3_DEVI void prefill_rows(const PrefillParams& p, const PreKeys& k, const PreRow
     int64_t at, so;
     key_at(p, k, (uint32_t)v, at, so);
     float s[ROWS] = {};
-#pragma unroll 4
-    for (int j = 0; j < 32; j += N) {
+#pragma unroll 1
+    for (int j0 = 0; j0 < 32; j0 += AT_ONCE * N) {
+      Eight e[AT_ONCE];
       // (loads without a branch: where there is no key, or no dim of the lane's, of any row)
-      const int64_t r = pre_max(__shfl_sync(0xFFFFFFFFu, at, j + lane / L), 0), o = __shfl_sync(0xFFFFFFFFu, so, j + lane / L);
-      float y[8];
-      row8<FMT>(p.c.k + r, on ? c : 0, 1.f, p.c.k_exps() + o, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = on ? y[e] : 0.f;
+      for (int a = 0; a < AT_ONCE; ++a) {
+        const int64_t r = pre_max(__shfl_sync(0xFFFFFFFFu, at, j0 + a * N + lane / L), 0), o = __shfl_sync(0xFFFFFFFFu, so, j0 + a * N + lane / L);
+        e[a] = load8<FMT>(p.c.k + r, on ? c : 0, p.c.k_exps() + o);
+      }
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        float d = 0.f;
+      for (int a = 0; a < AT_ONCE; ++a) {
+        const int j = j0 + a * N;
+        float y[8];
+        values8<FMT>(e[a], 1.f, y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d = fmaf(y[e], q[i][e], d);
+        for (int i = 0; i < ROWS; ++i) {
+          float d = 0.f;
 #pragma unroll
-        for (int a = L / 2; a; a >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, a);
-        d = __shfl_sync(0xFFFFFFFFu, d, (lane - j) * L & 31);  // that of key lane, where it is one of these
-        if ((uint32_t)(lane - j) < (uint32_t)N) s[i] = d;
+          for (int x8 = 0; x8 < 8; ++x8) d = fmaf(on ? y[x8] : 0.f, q[i][x8], d);
+#pragma unroll
+          for (int b = L / 2; b; b >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, b);
+          d = __shfl_sync(0xFFFFFFFFu, d, (lane - j) * L & 31);  // that of key lane, where it is one of these
+          if ((uint32_t)(lane - j) < (uint32_t)N) s[i] = d;
+        }
       }
     }
     float w[ROWS];
@@ -393,18 +433,28 @@ K3_DEVI void prefill_rows(const PrefillParams& p, const PreKeys& k, const PreRow
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[i][e] *= fall;
     }
-#pragma unroll 4
-    for (int j = 0; j < 32; j += N) {
-      const int64_t r = pre_max(__shfl_sync(0xFFFFFFFFu, at, j + lane / L), 0), o = __shfl_sync(0xFFFFFFFFu, so, j + lane / L);
-      float y[8];
-      row8<FMT>(p.c.v + r, on ? c : 0, FMT == CF_E4M3 ? p.c.vs[o] : 1.f, p.c.v_exps() + o, y);
+#pragma unroll 1
+    for (int j0 = 0; j0 < 32; j0 += AT_ONCE * N) {
+      Eight e[AT_ONCE];
+      float scale[AT_ONCE];
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const float wj = __shfl_sync(0xFFFFFFFFu, w[i], j + lane / L);
+      for (int a = 0; a < AT_ONCE; ++a) {
+        const int64_t r = pre_max(__shfl_sync(0xFFFFFFFFu, at, j0 + a * N + lane / L), 0), o = __shfl_sync(0xFFFFFFFFu, so, j0 + a * N + lane / L);
+        e[a] = load8<FMT>(p.c.v + r, on ? c : 0, p.c.v_exps() + o);
+        scale[a] = FMT == CF_E4M3 ? __ldg(p.c.vs + o) : 1.f;
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float sum = fmaf(wj, y[e], acc[i][e]);
-          acc[i][e] = wj >= 0.f ? sum : acc[i][e];
+      for (int a = 0; a < AT_ONCE; ++a) {
+        float y[8];
+        values8<FMT>(e[a], scale[a], y);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          const float wj = __shfl_sync(0xFFFFFFFFu, w[i], j0 + a * N + lane / L);
+#pragma unroll
+          for (int x8 = 0; x8 < 8; ++x8) {
+            const float sum = fmaf(wj, y[x8], acc[i][x8]);
+            acc[i][x8] = wj >= 0.f ? sum : acc[i][x8];
+          }
         }
       }
     }
@@ -432,73 +482,63 @@ K3_DEVI void prefill_rows(const PrefillParams& p, const PreKeys& k, const PreRow
 // A warp's rows that are not finite (in `rows`, a lane a row; out holds them).
 template <int FMT, int DP>
 __device__ __noinline__ void prefill_again(const PrefillParams& p, const PreKeys k, const PreRow x, uint32_t rows, int lane) {
-  const bool mine = rows >> lane & 1;
   auto seen = [&](int64_t v0) {  // by the lane's row
     return bits_below((int)(x.seen.hi - v0)) & (~bits_below((int)(x.seen.lo - v0)) | bits_below((int)(x.seen.sk - v0)));
   };
-  // ---- parts 0 and 1: the keys that not all of them see, behind the first one's last, in front of the last one's window
-  int hi0 = mine ? x.seen.hi : INT32_MAX, hi1 = mine ? x.seen.hi : 0, lo1 = mine ? x.seen.lo : 0;
-#pragma unroll
-  for (int a = 16; a; a >>= 1) {
-    hi0 = min(hi0, __shfl_xor_sync(0xFFFFFFFFu, hi0, a));
-    hi1 = max(hi1, __shfl_xor_sync(0xFFFFFFFFu, hi1, a));
-    lo1 = max(lo1, __shfl_xor_sync(0xFFFFFFFFu, lo1, a));
-  }
-  uint32_t hidden = 0, unseen = 0, open = rows, dims[8];
+  // ---- the rows' dims that are NaN, and infinite, a byte a row, a lane eight dims
+  uint32_t dims[2][8];
+  int end = 0;  // of the keys that any of them sees
   __syncwarp();  // (what other lanes have written is read, and written again)
 #pragma unroll 1
-  for (int part = 0; part < 3; ++part) {
-    if (part == 2) {
-      // ---- the rows that all of these are finite for: their dims that are not finite (a byte a row, a lane
-      // eight dims), until a visible value accounts for each
-      unseen = __ballot_sync(0xFFFFFFFFu, mine && hidden);
-      open = rows & ~unseen;
-#pragma unroll 1
-      for (int g = 0; g < 8; ++g) {
-        uint32_t bytes = 0;
+  for (int g = 0; g < 8; ++g) {
+    uint32_t nan = 0, inf = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t row = __shfl_sync(0xFFFFFFFFu, x.row, 4 * g + i);
-          const int head = __shfl_sync(0xFFFFFFFFu, x.head, 4 * g + i);
-          const bool on = (open >> (4 * g + i) & 1) && 8 * lane < p.D;
-          const uint4 v = on ? *reinterpret_cast<const uint4*>(p.out + (row * p.Hq + head) * p.D + 8 * lane) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, x.row, 4 * g + i);
+      const int head = __shfl_sync(0xFFFFFFFFu, x.head, 4 * g + i), hi = __shfl_sync(0xFFFFFFFFu, x.seen.hi, 4 * g + i);
+      const bool there = rows >> (4 * g + i) & 1;
+      if (there) end = max(end, hi);
+      const uint4 v = there && 8 * lane < p.D ? *reinterpret_cast<const uint4*>(p.out + (row * p.Hq + head) * p.D + 8 * lane)
+                                              : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) bytes |= (uint32_t)((w[e / 2] >> (16 * (e & 1)) & 0x7F80u) == 0x7F80u) << (8 * i + e);
-        }
-        dims[g] = bytes;
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = w[e / 2] >> (16 * (e & 1)) & 0x7FFFu;
+        nan |= (uint32_t)(m > 0x7F80u) << (8 * i + e);
+        inf |= (uint32_t)(m == 0x7F80u) << (8 * i + e);
       }
     }
-    const int64_t begin = part == 0 ? hi0 : part == 1 ? x.seen.sk : 0, end = part == 0 ? k.keys : part == 1 ? min(lo1, k.keys) : hi1;
+    dims[0][g] = nan;
+    dims[1][g] = inf;
+  }
+  // ---- until a visible value accounts for each
+  uint32_t open = rows;
 #pragma unroll 1
-    for (int64_t v0 = begin & ~31; open && v0 < end; v0 += 32) {
-      uint32_t keys = not_finite32<FMT, DP>(p, k, (uint32_t)v0, lane);
-      const uint32_t mask = seen(v0);
-      if (part < 2) {
-        hidden |= keys & ~mask;
-        continue;
-      }
+  for (int64_t v0 = 0; open && v0 < end; v0 += 32) {
+    uint32_t keys = not_finite32<FMT, DP>(p, k, (uint32_t)v0, lane);
+    const uint32_t mask = seen(v0);
 #pragma unroll 1
-      for (; keys && open; keys &= keys - 1) {
-        const int j = __ffs(keys) - 1;
-        int64_t at, so;
-        key_at(p, k, (uint32_t)v0 + j, at, so);
-        const uint32_t its = 8 * lane < p.D ? not_finite8<FMT>(p, at, so, lane) : 0, sees = __ballot_sync(0xFFFFFFFFu, mask >> j & 1);
-        uint32_t left = 0;
+    for (; keys && open; keys &= keys - 1) {
+      const int j = __ffs(keys) - 1;
+      int64_t at, so;
+      key_at(p, k, (uint32_t)v0 + j, at, so);
+      const uint32_t its = 8 * lane < p.D ? not_finite8<FMT>(p, at, so, lane) : 0, sees = __ballot_sync(0xFFFFFFFFu, mask >> j & 1);
+      uint32_t left = 0;
 #pragma unroll 1
-        for (int g = 0; g < 8; ++g) {
-          // (a row's bit to each bit of its byte; a byte's any bit to a row's bit)
-          const uint32_t bytes = dims[g] & ~(its * 0x01010101u & ((sees >> (4 * g) & 15) * 0x00204081u & 0x01010101u) * 255u);
-          dims[g] = bytes;
+      for (int g = 0; g < 8; ++g) {
+        // (a row's bit to each bit of its byte; a byte's any bit to a row's bit)
+        const uint32_t bytes = ((sees >> (4 * g) & 15) * 0x00204081u & 0x01010101u) * 255u;
+        const uint32_t nan = dims[0][g] & ~((its & 255) * 0x01010101u & bytes), inf = dims[1][g] & ~((its >> 8) * 0x01010101u & bytes);
+        dims[0][g] = nan;
+        dims[1][g] = inf;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) left |= (uint32_t)((bytes >> (8 * i) & 255) != 0) << (4 * g + i);
-        }
-        open &= __reduce_or_sync(0xFFFFFFFFu, left);
+        for (int i = 0; i < 4; ++i) left |= (uint32_t)(((nan | inf) >> (8 * i) & 255) != 0) << (4 * g + i);
       }
+      open &= __reduce_or_sync(0xFFFFFFFFu, left);
     }
   }
 #pragma unroll 1
-  for (uint32_t which = unseen | open; which;) {
+  for (uint32_t which = open; which;) {
     prefill_rows<FMT, DP>(p, k, x, which, lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) which &= which - 1;

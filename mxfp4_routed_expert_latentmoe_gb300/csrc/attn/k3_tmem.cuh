@@ -48,7 +48,7 @@ K3_DEVI bool mb_test(uint32_t bar, uint32_t parity) {
 }
 // Waits for the phase of the given parity; false if the block has given up, or after MB_LOOKS looks of
 // some 7800 clocks each, about a minute (then it has).  The longest that a block's warps wait for one
-// another is for rows that are formed again: 1 to 5 s for a tile over half a million tokens (64 to 256 dims).
+// another is for rows that are formed again: 0.5 to 3 s for a tile over half a million tokens (64 to 256 dims).
 constexpr uint32_t MB_LOOKS = 1u << 24;
 #ifndef K3_MB_LOOKS  // (a test lets chosen waits run out at once)
 #define K3_MB_LOOKS MB_LOOKS

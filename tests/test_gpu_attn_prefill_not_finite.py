@@ -112,9 +112,27 @@ def test_sums_that_leave_fp32_on_the_way(attn, fmt, spoilt):
     _check(_rising(attn, fmt, spoilt), 40)
 
 
+def test_an_infinity_is_no_nan_for_a_hidden_value(attn):
+    """Infinities that a token sees stay infinities, whatever keys it does not see hold in the same dims."""
+    for window in (0, 90):
+        c = Call(attn, [(200, 200)], 16, "bf16", 8, 1, 128, window)
+        pg, at = (c.s.slots[0] // 16).long(), (c.s.slots[0] % 16).long()
+        c.s.cache.v[pg[100], 0, at[100], 5] = math.inf
+        c.s.cache.v[pg[100], 0, at[100], 6] = -math.inf
+        c.s.cache.v[pg[150], 0, at[150], 5:8] = math.nan
+        c.s.cache.v[pg[199], 0, at[199], 5] = -math.inf
+        c.run()
+        _check(c, 200)
+        out = c.out.float().cpu()
+        assert (out[100:150, :, 5] == math.inf).all() and (out[100:150, :, 6] == -math.inf).all()
+        assert torch.isnan(out[150:199 if window == 0 else 190, :, 5:8]).all() and torch.isfinite(out[:100]).all()
+
+
+@pytest.mark.parametrize("where", [[0], range(4000)], ids=["first", "all"])
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_what_a_value_costs(attn, fmt):
-    """A NaN that all tokens see costs them a look (hundreds of times the call, were they formed again one by one)."""
+def test_what_a_value_costs(attn, fmt, where):
+    """NaN that all tokens see, in the first token or all, cost them a look (hundreds of times the call, were they
+    formed again one by one)."""
     c = Call(attn, [(4000, 4000)], 64, fmt, 32, 4, 128)
     ms = []
     for _ in range(2):
@@ -125,8 +143,11 @@ def test_what_a_value_costs(attn, fmt):
         end.record()
         end.synchronize()
         ms.append(start.elapsed_time(end))
-        for head in range(4):
-            _spoil(c, 0, 0, head, "all")
+        pg, at = (c.s.slots[0][list(where)] // 64).long(), (c.s.slots[0][list(where)] % 64).long()
+        if fmt == "bf16":
+            c.s.cache.v[pg, :, at] = math.nan
+        else:
+            c.s.cache.v_scale[pg, :, at] = math.nan if fmt == "e4m3" else 255
     assert not torch.isfinite(c.out).any() and torch.isfinite(c.lse).all()
     assert ms[1] <= 10 * ms[0], ms
 
