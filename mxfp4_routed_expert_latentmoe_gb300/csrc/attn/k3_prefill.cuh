@@ -28,7 +28,7 @@
 // weights 1500, to the last 2500 (maximum 700, then 32 logits at a time; the two halves' warps share the
 // issue slots, neither pipe is full), then its turn at the tensor core; and a tile's start, some 14000 clocks
 // (queries once the last products are through, the sums' way out; pre_start).  Codes: the copying warps (a chunk of
-// 1500 behind 30001 tokens, MXFP4: 1.92 ms, 41% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses
+// 1500 behind 30001 tokens, MXFP4: 1.91 ms, 42% of the rate; of 6440 clocks 2500 are conversion and 2100 addresses
 // and copies; E4M3 in a window of 1000: 0.56 ms), and for few rows (drafts: 200 us) the chain of one half.
 // Ten copying warps of 64 registers instead of six of 96 were 6 to 20% slower, rows of codes as bulk
 // copies of a row each (some 85 clocks to issue one) 35%.
